@@ -11,7 +11,10 @@
  *      the W4A16 product Y = (X / s*) Dequant(Wq);
  *   4. variants of the search: over a caller's scale table (other statistics and
  *      scale families), over clip ratios, jointly over projections that share X, and
- *      the power-of-two per-group greedy of [P4].
+ *      the power-of-two per-group greedy of [P4];
+ *   5. the microscaled (MX) operators: 4-bit floating-point weights with a power-of-two scale
+ *      per 32 channels, activations quantized to 8 or 4 bits in the same way (on their own,
+ *      behind a gate, or as the output of a root-mean-square norm), and their product.
  *
  * Sources (page title -- section), for the definitions cited below:
  *   [P1] "AWQ (Activation-aware Weight Quantization)" (compassingai.com)
@@ -48,7 +51,7 @@ extern "C" {
 #define AWQ_OK 0
 #define AWQ_ERR_INVALID_ARG (-1) /* null/misaligned pointer, non-positive size, K % group_size != 0, ... */
 #define AWQ_ERR_UNSUPPORTED (-2) /* w_bit != 4, group_size not in {32, 64, 128}, n_grid outside [2, 64],
-                                    clip_ratio outside [0, 1] */
+                                    clip_ratio outside [0, 1], MX bits not 8 or 4 */
 #define AWQ_ERR_WORKSPACE (-3)   /* workspace smaller than the matching *_workspace_size() */
 #define AWQ_ERR_HIP (-4)         /* a HIP call failed; awq_last_hip_error() holds its code */
 #define AWQ_ERR_SCRATCH (-5)     /* awq_w4a16_gemm_noalloc: the call needs more than its fixed scratch */
@@ -287,6 +290,90 @@ size_t awq_w4a16_gemm_static_scratch_bytes(void);
 int awq_w4a16_gemm_noalloc(const void* X_bf16, int64_t M, const float* s, const uint32_t* codes,
                            const float* scales, const uint8_t* zeros, int64_t K, int64_t N,
                            int32_t group_size, void* Y_bf16, void* stream);
+
+/* ---------------------------------------------------------------- microscaled (MX) operators
+ * A block is 32 consecutive input channels of one row of activations or of one output column of
+ * weights.  It holds one scale byte E, which stands for 2^(E - 127), and 32 elements in
+ *   e4m3 (8 bits: sign, 4 exponent, 3 mantissa bits; largest 448), for activations, or
+ *   e2m1 (4 bits: sign, 2 exponent, 1 mantissa bit: 0, .5, 1, 1.5, 2, 3, 4, 6), for both.
+ * Quantizing 32 float32 numbers p:
+ *   E = max(biased exponent of max|p| - e_max, 0), e_max = 8 (e4m3) or 2 (e2m1): the largest
+ *       power-of-two scale under which the largest element stays in the format's top binade;
+ *   element = p / 2^(E - 127) rounded to nearest even, saturated at the largest magnitude.
+ * A block whose numbers are all zero has E = 0.  A block that holds an infinity or a NaN has
+ * E = 255 and zero elements; every value it stands for is NaN, and so is every product with it.
+ * The value of an element is element * 2^(E - 127).
+ *
+ * Layouts (Kb = K/32 rounded up to a multiple of 4; Nt = ceil(N/64)):
+ *   activations  codes: bits = 8: uint8 [M, K]; bits = 4: uint8 [M, K/2], channel 2i in the low half
+ *                of byte i.  scales: uint8 [M, K/32].
+ *   weights      codes: uint8 [Nt, Kb, 64, 16]: the 16 bytes of (t, b, c) are block b (channels
+ *                32b .. 32b+31, channel 2i in the low half of byte i) of output column 64t + c.
+ *                scales: uint8 [Nt, Kb, 64]: byte 4i + j of (t, b) belongs to column 64t + 16j + i.
+ *                Blocks past K and columns past N hold zeros (codes and scales), written by
+ *                awq_mx_pack and relied on by awq_mx_gemm.
+ * K must be a multiple of 32 (of 8 for a norm without codes).  bits is 8 or 4 (AWQ_ERR_UNSUPPORTED
+ * otherwise).  s, where it may be NULL, is float32 [K], positive and finite: the input scales of an
+ * AWQ search; weights are multiplied by it and activations divided.  Outputs must not overlap
+ * inputs or each other (AWQ_ERR_INVALID_ARG) unless a paragraph below says so.  Codes, weights'
+ * scales, s and bf16 activations are 16-byte aligned; W needs only its own type's alignment.
+ */
+/* Bytes of packed weights and of their scales (0 for bad sizes): K a multiple of 32, at most
+ * 65535 * 128; K * N at most 2^36. */
+size_t awq_mx_codes_bytes(int64_t K, int64_t N);
+size_t awq_mx_scales_bytes(int64_t K, int64_t N);
+
+/* Weights into MX blocks: p = s_k * w_kn (one float32 product), e2m1 blocks along K.
+ *   W  bf16 [K, N], any N;  s  float32 [K] or NULL (1).
+ */
+int awq_mx_pack(const void* W_bf16, int64_t K, int64_t N, const float* s, uint8_t* codes, uint8_t* scales,
+                void* stream);
+/* And back: w_kn = element * 2^(E - 127) / s_k, rounded to bf16 once (exact for s = NULL), for
+ * scoring a packing or feeding a bf16 product.
+ */
+int awq_mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t K, int64_t N, const float* s, void* W_bf16,
+                  void* stream);
+
+/* Activations into MX blocks: p = x / s_k, or with a gate p = x * g / (1 + e^-g) / s_k (the input of a
+ * gated MLP's last layer: x = up, g = gate), evaluated in float32.
+ *   X, gate  bf16 [M, K] (gate may be NULL);  s  float32 [K] or NULL (1).
+ */
+int awq_mx_quantize(const void* X_bf16, const void* gate_bf16, int64_t M, int64_t K, const float* s, int32_t bits,
+                    uint8_t* codes, uint8_t* scales, void* stream);
+
+/* Root-mean-square norm behind a residual addition, with a quantized output:
+ *   h = x + r,   y = h * weight / sqrt(mean_k h^2 + eps),
+ * h in float32 (r = 0 when residual is NULL), the squares summed in float64.
+ *   X, residual  bf16 [M, K] (residual may be NULL);  weight  bf16 [K];  eps in (0, 1].
+ *   residual_out bf16 [M, K] or NULL (NULL when residual is): h rounded to bf16.
+ *   Y            bf16 [M, K] or NULL: y rounded to bf16.
+ *   codes, scales  y / s_k in MX blocks of `bits` bits, from the float32 y; both or neither.  s
+ *                (float32 [K] or NULL) belongs to them alone: Y is not divided.  bits is not read
+ *                when codes is NULL.
+ * At least one of Y and codes must be given.  residual_out and Y may each be the same address as X
+ * or residual (in place), but not the same buffer as each other.
+ */
+int awq_rms_norm(const void* X_bf16, const void* residual_bf16, const void* weight_bf16, int64_t M, int64_t K,
+                 float eps, void* residual_out, void* Y_bf16, const float* s, int32_t bits, uint8_t* codes,
+                 uint8_t* scales, void* stream);
+
+/* The product of MX activations and MX weights:
+ *   Y[m, n] = sum_k xval_mk * wval_kn, float32 accumulation on the scaled matrix cores, bf16 out.
+ * With 8-bit activations the matrix core adds the products of eight consecutive channels with 13
+ * binary places below the largest (about 1e-4 of a typical sum, under bf16's rounding); with 4-bit
+ * ones a block's sum is exact.
+ *   xcodes, xscales  activations of `bits` bits;  codes, scales  weights as awq_mx_pack writes them;
+ *   Y  bf16 [M, N], N % 8 == 0, M at most 65535 * 16.
+ *   workspace >= awq_mx_gemm_workspace_size(M, K, N, bits) bytes (the size may be 0), 256-byte
+ *   aligned.  Its first 64 KiB hold arrival counters under the rules of awq_w4a16_gemm's: zero before
+ *   the first call, left zero by every completed call, so that one workspace serves any sequence of
+ *   calls of either product.  Calls that share a workspace must be ordered, replays of captured
+ *   graphs included.
+ */
+size_t awq_mx_gemm_workspace_size(int64_t M, int64_t K, int64_t N, int32_t bits);
+int awq_mx_gemm(const uint8_t* xcodes, const uint8_t* xscales, int32_t bits, int64_t M, const uint8_t* codes,
+                const uint8_t* scales, int64_t K, int64_t N, void* Y_bf16, void* workspace, size_t ws_bytes,
+                void* stream);
 
 /* ---------------------------------------------------------------- status helpers */
 const char* awq_status_string(int status);

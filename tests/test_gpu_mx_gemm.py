@@ -1,0 +1,128 @@
+"""The MX product on the GPU against float64 products of the values its operands stand for, within the
+bound that float32 accumulation and one bf16 rounding leave."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mx_oracle as O
+from tests.mx_util import A, DEV, check_product, product, random_acts, random_weights
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [(1, 32, 8), (1, 128, 64), (1, 8192, 1024), (2, 96, 72), (3, 160, 200), (7, 4096, 520), (13, 2080, 136),
+          (16, 512, 4096), (17, 1024, 64), (31, 352, 328), (33, 512, 512), (64, 224, 1032), (65, 1152, 256),
+          (127, 128, 136), (129, 1056, 264), (200, 608, 520), (256, 512, 512), (257, 2048, 776), (300, 4096, 1024),
+          (513, 96, 264), (1030, 736, 1288)]
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("M,K,N", SHAPES)
+def test_product(M, K, N, bits):
+    xc, xs, x = random_acts(M, K, bits, M + K + N)
+    wc, wsc, w = random_weights(K, N, M + K + N + 1)
+    check_product(product(xc, xs, wc, wsc, M, K, N), x, w, bits, (M, K, N, bits))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 512), (5, 1024, 192), (40, 1120, 256), (300, 512, 520), (600, 1024, 776)])
+def test_integers_are_exact(M, K, N, bits):
+    """Elements that are small integers under scales of 1: every partial sum is a float32 integer, so the
+    product is the bf16 rounding of the exact one, whatever the order of its sums."""
+    rng = np.random.default_rng(M)
+    x, w = rng.integers(-3, 4, (M, K)).astype(np.float64), rng.integers(-3, 4, (K, N)).astype(np.float64)
+    E = np.full((M, K // 32), 127, np.uint8)
+    c = O.round_codes(x, bits)
+    t = torch.from_numpy(c if bits == 8 else O.pair(c))
+    xc = (t.view(torch.float8_e4m3fn) if bits == 8 else t).to(DEV)
+    wc, wsc = (torch.from_numpy(a).to(DEV) for a in O.weights_layout(O.round_codes(w, 4), np.full((K // 32, N), 127, np.uint8)))
+    Y = product(xc, torch.from_numpy(E).to(DEV), wc, wsc, M, K, N)
+    assert torch.equal(Y.cpu(), torch.from_numpy((x @ w).astype(np.float32)).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("M,K,N", [(1, 256, 128), (6, 1024, 72), (100, 384, 264), (400, 512, 520)])
+def test_one_element_at_a_time(M, K, N, bits):
+    """Each row of x has one nonzero element, with its block's own scale: row m of Y is one row of W times a
+    power of two, exactly.  A block or a scale taken from another place shows."""
+    rng = np.random.default_rng(K)
+    k = rng.integers(0, K, M)
+    c = np.zeros((M, K), np.uint8)
+    c[np.arange(M), k] = O.round_codes(np.ones(M), bits)
+    E = rng.integers(120, 134, (M, K // 32)).astype(np.uint8)
+    t = torch.from_numpy(c if bits == 8 else O.pair(c))
+    xc = (t.view(torch.float8_e4m3fn) if bits == 8 else t).to(DEV)
+    wc, wsc, w = random_weights(K, N, K)
+    Y = product(xc, torch.from_numpy(E).to(DEV), wc, wsc, M, K, N)
+    ref = w[k] * 2.0 ** (E[np.arange(M), k // 32] - 127.0)[:, None]
+    assert torch.equal(Y.cpu().float(), torch.from_numpy(ref.astype(np.float32)))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("M,K,N", [(1, 1024, 128), (20, 256, 64), (300, 640, 264)])
+def test_nan_blocks_and_extreme_scales(M, K, N, bits):
+    xc, xs, _ = random_acts(M, K, bits, 1)
+    wc, wsc, _ = random_weights(K, N, 2)
+    E = xs.cpu().numpy().copy()
+    F = wsc.cpu().numpy().copy()
+    if M > 2:
+        E[1, 0], E[2, -1] = 0, 0                 # the smallest scale
+        E[M // 2, K // 64] = 255                 # a row of NaN
+    F[0, 1, O.scale_position(5)] = 255           # a column of NaN
+    F[0, 0, O.scale_position(9)] = 0
+    F[0, 2, O.scale_position(9)] = 200
+    c = xc.view(torch.uint8).cpu().numpy()
+    x = O.values(c if bits == 8 else O.unpair(c), E, bits)
+    w = O.weights_values(wc.cpu().numpy(), F, K, N)
+    Y = product(xc, torch.from_numpy(E).to(DEV), wc, torch.from_numpy(F).to(DEV), M, K, N)
+    check_product(Y, x, w, bits, (M, K, N, bits))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("M,K,N", [(1, 1024, 136), (9, 96, 72), (70, 128, 200), (300, 512, 264)])
+def test_nothing_else_is_written_or_read(M, K, N, bits):
+    """Y lies between guard rows; the activations are followed by NaN codes and NaN scales, which no row
+    may see (K = 96 ends inside a 128-channel chunk)."""
+    xc, xs, x = random_acts(M, K, bits, 4)
+    wc, wsc, w = random_weights(K, N, 5)
+    nb = xc.view(torch.uint8).numel()
+    big = torch.full((nb + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
+    big[:nb] = xc.view(torch.uint8).reshape(-1)
+    bs = torch.full((xs.numel() + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
+    bs[:xs.numel()] = xs.reshape(-1)
+    xc = big[:nb].view(M, -1)
+    xc = xc.view(torch.float8_e4m3fn) if bits == 8 else xc
+    Yg = torch.full((M * N + 2048,), 3.0, dtype=torch.bfloat16, device=DEV)
+    Y = Yg[1024:1024 + M * N].view(M, N)
+    ws = A.workspace(A.awq_mx_gemm_workspace_size(M, K, N, bits), DEV)
+    A.awq_mx_gemm(xc, bs[:xs.numel()].view(M, -1), wc, wsc, Y, ws)
+    torch.cuda.synchronize()
+    assert (Yg[:1024] == 3).all() and (Yg[1024 + M * N:] == 3).all()
+    check_product(Y, x, w, bits, (M, K, N, bits))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_repeated_calls_agree_on_one_workspace(bits):
+    """One workspace for every shape in turn, three rounds: equal bits each time, counters left at zero."""
+    shapes = [(1, 8192, 1024), (13, 4096, 520), (64, 2048, 256), (300, 1024, 776), (1, 1024, 64), (129, 4096, 264)]
+    ops = [(random_acts(M, K, bits, i)[:2], random_weights(K, N, i)[:2]) for i, (M, K, N) in enumerate(shapes)]
+    ws = A.workspace(max(A.awq_mx_gemm_workspace_size(*s, bits) for s in shapes), DEV)
+    first = None
+    for _ in range(3):
+        ys = [product(*a, *b, *s, ws=ws) for s, (a, b) in zip(shapes, ops)]
+        assert not ws[:65536].any()
+        if first is None:
+            first = ys
+        assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(first, ys))
+
+
+def test_rows_do_not_depend_on_their_neighbours():
+    """A row's result is the same bits alone in a batch of the same plan, wherever it stands."""
+    M, K, N = 300, 1024, 264
+    for bits in (8, 4):
+        xc, xs, _ = random_acts(M, K, bits, 1)
+        wc, wsc, _ = random_weights(K, N, 2)
+        Y = product(xc, xs, wc, wsc, M, K, N)
+        p = torch.randperm(M, generator=torch.Generator().manual_seed(0)).to(DEV)
+        xp = xc.view(torch.uint8)[p].contiguous()
+        Z = product(xp.view(xc.dtype), xs[p].contiguous(), wc, wsc, M, K, N)
+        assert torch.equal(Y[p].view(torch.int16), Z.view(torch.int16))

@@ -8,6 +8,7 @@ fails loudly -- there is no fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -72,6 +73,14 @@ _SIGNATURES = {
     "awq_w4a16_gemm": (ctypes.c_int, [_P, _I64, _P, _P, _P, _P, _I64, _I64, _I32, _P, _P, _SZ, _P]),
     "awq_w4a16_gemm_static_scratch_bytes": (_SZ, []),
     "awq_w4a16_gemm_noalloc": (ctypes.c_int, [_P, _I64, _P, _P, _P, _P, _I64, _I64, _I32, _P, _P]),
+    "awq_mx_codes_bytes": (_SZ, [_I64, _I64]),
+    "awq_mx_scales_bytes": (_SZ, [_I64, _I64]),
+    "awq_mx_pack": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P]),
+    "awq_mx_unpack": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _P]),
+    "awq_mx_quantize": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _I32, _P, _P, _P]),
+    "awq_rms_norm": (ctypes.c_int, [_P, _P, _P, _I64, _I64, ctypes.c_float, _P, _P, _P, _I32, _P, _P, _P]),
+    "awq_mx_gemm_workspace_size": (_SZ, [_I64, _I64, _I64, _I32]),
+    "awq_mx_gemm": (ctypes.c_int, [_P, _P, _I32, _I64, _P, _P, _I64, _I64, _P, _P, _SZ, _P]),
     "awq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "awq_last_hip_error": (ctypes.c_int, []),
     "awq_version": (ctypes.c_char_p, []),
@@ -452,3 +461,216 @@ def run_greedy(X: torch.Tensor, W: torch.Tensor, cfg: awq_qconfig, n_cand: int =
     awq_pack(W, s_best, cfg, codes, scales, zeros, stream)
     return {"mean_abs": mean_abs, "s_best": s_best, "err_rtn": err_rtn, "err": err,
             "q": Quantized(codes, scales, zeros, s_best, g)}
+
+
+# ------------------------------------------------------------------ microscaled (MX) operators
+_SCALE_DTYPES = (torch.uint8, torch.float8_e8m0fnu)   # a scale byte E stands for 2^(E - 127)
+_MX_BITS = {torch.float8_e4m3fn: 8, torch.uint8: 4}    # activations: e4m3 [.., K], or e2m1 pairs [.., K/2]
+
+
+def _mx_device(fn: str, *tensors: Optional[torch.Tensor]) -> None:
+    """Every tensor contiguous on one device, and that device the current one: the kernels are
+    launched on the current device's stream."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("libawq takes device tensors")
+        if not t.is_contiguous():
+            raise ValueError("libawq takes contiguous tensors")
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{fn}: tensors on different devices")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{fn}: tensors are on device {dev}, which is not the current device")
+
+
+def _mx_ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _mx_rows(fn: str, K: int, what: int = 32) -> None:
+    if K <= 0 or K % what:
+        raise ValueError(f"{fn}: K = {K} must be a positive multiple of {what}")
+
+
+def _mx_weights(fn: str, codes: torch.Tensor, scales: torch.Tensor, K: int, N: int) -> None:
+    kb, nt = -(-K // 128) * 4, -(-N // 64)
+    _expect(fn, "codes", codes, torch.uint8, (nt, kb, 64, 16))
+    _expect(fn, "scales", scales, _SCALE_DTYPES, (nt, kb, 64))
+
+
+def _mx_acts(fn: str, codes: torch.Tensor, scales: torch.Tensor, M: int, K: int) -> int:
+    bits = _MX_BITS.get(codes.dtype)
+    if bits is None:
+        raise ValueError(f"{fn}: activation codes must be torch.float8_e4m3fn (8 bits) or torch.uint8 (4 bits), "
+                         f"got {codes.dtype}")
+    _expect(fn, "codes", codes, codes.dtype, (M, K if bits == 8 else K // 2))
+    _expect(fn, "scales", scales, _SCALE_DTYPES, (M, K // 32))
+    return bits
+
+
+def awq_mx_codes_bytes(K: int, N: int) -> int:
+    return int(_lib.awq_mx_codes_bytes(K, N))
+
+
+def awq_mx_scales_bytes(K: int, N: int) -> int:
+    return int(_lib.awq_mx_scales_bytes(K, N))
+
+
+def awq_mx_pack(W: torch.Tensor, s: Optional[torch.Tensor], codes: torch.Tensor, scales: torch.Tensor,
+                stream=None) -> None:
+    fn = "awq_mx_pack"
+    K, N = _matrix(fn, "W", W)
+    _mx_rows(fn, K)
+    _expect(fn, "s", s, torch.float32, (K,), optional=True)
+    _mx_weights(fn, codes, scales, K, N)
+    _mx_device(fn, W, s, codes, scales)
+    _check(fn, _lib.awq_mx_pack(_mx_ptr(W), K, N, _mx_ptr(s), _mx_ptr(codes), _mx_ptr(scales), _stream(stream)))
+
+
+def awq_mx_unpack(codes: torch.Tensor, scales: torch.Tensor, s: Optional[torch.Tensor], W: torch.Tensor,
+                  stream=None) -> None:
+    fn = "awq_mx_unpack"
+    K, N = _matrix(fn, "W", W)
+    _mx_rows(fn, K)
+    _expect(fn, "s", s, torch.float32, (K,), optional=True)
+    _mx_weights(fn, codes, scales, K, N)
+    _mx_device(fn, codes, scales, s, W)
+    _check(fn, _lib.awq_mx_unpack(_mx_ptr(codes), _mx_ptr(scales), K, N, _mx_ptr(s), _mx_ptr(W), _stream(stream)))
+
+
+def awq_mx_quantize(X: torch.Tensor, gate: Optional[torch.Tensor], s: Optional[torch.Tensor], codes: torch.Tensor,
+                    scales: torch.Tensor, stream=None) -> None:
+    fn = "awq_mx_quantize"
+    M, K = _matrix(fn, "X", X)
+    _mx_rows(fn, K)
+    _expect(fn, "gate", gate, torch.bfloat16, (M, K), optional=True)
+    _expect(fn, "s", s, torch.float32, (K,), optional=True)
+    bits = _mx_acts(fn, codes, scales, M, K)
+    _mx_device(fn, X, gate, s, codes, scales)
+    _check(fn, _lib.awq_mx_quantize(_mx_ptr(X), _mx_ptr(gate), M, K, _mx_ptr(s), bits, _mx_ptr(codes),
+                                    _mx_ptr(scales), _stream(stream)))
+
+
+def awq_rms_norm(X: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor, eps: float,
+                 residual_out: Optional[torch.Tensor], Y: Optional[torch.Tensor], s: Optional[torch.Tensor] = None,
+                 codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None) -> None:
+    fn = "awq_rms_norm"
+    M, K = _matrix(fn, "X", X)
+    _mx_rows(fn, K, 8 if codes is None else 32)
+    _expect(fn, "residual", residual, torch.bfloat16, (M, K), optional=True)
+    _expect(fn, "weight", weight, torch.bfloat16, (K,))
+    _expect(fn, "residual_out", residual_out, torch.bfloat16, (M, K), optional=True)
+    _expect(fn, "Y", Y, torch.bfloat16, (M, K), optional=True)
+    _expect(fn, "s", s, torch.float32, (K,), optional=True)
+    if (codes is None) != (scales is None):
+        raise ValueError(f"{fn}: codes and scales are given together or not at all")
+    bits = 8 if codes is None else _mx_acts(fn, codes, scales, M, K)
+    _mx_device(fn, X, residual, weight, residual_out, Y, s, codes, scales)
+    _check(fn, _lib.awq_rms_norm(_mx_ptr(X), _mx_ptr(residual), _mx_ptr(weight), M, K, float(eps),
+                                 _mx_ptr(residual_out), _mx_ptr(Y), _mx_ptr(s), bits, _mx_ptr(codes),
+                                 _mx_ptr(scales), _stream(stream)))
+
+
+def awq_mx_gemm_workspace_size(M: int, K: int, N: int, bits: int) -> int:
+    return int(_lib.awq_mx_gemm_workspace_size(M, K, N, bits))
+
+
+def awq_mx_gemm(xcodes: torch.Tensor, xscales: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                Y: torch.Tensor, ws: Optional[torch.Tensor], stream=None) -> None:
+    fn = "awq_mx_gemm"
+    M, N = _matrix(fn, "Y", Y)
+    K = 32 * _matrix(fn, "xscales", xscales, xscales.dtype if xscales.dtype in _SCALE_DTYPES else torch.uint8)[1]
+    bits = _mx_acts(fn, xcodes, xscales, M, K)
+    _mx_weights(fn, codes, scales, K, N)
+    _mx_device(fn, xcodes, xscales, codes, scales, Y, ws)
+    _check(fn, _lib.awq_mx_gemm(_mx_ptr(xcodes), _mx_ptr(xscales), bits, M, _mx_ptr(codes), _mx_ptr(scales), K, N,
+                                _mx_ptr(Y), _mx_ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+@contextlib.contextmanager
+def _allocating_on(stream):
+    """What the helpers below allocate (and zero-fill) belongs to the stream that they launch on."""
+    if stream is None:
+        yield
+        return
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        yield
+
+
+class MxWeights:
+    """Device buffers of one layer's MX weights: codes uint8 [ceil(N/64), Kb, 64, 16], scales
+    [ceil(N/64), Kb, 64], the input scales s [K] (or None) and the layer's K and N."""
+
+    def __init__(self, codes, scales, s, K, N):
+        self.codes, self.scales, self.s, self.K, self.N = codes, scales, s, K, N
+
+
+class MxActs:
+    """Device buffers of MX activations: codes float8_e4m3fn [M, K] or uint8 [M, K/2], scales [M, K/32]."""
+
+    def __init__(self, codes, scales):
+        self.codes, self.scales = codes, scales
+
+
+def mx_pack(W: torch.Tensor, s: Optional[torch.Tensor] = None, stream=None) -> MxWeights:
+    """Allocate and pack one layer's weights (s: the s* of a search over the layer, or None)."""
+    K, N = W.shape
+    kb, nt = -(-K // 128) * 4, -(-N // 64)
+    with _allocating_on(stream):
+        codes = torch.empty((nt, kb, 64, 16), dtype=torch.uint8, device=W.device)
+        scales = torch.empty((nt, kb, 64), dtype=torch.float8_e8m0fnu, device=W.device)
+    awq_mx_pack(W, s, codes, scales, stream)
+    return MxWeights(codes, scales, s, K, N)
+
+
+def mx_unpack(q: MxWeights, stream=None) -> torch.Tensor:
+    """The bf16 weights that q stands for, divided by its input scales."""
+    with _allocating_on(stream):
+        W = torch.empty((q.K, q.N), dtype=torch.bfloat16, device=q.codes.device)
+    awq_mx_unpack(q.codes, q.scales, q.s, W, stream)
+    return W
+
+
+def _mx_acts_like(X: torch.Tensor, bits: int, stream) -> MxActs:
+    M, K = X.shape
+    if bits not in (8, 4):
+        raise ValueError(f"activations take 8 or 4 bits, got {bits}")
+    with _allocating_on(stream):
+        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device) if bits == 8 else \
+            torch.empty((M, K // 2), dtype=torch.uint8, device=X.device)
+        return MxActs(codes, torch.empty((M, K // 32), dtype=torch.float8_e8m0fnu, device=X.device))
+
+
+def mx_quantize(X: torch.Tensor, s: Optional[torch.Tensor] = None, bits: int = 8,
+                gate: Optional[torch.Tensor] = None, stream=None) -> MxActs:
+    """X (or silu(gate) * X) divided by s, in MX blocks of `bits` bits."""
+    a = _mx_acts_like(X, bits, stream)
+    awq_mx_quantize(X, gate, s, a.codes, a.scales, stream)
+    return a
+
+
+def rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: Optional[torch.Tensor] = None,
+             s: Optional[torch.Tensor] = None, bits: int = 8, stream=None):
+    """(MX activations of the norm divided by s, the updated residual or None)."""
+    a = _mx_acts_like(X, bits, stream)
+    with _allocating_on(stream):
+        out = None if residual is None else torch.empty_like(X)
+    awq_rms_norm(X, residual, weight, eps, out, None, s, a.codes, a.scales, stream)
+    return a, out
+
+
+def mx_gemm(a: MxActs, q: MxWeights, stream=None) -> torch.Tensor:
+    """The product of MX activations (divided by q.s when they were quantized) and MX weights."""
+    M = a.codes.shape[0]
+    bits = _MX_BITS.get(a.codes.dtype, 0)
+    with _allocating_on(stream):
+        Y = torch.empty((M, q.N), dtype=torch.bfloat16, device=a.codes.device)
+        ws = workspace(awq_mx_gemm_workspace_size(M, q.K, q.N, bits), a.codes.device)
+    awq_mx_gemm(a.codes, a.scales, q.codes, q.scales, Y, ws, stream)
+    return Y

@@ -36,6 +36,10 @@ int check_cfg(const awq_qconfig* cfg, int64_t K) {
 
 }  // namespace
 
+namespace awq {
+int record_hip(hipError_t e) { return hip_status(e); }   // for the entry points in other sources
+}  // namespace awq
+
 extern "C" {
 
 size_t awq_act_stats_workspace_size(int64_t T, int64_t K) {

@@ -1,0 +1,115 @@
+// Microscaled (MX) operators: formats shared by their kernels, and the host-side launchers
+// (internal; the public ABI is include/awq.h).
+//
+// A block is 32 consecutive input channels.  Its scale is 2^(E - 127), E one byte, and its elements
+// are p / 2^(E - 127) in e4m3 (8 bits) or e2m1 (4 bits), rounded to nearest even and saturated:
+//   E = max(biased exponent of max|p| - e_max, 0),  e_max = 8 (e4m3) or 2 (e2m1),
+// so that the largest element lands in the format's top binade.  E = 255 marks a block that holds
+// an infinity or a NaN (its elements are stored as zeros; every value it stands for is NaN).
+#pragma once
+#include "awq_device.h"
+
+namespace awq {
+
+constexpr int kMxBlock = 32;     // channels per scale
+constexpr int kMxTile = 64;      // output columns per tile of packed weights
+constexpr int kMxChunk = 128;    // channels per scaled matrix-core product: packed weights are padded to it
+
+inline int64_t mx_kb(int64_t K) { return (K + kMxChunk - 1) / kMxChunk * (kMxChunk / kMxBlock); }   // blocks, padded
+inline int64_t mx_nt(int64_t N) { return (N + kMxTile - 1) / kMxTile; }
+inline size_t mx_codes_bytes(int64_t K, int64_t N) { return (size_t)mx_nt(N) * mx_kb(K) * kMxTile * 16; }
+inline size_t mx_scales_bytes(int64_t K, int64_t N) { return (size_t)mx_nt(N) * mx_kb(K) * kMxTile; }
+
+// ---- formats on the device
+// Scale byte of a block whose largest |p| has the float32 bits `top` (NaN > infinity > finite as
+// unsigned integers, so an integer maximum of |p| finds them).
+template <int BITS>
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
+    const int e = (int)(top >> 23);
+    return e == 255 ? 255u : (uint32_t)max(e - (BITS == 8 ? 8 : 2), 0);
+}
+// 2^(127 - E), the factor from values to stored elements; E <= 252 for a finite block.
+__device__ __forceinline__ float mx_to_stored(uint32_t E) { return __uint_as_float((254u - E) << 23); }
+// 2^(E - 127), the factor from stored elements to values (E = 0: the subnormal 2^-127; 255: NaN).
+__device__ __forceinline__ float mx_to_value(uint32_t E) {
+    return __uint_as_float(E == 0 ? 0x00400000u : E == 255 ? 0x7fc00000u : E << 23);
+}
+// Eight elements of a block -> packed codes.  e4m3: two words, saturated first (the conversion
+// itself turns what rounds beyond 448 into NaN).  e2m1: one word (the conversion saturates).
+__device__ __forceinline__ uint2 mx_e4m3x8(const float (&q)[8]) {
+    int w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        int r = 0;
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(__builtin_amdgcn_fmed3f(q[4 * h], -448.f, 448.f),
+                                            __builtin_amdgcn_fmed3f(q[4 * h + 1], -448.f, 448.f), r, false);
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(__builtin_amdgcn_fmed3f(q[4 * h + 2], -448.f, 448.f),
+                                            __builtin_amdgcn_fmed3f(q[4 * h + 3], -448.f, 448.f), r, true);
+        w[h] = r;
+    }
+    return uint2{(uint32_t)w[0], (uint32_t)w[1]};
+}
+__device__ __forceinline__ uint32_t mx_e2m1x8(const float (&q)[8]) {
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, q[0], q[1], 1.f, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, q[2], q[3], 1.f, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, q[4], q[5], 1.f, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, q[6], q[7], 1.f, 3);
+    return r;
+}
+// The largest |p| (as integer bits) of a block held by four consecutive lanes, eight elements each;
+// all four lanes must be active.
+__device__ __forceinline__ uint32_t mx_block_top(const float (&p)[8]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(p[i]) & 0x7fffffffu);
+    top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0xB1, 0xf, 0xf, true));   // lanes 1 0 3 2
+    return max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0x4E, 0xf, 0xf, true));  // lanes 2 3 0 1
+}
+// Quantizes the eight elements of octet `oct` of a row (block oct / 4) and stores codes and scale.
+template <int BITS>
+__device__ __forceinline__ void mx_store8(const float (&p)[8], uint8_t* codes_row, uint8_t* scales_row, int64_t oct) {
+    const uint32_t top = mx_block_top(p);
+    const uint32_t E = mx_scale_byte<BITS>(top);
+    const bool bad = E == 255;
+    const float f = mx_to_stored(bad ? 127 : E);
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = bad ? 0.f : p[i] * f;
+    if constexpr (BITS == 8) *(uint2*)(codes_row + oct * 8) = mx_e4m3x8(q);
+    else *(uint32_t*)(codes_row + oct * 4) = mx_e2m1x8(q);
+    if ((oct & 3) == 0) scales_row[oct >> 2] = (uint8_t)E;
+}
+// 16 bytes of bf16 -> eight floats
+__device__ __forceinline__ void bf16x8_to_f32(const u32x4& v, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(v[i]);
+        x[2 * i + 1] = bf16_hi(v[i]);
+    }
+}
+
+// ---- host side
+// Records a HIP error for awq_last_hip_error and returns the call's status (awq_api.hip).
+int record_hip(hipError_t e);
+
+hipError_t launch_mx_pack(const uint16_t* W, int64_t K, int64_t N, const float* s, uint8_t* codes, uint8_t* scales,
+                          hipStream_t st);
+hipError_t launch_mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t K, int64_t N, const float* s,
+                            uint16_t* W, hipStream_t st);
+hipError_t launch_mx_quantize(const uint16_t* X, const uint16_t* gate, int64_t M, int64_t K, const float* s, int bits,
+                              uint8_t* codes, uint8_t* scales, hipStream_t st);
+hipError_t launch_rms_norm(const uint16_t* X, const uint16_t* residual, const uint16_t* weight, int64_t M, int64_t K,
+                           float eps, uint16_t* residual_out, uint16_t* Y, const float* s, int bits, uint8_t* codes,
+                           uint8_t* scales, hipStream_t st);
+
+struct MxGemmPlan {
+    int64_t col_tiles, row_tiles;   // workgroup tiles
+    size_t ws_bytes;
+};
+MxGemmPlan plan_mx_gemm(int64_t M, int64_t K, int64_t N, int bits);
+hipError_t launch_mx_gemm(const uint8_t* xcodes, const uint8_t* xscales, int bits, int64_t M, const uint8_t* codes,
+                          const uint8_t* scales, int64_t K, int64_t N, uint16_t* Y, void* ws, const MxGemmPlan& p,
+                          hipStream_t st);
+
+}  // namespace awq
