@@ -104,6 +104,8 @@ hipError_t launch_rms_norm(const uint16_t* X, const uint16_t* residual, const ui
                            uint8_t* scales, hipStream_t st);
 
 struct MxGemmPlan {
+    int wm;                         // 0: the register kernel; else LDS tiles of 64 wm rows
+    int nz;                         // slices of K
     int64_t col_tiles, row_tiles;   // workgroup tiles
     size_t ws_bytes;
 };
