@@ -363,7 +363,7 @@ int awq_rms_norm(const void* X_bf16, const void* residual_bf16, const void* weig
  * binary places below the largest (about 1e-4 of a typical sum, under bf16's rounding); with 4-bit
  * ones a block's sum is exact.
  *   xcodes, xscales  activations of `bits` bits;  codes, scales  weights as awq_mx_pack writes them;
- *   Y  bf16 [M, N], N % 8 == 0, M at most 65535 * 16.
+ *   Y  bf16 [M, N], N % 8 == 0, N at most 4194304, M at most 65535 * 16.
  *   workspace >= awq_mx_gemm_workspace_size(M, K, N, bits) bytes (the size may be 0), 256-byte
  *   aligned.  Its first 64 KiB hold arrival counters under the rules of awq_w4a16_gemm's: zero before
  *   the first call, left zero by every completed call, so that one workspace serves any sequence of

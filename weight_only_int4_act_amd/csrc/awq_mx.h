@@ -106,6 +106,7 @@ hipError_t launch_rms_norm(const uint16_t* X, const uint16_t* residual, const ui
 struct MxGemmPlan {
     int wm;                         // 0: the register kernel; else LDS tiles of 64 wm rows
     int nz;                         // slices of K
+    int cstride;                    // arrival counter i at word i * cstride of the counter region
     int64_t col_tiles, row_tiles;   // workgroup tiles
     size_t ws_bytes;
 };

@@ -7,6 +7,7 @@ namespace {
 
 constexpr int64_t kIntMax = 0x7fffffff;
 constexpr int64_t kRowsMax = (int64_t)65535 * 16;        // M of the product
+constexpr int64_t kColsMax = 4194304;                    // N of the product (32-bit offsets of a row tile of Y)
 constexpr int64_t kWeightMax = (int64_t)1 << 36;         // K * N of packed weights
 
 bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
@@ -103,7 +104,8 @@ int awq_rms_norm(const void* X_bf16, const void* residual_bf16, const void* weig
 }
 
 size_t awq_mx_gemm_workspace_size(int64_t M, int64_t K, int64_t N, int32_t bits) {
-    if (!rows_ok(M, K) || M > kRowsMax || !weights_ok(K, N) || (bits != 8 && bits != 4)) return 0;
+    if (!rows_ok(M, K) || M > kRowsMax || !weights_ok(K, N) || N > kColsMax || (bits != 8 && bits != 4))
+        return 0;
     return awq::plan_mx_gemm(M, K, N, bits).ws_bytes;
 }
 
@@ -111,7 +113,8 @@ int awq_mx_gemm(const uint8_t* xcodes, const uint8_t* xscales, int32_t bits, int
                 const uint8_t* scales, int64_t K, int64_t N, void* Y_bf16, void* workspace, size_t ws_bytes,
                 void* stream) {
     if (!xcodes || !xscales || !codes || !scales || !Y_bf16) return AWQ_ERR_INVALID_ARG;
-    if (!rows_ok(M, K) || M > kRowsMax || !weights_ok(K, N) || N % 8 != 0) return AWQ_ERR_INVALID_ARG;
+    if (!rows_ok(M, K) || M > kRowsMax || !weights_ok(K, N) || N > kColsMax || N % 8 != 0)
+        return AWQ_ERR_INVALID_ARG;
     if (bits != 8 && bits != 4) return AWQ_ERR_UNSUPPORTED;
     if (!aligned(xcodes, 16) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(Y_bf16, 16))
         return AWQ_ERR_INVALID_ARG;

@@ -8,6 +8,7 @@
 // 128 and bytes 64+16g .. 64+16g+15.  In both, the scale byte of lane (i, g) applies to block g
 // (channels 32g .. 32g+31).  Results: lane (i, g), element r = weight column 4g + r, row i.
 #include <algorithm>
+#include <type_traits>
 
 #include "awq_mx.h"
 
@@ -25,87 +26,182 @@ __device__ __forceinline__ floatx4 mx_mfma(const u32x4& w, const i32x8& x, const
                                                             (int)xscale);
 }
 
-// 16 rows x 64 columns per workgroup; its four wavefronts take every fourth 128-channel chunk and
-// their sums meet in LDS in a fixed order.
-template <int BITS>
-__global__ __launch_bounds__(256) void k_mx_gemm(const uint8_t* __restrict__ xcodes,
-                                                 const uint8_t* __restrict__ xscales, int64_t M,
-                                                 const uint8_t* __restrict__ codes,
-                                                 const uint8_t* __restrict__ scales, int64_t K, int64_t N,
-                                                 int64_t kb_all, uint16_t* __restrict__ Y) {
-    __shared__ floatx4 red[3][4][64];
-    lds_poison_start(&red[0][0][0], 3 * 4 * 64);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-    const int64_t tile = blockIdx.x, m = (int64_t)blockIdx.y * 16 + i;
-    const int64_t row = min(m, M - 1);           // rows past M repeat the last one and are not stored
-    const uint8_t* xr = xcodes + row * (BITS == 8 ? K : K / 2);
-    const uint8_t* xs = xscales + row * (K / kMxBlock);
-    const int64_t blocks = K / kMxBlock;
-    floatx4 acc[4];
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)(uint32_t)bytes, 0x00020000);
+}
+constexpr uint32_t kOutside = 0x80000000u;   // an offset past every resource (all are below 2 GiB)
+constexpr int kCpolStream = 2;               // non-temporal: data read once
+constexpr int kCpolAgent = 16;               // device-coherent level (the sc1 bit)
+__device__ __forceinline__ void store4_agent(__amdgpu_buffer_rsrc_t r, uint32_t off, floatx4 v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, off, 0, kCpolAgent);
+}
+__device__ __forceinline__ floatx4 load4_agent(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kCpolAgent));
+}
+
+
+// ---------------------------------------------------------------- up to 64 rows: weights streamed once
+// Bound by the weights' bytes.  A workgroup owns 64 columns (one tile of packed weights, contiguous
+// in memory) and a slice of K; its NW wavefronts take every NW-th 128-channel chunk and keep D of
+// them in flight in registers: 4 KB of codes by non-temporal loads, the scale words, and the rows'
+// elements and scale bytes (16 RF rows, repeated reads that the caches serve).  A load past the slice,
+// past K or past the last row lies outside its buffer resource: it brings zeros and costs no traffic,
+// so the loop needs no branch between a load and its use.  The wavefronts' sums meet in LDS in a fixed
+// order; with several slices the last workgroup to arrive adds the
+// float32 partials in slice order.
+template <int BITS, int RF, int NW, int D>
+__global__ __launch_bounds__(64 * NW) void k_mx_gemm_rows(
+    const uint8_t* __restrict__ xcodes, const uint8_t* __restrict__ xscales, int rows,
+    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t K, int64_t N, int64_t kb_all,
+    uint16_t* __restrict__ Y, float* __restrict__ part, uint32_t* __restrict__ cnt, int cstride) {
+    constexpr int H = BITS == 8 ? 2 : 1;         // 16-byte pieces of a lane's elements
+    __shared__ floatx4 red[NW][RF][4][64];
+    __shared__ uint32_t arrival;
+    lds_poison_start(&red[0][0][0][0], NW * RF * 4 * 64);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int i = lane & 15, g = lane >> 4;
+    const int64_t tile = blockIdx.x;
+    const int z = blockIdx.y, nz = gridDim.y;
+    const int chunks = (int)(kb_all / 4), per = (chunks + nz - 1) / nz;
+    const int cb = min(z * per, chunks), ce = min(cb + per, chunks);
+    const uint32_t xrow = (uint32_t)(BITS == 8 ? K : K / 2), srow = (uint32_t)(K / kMxBlock);
+    const __amdgpu_buffer_rsrc_t wr = rsrc(codes + tile * kb_all * 1024, kb_all * 1024);
+    const __amdgpu_buffer_rsrc_t fr = rsrc(scales + tile * kb_all * 64, kb_all * 64);
+    const __amdgpu_buffer_rsrc_t xr = rsrc(xcodes, (int64_t)rows * xrow);
+    const __amdgpu_buffer_rsrc_t sr = rsrc(xscales, (int64_t)rows * srow);
+
+    struct Buf {
+        u32x4 w[4], x[RF][H];
+        uint32_t we, xe[RF];
+    };
+    auto issue = [&](int c, Buf& b) {
+        const bool in = c < ce;
+        const uint32_t wo = in ? (uint32_t)c * 4096 + g * 1024 + i * 16 : kOutside;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = floatx4{0.f, 0.f, 0.f, 0.f};
-    for (int64_t c = wave; c < kb_all / 4; c += 4) {
-        const int64_t kb = 4 * c + g;
-        i32x8 x = i32x8{0, 0, 0, 0, 0, 0, 0, 0};
-        // past K: zero elements with the scale 1 (the weights are padded with zeros there)
-        const uint32_t xe = kb < blocks ? xs[kb] : 127u;
-        if constexpr (BITS == 8) {
+        for (int rf = 0; rf < RF; ++rf) {
+            const uint32_t r = rf * 16 + i;
+            const bool inx = in && (int)r < rows;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t k = c * kMxChunk + 64 * h + 16 * g;
-                if (k < K) {
-                    const u32x4 v = *(const u32x4*)(xr + k);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[4 * h + e] = (int)v[e];
-                }
+            for (int h = 0; h < H; ++h) {
+                const uint32_t k = (uint32_t)c * (BITS == 8 ? 128 : 64) + h * 64 + g * 16;   // byte of the row
+                b.x[rf][h] = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, inx && k < xrow ? r * xrow + k : kOutside, 0, 0));
             }
-        } else if (kb < blocks) {
-            const u32x4 v = *(const u32x4*)(xr + kb * 16);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = (int)v[e];
+            const uint32_t kb = 4 * (uint32_t)c + g;
+            b.xe[rf] = __builtin_amdgcn_raw_buffer_load_b8(sr, inx && kb < srow ? r * srow + kb : kOutside, 0, 0);
         }
-        const int64_t wb = (tile * kb_all + kb) * kMxTile;
-        const uint32_t we = *(const uint32_t*)(scales + wb + 4 * i);
-        u32x4 w[4];
+        b.we = __builtin_amdgcn_raw_buffer_load_b32(fr, in ? (uint32_t)c * 256 + lane * 4 : kOutside, 0, kCpolStream);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = *(const u32x4*)(codes + (wb + 16 * j + i) * 16);
-        acc[0] = mx_mfma<BITS, 0>(w[0], x, acc[0], we, xe);
-        acc[1] = mx_mfma<BITS, 1>(w[1], x, acc[1], we, xe);
-        acc[2] = mx_mfma<BITS, 2>(w[2], x, acc[2], we, xe);
-        acc[3] = mx_mfma<BITS, 3>(w[3], x, acc[3], we, xe);
+        for (int j = 0; j < 4; ++j)
+            b.w[j] = __builtin_bit_cast(u32x4,
+                                        __builtin_amdgcn_raw_buffer_load_b128(wr, wo, j * 256, kCpolStream));
+    };
+    floatx4 acc[RF][4];
+#pragma unroll
+    for (int rf = 0; rf < RF; ++rf)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[rf][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+    auto consume = [&](const Buf& b) {
+        i32x8 x[RF];
+#pragma unroll
+        for (int rf = 0; rf < RF; ++rf) {
+            const u32x4 a = b.x[rf][0], d = H == 2 ? b.x[rf][H - 1] : u32x4{0, 0, 0, 0};
+            x[rf] = i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)d[0], (int)d[1], (int)d[2], (int)d[3]};
+        }
+#pragma unroll
+        for (int rf = 0; rf < RF; ++rf) {
+            acc[rf][0] = mx_mfma<BITS, 0>(b.w[0], x[rf], acc[rf][0], b.we, b.xe[rf]);
+            acc[rf][1] = mx_mfma<BITS, 1>(b.w[1], x[rf], acc[rf][1], b.we, b.xe[rf]);
+            acc[rf][2] = mx_mfma<BITS, 2>(b.w[2], x[rf], acc[rf][2], b.we, b.xe[rf]);
+            acc[rf][3] = mx_mfma<BITS, 3>(b.w[3], x[rf], acc[rf][3], b.we, b.xe[rf]);
+        }
+    };
+    Buf buf[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) issue(cb + wave + NW * d, buf[d]);
+    for (int c = cb + wave; c < ce; c += NW * D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            __builtin_amdgcn_sched_barrier(0);   // keep the loads of D chunks ahead of their products
+            consume(buf[d]);
+            issue(c + NW * (D + d), buf[d]);
+        }
     }
     // the products must not move into the branches below: they need every lane's operands
 #pragma unroll
-    for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[j]));
-    if (wave > 0) {
+    for (int rf = 0; rf < RF; ++rf)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) red[wave - 1][j][lane] = acc[j];
-    }
+        for (int j = 0; j < 4; ++j) {
+            asm volatile("" : "+v"(acc[rf][j]));
+            red[wave][rf][j][lane] = acc[rf][j];
+        }
     __syncthreads();
-    if (wave > 0) return;
+    // the joins: wavefront w takes fragment w % 4 and, with eight wavefronts, half of the row fragments
+    constexpr int P = NW / 4, RP = (RF + P - 1) / P;
+    const int frag = wave % 4, rf0 = wave / 4 * RP;
+    floatx4 sum[RP];                             // columns 16 frag + 4g .. + 3
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const floatx4 v = ((acc[j] + red[0][j][lane]) + red[1][j][lane]) + red[2][j][lane];
-        const int64_t n = tile * kMxTile + 16 * j + 4 * g;
-        if (m < M && n < N)                      // N % 8 == 0: n < N implies n + 3 < N
-            *(uint2*)(Y + m * N + n) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    for (int q = 0; q < RP; ++q) {
+        const int rf = min(rf0 + q, RF - 1);
+        sum[q] = red[0][rf][frag][lane];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) sum[q] += red[w][rf][frag][lane];
     }
+    const int64_t n = tile * kMxTile + 16 * frag + 4 * g;
+    auto write_y = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < RP; ++q) {
+            const int r = (rf0 + q) * 16 + i;
+            if (r < rows && n < N)               // N % 8 == 0: n < N implies n + 3 < N
+                *(uint2*)(Y + (int64_t)r * N + n) =
+                    uint2{pack_bf16x2(sum[q][0], sum[q][1]), pack_bf16x2(sum[q][2], sum[q][3])};
+        }
+    };
+    if (nz == 1) {
+        write_y();
+        return;
+    }
+    constexpr uint32_t kPart = RF * 4 * 1024;
+    const __amdgpu_buffer_rsrc_t pr = rsrc(part + tile * nz * (kPart / 4), (int64_t)nz * kPart);
+    auto poff = [&](int s, int q) {
+        return rf0 + q < RF ? (uint32_t)(s * kPart + ((rf0 + q) * 4 + frag) * 1024 + lane * 16) : kOutside;
+    };
+#pragma unroll
+    for (int q = 0; q < RP; ++q) store4_agent(pr, poff(z, q), sum[q]);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wavefront's partial has landed
+    __syncthreads();
+    if (threadIdx.x == 0)
+        arrival = __hip_atomic_fetch_add(cnt + tile * cstride, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (arrival != (uint32_t)(nz - 1)) return;
+#pragma unroll
+    for (int q = 0; q < RP; ++q) sum[q] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < nz; ++s)
+#pragma unroll
+        for (int q = 0; q < RP; ++q) sum[q] += load4_agent(pr, poff(s, q));
+    write_y();
+    if (threadIdx.x == 0) __hip_atomic_store(cnt + tile * cstride, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // ---------------------------------------------------------------- rows by the hundred: tiles in LDS
-// 64 WM rows x 256 columns per workgroup, WM x WN wavefronts, each with 64 rows and 256/WN columns in
-// registers.  Per 128-channel chunk both operands are copied once per workgroup straight into LDS
-// (three stages: while chunk c is multiplied, c+1 has landed or is landing and c+2 is requested), in
-// the order in which the matrix core's lanes read them back:
-//   activations  1 KB per 16 rows and 64 bytes of each row: slot 4r + (p ^ (r/4 % 4)) holds piece p
-//                (16 bytes) of row r, so that the 16 lanes that read one piece of 16 rows hit 64
-//                different banks;
+// 16 RF WM rows x 256 columns per workgroup, WM x WN wavefronts, each with RF x CF fragments of 16 x 16
+// results in registers.  Per 128-channel chunk both operands are copied once per workgroup straight
+// into LDS, ST chunks deep, in the order in which the matrix core's lanes read them back:
+//   activations  1 KB units.  8 bits: 8 rows of 128 bytes; the two 16-byte pieces g and g + 4 that one
+//                lane needs lie together, at 32-byte slot g ^ (row/2 % 4).  4 bits: 16 rows of 64 bytes,
+//                piece g at 16-byte slot g ^ (row/4 % 4).  So a transfer reads whole lines, and lanes
+//                reading the same piece of eight rows hit different banks;
 //   weights      the packed order: 1 KB per block of 64 columns, read 256 contiguous bytes at a time;
-//   scales       weights: 64 bytes per block and 64 columns; activations: the bytes of four chunks at
-//                a time, from the 4-byte boundary at or before them (16 bytes and 4 more per row).
+//   scales       weights: 64 bytes per block and 64 columns; activations: one 4-byte word per row and
+//                chunk, from the 4-byte boundary at or before the chunk's bytes, in a ring of their own: a
+//                row whose scales do not start on a boundary takes bytes from the next chunk's word, too.
 // Every transfer is issued from inline asm and waited for with counted vmcnt waits (transfers of a
-// wavefront complete in order); the barrier after the wait publishes the stage to all wavefronts, and
-// says that nobody reads the stage before any more, which is the next one to be refilled.
+// wavefront complete in order).  A turn multiplies one chunk in two halves of CF/2 column fragments,
+// each product followed by its share of everything else, because a wavefront issues in order and a
+// product keeps its matrix core busy for 32 cycles: during the first half the transfers of chunk
+// c + ST - 1 are issued and the second half's weights are read from LDS; then a barrier says that chunk c
+// is in every wavefront's registers and chunk c + 1 has landed; during the second half the next chunk's
+// activations and first weights are read.
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ i32x4 byte_rsrc(const void* base, uint32_t bytes) {
     const uint64_t a = (uint64_t)(uintptr_t)base;
@@ -139,15 +235,6 @@ __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t voff, uint32_t soff, u
         : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(soff)), "s"(__builtin_amdgcn_readfirstlane(lds))
         : "memory");
 }
-constexpr uint32_t kOutside = 0x80000000u;   // a voff past every resource (all are below 2 GiB)
-
-__device__ __forceinline__ void store4_agent(__amdgpu_buffer_rsrc_t r, uint32_t off, floatx4 v) {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, off, 0, 16);
-}
-__device__ __forceinline__ floatx4 load4_agent(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    return __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 16));
-}
-
 // The results of four 16-column fragments for 16 rows (lane (i, g): row i, columns 16j + 4g .. + 3 of
 // fragment j) as bf16, rearranged so that lane (i, g) holds columns 16g .. 16g + 15 of row i: a 4 x 4
 // transposition between fragments and lane groups.
@@ -171,27 +258,61 @@ __device__ __forceinline__ void mx_rows16(const floatx4 (&v)[4], u32x4 (&out)[2]
     }
 }
 
-template <int BITS, int WM, int WN>
+// acc += weights x activations in place, in accumulation registers; J: the byte of the weights' scale
+// word.  (From the builtin the compiler makes products that write other registers than they read, and
+// copies 256 accumulators around every turn.)  The compiler does not see a product in this: what the
+// operands come from must be two instructions away, and results are read after mx_settle.
+template <int BITS>
+using XFrag = std::conditional_t<BITS == 8, i32x8, u32x4>;      // a lane's elements of a row fragment
+template <int BITS, int J>
+__device__ __forceinline__ void mx_mfma_acc(floatx4& acc, const u32x4& w, const XFrag<BITS>& x, uint32_t wscale,
+                                            uint32_t xscale) {
+#ifdef __HIP_DEVICE_COMPILE__                   // the host pass does not know these register classes
+#define MX_MFMA(OPSEL)                                                                                            \
+    if constexpr (BITS == 8)                                                                                      \
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " OPSEL " cbsz:4"                  \
+                     : "+a"(acc) : "v"(w), "v"(x), "v"(wscale), "v"(xscale));                                     \
+    else                                                                                                          \
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " OPSEL " cbsz:4 blgp:4"           \
+                     : "+a"(acc) : "v"(w), "v"(x), "v"(wscale), "v"(xscale))
+    if constexpr (J == 0) { MX_MFMA("op_sel_hi:[0,0,0]"); }
+    if constexpr (J == 1) { MX_MFMA("op_sel:[1,0,0] op_sel_hi:[0,0,0]"); }
+    if constexpr (J == 2) { MX_MFMA("op_sel_hi:[1,0,0]"); }
+    if constexpr (J == 3) { MX_MFMA("op_sel:[1,0,0] op_sel_hi:[1,0,0]"); }
+#undef MX_MFMA
+#endif
+}
+__device__ __forceinline__ void mx_pin(floatx4& acc) {
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("" : "+a"(acc));
+#endif
+}
+// No result of mx_mfma_acc is read before this many wait states (18 cover the longest product).
+__device__ __forceinline__ void mx_settle() { asm volatile("s_nop 15\n\ts_nop 7"); }
+
+template <int BITS, int WM, int WN, int RF, int CF, int ST>
 struct TileShape {
-    static constexpr int kWaves = WM * WN, kRows = 64 * WM, kCols = 256;
-    static constexpr int kHalves = BITS == 8 ? 2 : 1;             // 64-byte pieces of a row's chunk
-    static constexpr int kXk = kRows / 16 * kHalves;              // 1 KB units of activations per chunk
+    static constexpr int kWaves = WM * WN, kRows = 16 * RF * WM, kCols = 16 * CF * WN;
+    static_assert(kCols == 256 && kRows % 64 == 0 && CF % 4 == 0, "tile shape");
+    static constexpr int kXk = kRows * BITS / 64;                 // 1 KB units of activations per chunk
     static constexpr int kWk = kCols / 64 * 4;                    // 1 KB units of weights per chunk
-    static constexpr int kData = (kXk + kWk) / kWaves;            // transfers per wavefront and chunk
-    static_assert(kXk % kWaves == 0 && kWk % kWaves == 0, "even shares");
-    static constexpr int kStage = (kXk + kWk + 1) * 1024;         // and 1 KB of weight scales
-    static constexpr int kXs = kRows * 20;                        // activation scales of four chunks
-    static constexpr int kLds = 3 * kStage + 2 * kXs;
+    static constexpr int kXu = kXk / kWaves, kWu = kWk / kWaves;  // per wavefront
+    static constexpr int kData = kXu + kWu + 2;                   // and a share of the scales
+    static_assert(kXk % kWaves == 0 && kWk % kWaves == 0 && kWaves == 4, "even shares");
+    static constexpr int kStage = (kXk + kWk + 1) * 1024;         // with 1 KB of weight scales
+    static constexpr int kRing = ST + 1, kPlane = kRows * 4;      // words of activation scales
+    static constexpr int kLds = ST * kStage + kRing * kPlane;
+    static_assert(kLds <= 160 * 1024, "LDS of a CU");
+    static_assert(ST >= 3 && (ST - 1) * kData + 1 < 64, "counted waits");
 };
 
-template <int BITS, int WM, int WN>
+template <int BITS, int WM, int WN, int RF, int CF, int ST>
 __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     const uint8_t* __restrict__ xcodes, const uint8_t* __restrict__ xscales, int64_t M,
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t K, int64_t N, int64_t kb_all,
     uint16_t* __restrict__ Y, float* __restrict__ part, uint32_t* __restrict__ cnt, int row_tiles, int col_tiles,
     int nz, int total, int per_xcd) {
-    using S = TileShape<BITS, WM, WN>;
-    constexpr int CF = 16 / WN;                  // 16-column fragments per wavefront
+    using S = TileShape<BITS, WM, WN, RF, CF, ST>;
     extern __shared__ u32x4 lds[];
     const int logical = xcd_tile(blockIdx.x, per_xcd);
     if (logical >= total) return;
@@ -205,236 +326,330 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int i = lane & 15, g = lane >> 4;
     const int wm = wave / WN, wn = wave % WN;
-    const int chunks = (int)(kb_all / 4), per = (chunks + nz - 1) / nz;
+    const int chunks = (int)(kb_all / 4), per = ((chunks + nz - 1) / nz + 1) / 2 * 2;
     const int cb = min(z * per, chunks), ce = min(cb + per, chunks);
     const int64_t row0 = (int64_t)rt * S::kRows, t0 = (int64_t)ct * 4, nt = (N + 63) / 64;
     const int rows = (int)min<int64_t>(S::kRows, M - row0);       // rows past the last repeat it
+    const int cts = (int)min<int64_t>(4, nt - t0);                // column tiles past the last repeat it
     const uint32_t xrow = (uint32_t)(BITS == 8 ? K : K / 2), srow = (uint32_t)(K / kMxBlock);
+    const uint32_t wtile = (uint32_t)kb_all * 1024, ftile = (uint32_t)kb_all * 64;
+    const int Kc = (int)K;
 
-    const uint32_t base = (uint32_t)(uintptr_t)lds;
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
     const i32x4 xr = byte_rsrc(xcodes + row0 * xrow, (uint32_t)rows * xrow);
-    const i32x4 wr = byte_rsrc(codes + t0 * kb_all * 1024, (uint32_t)(min<int64_t>(4, nt - t0) * kb_all * 1024));
-    const i32x4 fr = byte_rsrc(scales + t0 * kb_all * 64, (uint32_t)(min<int64_t>(4, nt - t0) * kb_all * 64));
+    const i32x4 wr = byte_rsrc(codes + t0 * wtile, (uint32_t)cts * wtile);
+    const i32x4 fr = byte_rsrc(scales + t0 * ftile, (uint32_t)cts * ftile);
     const uint8_t* s0 = xscales + row0 * srow;
     const uint32_t mis = (uint32_t)((uintptr_t)s0 & 3);           // read whole aligned words
     const i32x4 sr = byte_rsrc(s0 - mis, ((uint32_t)rows * srow + mis + 3) / 4 * 4);
 
-    uint32_t xoff[S::kXk / S::kWaves], woff[S::kWk / S::kWaves];
-    int xk[S::kXk / S::kWaves];                  // first channel of the lane's piece within a chunk
-#pragma unroll
-    for (int u = 0; u < S::kXk / S::kWaves; ++u) {
-        const int e = u * S::kWaves + wave, rf = e / S::kHalves, h = e % S::kHalves;
-        const int r = lane >> 2, p = (lane & 3) ^ ((r >> 2) & 3);
-        xoff[u] = (uint32_t)min(rf * 16 + r, rows - 1) * xrow + 64 * h + 16 * p;
-        xk[u] = BITS == 8 ? 64 * h + 16 * p : 32 * p;
-    }
-#pragma unroll
-    for (int u = 0; u < S::kWk / S::kWaves; ++u) {
-        const int e = u * S::kWaves + wave;
-        woff[u] = (uint32_t)(min<int64_t>(e / 4, nt - t0 - 1) * kb_all * 1024 + (e % 4) * 1024 + lane * 16);
-    }
-    const uint32_t foff = (uint32_t)(min<int64_t>(lane / 16, nt - t0 - 1) * kb_all * 64 + (lane % 16) * 16);
-    // activation scales of chunks 4q .. 4q+3: the first WM wavefronts bring 16 bytes of 64 rows each, the
-    // next WM the 4 bytes after them
-    static_assert(2 * WM <= S::kWaves, "a wavefront per part");
-    const bool wide = wave < WM;
-    const int spart = wide ? wave : wave - WM;
-    const uint32_t soff = (((uint32_t)min(spart * 64 + lane, rows - 1) * srow + mis) & ~3u) + (wide ? 0 : 16);
-    const uint32_t sdst = wide ? spart * 1024 : S::kRows * 16 + spart * 256;
-    auto issue_scales = [&](int q) {
-        const uint32_t dst = 3 * S::kStage + (q & 1) * S::kXs + sdst, from = 16u * (uint32_t)min(q, (chunks - 1) >> 2);
-        if (wave >= 2 * WM) return;
+    // This lane's piece of the wavefront's first activation unit (the next one is kWaves units further
+    // down, with the same piece), and the piece's first channel within a chunk.  Rows past `rows` and
+    // column tiles past `cts` lie outside the resources: zeros.
+    constexpr int kUnitRows = BITS == 8 ? 8 : 16, kPieces = BITS == 8 ? 8 : 4;
+    const int ur = wave * kUnitRows + lane / kPieces;
+    const int us = lane % kPieces;               // slot of the row
+    const int up = BITS == 8 ? ((us >> 1) ^ ((ur >> 1) & 3)) + 4 * (us & 1) : us ^ ((ur >> 2) & 3);
+    const uint32_t xoff = (uint32_t)ur * xrow + 16 * up, xstep = S::kWaves * kUnitRows * xrow;
+    const int xk = up * (BITS == 8 ? 16 : 32);
+    const uint32_t woff = wave * 1024 + lane * 16;               // block `wave` of the chunk; one column tile per unit
+    const uint32_t foff = wave * ftile + lane * 4;               // one column tile per wavefront
+    // activation scales: 64 rows per wavefront (the same rows by several where the tile has fewer)
+    constexpr int kParts = S::kRows / 64;
+    const int part64 = wave % kParts;
+    const uint32_t soff = ((uint32_t)(part64 * 64 + lane) * srow + mis) & ~3u;
+    auto plane_op = [&](int c, int slot) __attribute__((always_inline)) {
+        const uint32_t dst = ST * S::kStage + slot * S::kPlane + part64 * 256;
         if constexpr (kLdsPoison) {              // debug build: scales of about 2^120 where these will land
-            if (wide) lds[dst / 16 + lane] = lds_nan16();
-            else ((uint32_t*)lds)[dst / 4 + lane] = kLdsNan;
+            ((uint32_t*)lds)[dst / 4 + lane] = kLdsNan;
             lds_write_fence();
         }
-        if (wide) dma16(sr, soff + from, 0, base + dst);
-        else dma4(sr, soff + from, 0, base + dst);
+        dma4(sr, 4 * c < (int)srow + 4 ? soff + 4 * c : kOutside, 0, base + dst);
     };
-    auto issue = [&](int c, int stage) {
-        const uint32_t st = base + stage * S::kStage;
-        if constexpr (kLdsPoison) {              // debug build: NaN where this wavefront's transfers will land
-            u32x4* l = lds + stage * (S::kStage / 16);
-#pragma unroll
-            for (int u = 0; u < S::kXk / S::kWaves; ++u) l[(u * S::kWaves + wave) * 64 + lane] = lds_nan16();
-#pragma unroll
-            for (int u = 0; u < S::kWk / S::kWaves; ++u) l[(S::kXk + u * S::kWaves + wave) * 64 + lane] = lds_nan16();
-            if (wave == S::kWaves - 1) l[(S::kXk + S::kWk) * 64 + lane] = lds_nan16();
+    // transfer k of chunk c's batch (the activation scales are the next chunk's); a chunk past the slice
+    // brings zeros (no traffic), so that the counted waits stay the same
+    auto issue_op = [&](int c, int stage, int slot, int k) __attribute__((always_inline)) {
+        if (k == S::kData - 1) return plane_op(c + 1, slot);
+        const int left = c < ce ? Kc - c * kMxChunk : 0;
+        const uint32_t cc = (uint32_t)(c < chunks ? c : chunks - 1), st = stage * S::kStage;
+        const bool in_x = k > 0 && k <= S::kXu;
+        const int u = in_x ? k - 1 : k - 1 - S::kXu;
+        const uint32_t unit = k == 0 ? (S::kXk + S::kWk) * 1024 + wave * 256
+                                     : ((in_x ? 0 : S::kXk) + u * S::kWaves + wave) * 1024;
+        if constexpr (kLdsPoison) {              // debug build: NaN where this transfer will land
+            if (k == 0) ((uint32_t*)lds)[(st + unit) / 4 + lane] = kLdsNan;
+            else lds[(st + unit) / 16 + lane] = lds_nan16();
             lds_write_fence();
         }
-        if (wave == S::kWaves - 1) dma16(fr, foff, (uint32_t)c * 256, st + (S::kXk + S::kWk) * 1024);
-        const int left = (int)min<int64_t>(K - (int64_t)c * kMxChunk, kMxChunk);
-#pragma unroll
-        for (int u = 0; u < S::kXk / S::kWaves; ++u)
-            dma16(xr, xk[u] < left ? xoff[u] : kOutside, (uint32_t)c * (BITS == 8 ? 128 : 64),
-                  st + (u * S::kWaves + wave) * 1024);
-#pragma unroll
-        for (int u = 0; u < S::kWk / S::kWaves; ++u)
-            dma16(wr, woff[u], (uint32_t)c * 4096, st + (S::kXk + u * S::kWaves + wave) * 1024);
+        if (k == 0) dma4(fr, left > 0 ? foff : kOutside, cc * 256, base + st + unit);
+        else if (in_x) dma16(xr, xk < left ? xoff + u * xstep : kOutside, cc * (BITS == 8 ? 128 : 64), base + st + unit);
+        else dma16(wr, left > 0 ? woff + u * wtile : kOutside, cc * 4096, base + st + unit);
     };
 
-    // where this lane's scale byte of each of its four row fragments lies in the group's LDS area
-    uint32_t sa[4], sb[4];                       // chunks 0-2 (plus 4 each), chunk 3
+    // LDS byte offsets of this lane's operands within a stage, and of its scale byte of each row fragment
+    // within the chunk's words or the next chunk's
+    const uint32_t xl = BITS == 8
+        ? (2 * wm * RF + (i >> 3)) * 1024 + (i & 7) * 128 + ((g ^ ((i >> 1) & 3)) * 32)
+        : wm * RF * 1024 + i * 64 + ((g ^ ((i >> 2) & 3)) * 16);
+    const uint32_t wl = S::kXk * 1024 + g * 1024 + i * 16, fl = (S::kXk + S::kWk) * 1024 + g * 64 + i * 4;
+    uint32_t sa[RF];
+    bool later[RF];
 #pragma unroll
-    for (int rf = 0; rf < 4; ++rf) {
-        const int r = wm * 64 + rf * 16 + i;
-        const int sh = (int)(((uint32_t)min(r, rows - 1) * srow + mis) & 3);
-        sa[rf] = r * 16 + sh + g;
-        sb[rf] = sh + g >= 4 ? S::kRows * 16 + r * 4 + sh + g - 4 : r * 16 + 12 + sh + g;
+    for (int rf = 0; rf < RF; ++rf) {
+        const int r = (wm * RF + rf) * 16 + i, b = (int)(((uint32_t)r * srow + mis) & 3) + g;
+        sa[rf] = r * 4 + (b & 3);
+        later[rf] = b >= 4;
     }
 
-    floatx4 acc[4][CF];
+    floatx4 acc[RF][CF];
 #pragma unroll
-    for (int rf = 0; rf < 4; ++rf)
+    for (int rf = 0; rf < RF; ++rf)
 #pragma unroll
         for (int j = 0; j < CF; ++j) acc[rf][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-    auto compute = [&](int c, int stage) {
-        const u32x4* l = lds + stage * (S::kStage / 16);
-        const uint8_t* xs = (const uint8_t*)lds + 3 * S::kStage + ((c >> 2) & 1) * S::kXs;
-        const uint32_t* f = (const uint32_t*)(l + (S::kXk + S::kWk) * 64);
-        const bool inside = 4 * (int64_t)c + g < K / kMxBlock;    // past K: elements are zero, the scale 1
-        uint32_t xe[4], we[CF / 4];
-        i32x8 x[4];
-        const int slot = i * 4 + (g ^ ((i >> 2) & 3));
-#pragma unroll
-        for (int rf = 0; rf < 4; ++rf) {
-            const uint32_t e = xs[(c & 3) == 3 ? sb[rf] : sa[rf] + 4 * (c & 3)];
-            xe[rf] = inside ? e : 127u;
-            const u32x4 a = l[((wm * 4 + rf) * S::kHalves) * 64 + slot];
-            u32x4 b = u32x4{0, 0, 0, 0};
-            if constexpr (BITS == 8) b = l[((wm * 4 + rf) * S::kHalves + 1) * 64 + slot];
-            x[rf] = i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
-        }
-#pragma unroll
-        for (int w = 0; w < CF / 4; ++w) we[w] = f[(wn * (CF / 4) + w) * 64 + g * 16 + i];
-#pragma unroll
-        for (int j = 0; j < CF; j += 4) {
-            const int t4 = wn * (CF / 4) + j / 4;
-            u32x4 w[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) w[q] = l[(S::kXk + t4 * 4 + g) * 64 + 16 * q + i];
-#pragma unroll
-            for (int rf = 0; rf < 4; ++rf) acc[rf][j] = mx_mfma<BITS, 0>(w[0], x[rf], acc[rf][j], we[j / 4], xe[rf]);
-#pragma unroll
-            for (int rf = 0; rf < 4; ++rf) acc[rf][j + 1] = mx_mfma<BITS, 1>(w[1], x[rf], acc[rf][j + 1], we[j / 4], xe[rf]);
-#pragma unroll
-            for (int rf = 0; rf < 4; ++rf) acc[rf][j + 2] = mx_mfma<BITS, 2>(w[2], x[rf], acc[rf][j + 2], we[j / 4], xe[rf]);
-#pragma unroll
-            for (int rf = 0; rf < 4; ++rf) acc[rf][j + 3] = mx_mfma<BITS, 3>(w[3], x[rf], acc[rf][j + 3], we[j / 4], xe[rf]);
+    typedef int i32x8_a16 __attribute__((ext_vector_type(8), aligned(16)));
+    struct Acts {
+        XFrag<BITS> x[RF];
+        uint32_t e[RF];
+    };
+    struct Half {
+        u32x4 w[CF / 2];
+        uint32_t e;
+    };
+    constexpr int H = CF / 2, kFetchX = RF * 2, kFetchW = H + 1, kMul = RF * H;
+    const uint8_t* const lb = (const uint8_t*)lds;
+    // LDS reads, one at a time: activations (slots: of the chunk's scales and the next chunk's)
+    auto fetch_x_op = [&](int stage, int slot, int slot1, int k, Acts& a) __attribute__((always_inline)) {
+        const int rf = k / 2;
+        if (k % 2 == 1) {
+            a.e[rf] = lb[sa[rf] + (uint32_t)(later[rf] ? ST * S::kStage + slot1 * S::kPlane : ST * S::kStage + slot * S::kPlane)];
+        } else if constexpr (BITS == 8) {        // 32 contiguous bytes
+            a.x[rf] = *(const i32x8_a16*)(lb + stage * S::kStage + xl + rf * 2048);
+        } else {
+            a.x[rf] = *(const u32x4*)(lb + stage * S::kStage + xl + rf * 1024);
         }
     };
+    auto fetch_w_op = [&](int stage, int half, int k, Half& h) __attribute__((always_inline)) {
+        const int j = wn * CF + half * H + (k > 0 ? k - 1 : 0);   // fragment among the tile's 16
+        const uint8_t* l = lb + stage * S::kStage;
+        if (k == 0) h.e = *(const uint32_t*)(l + fl + j / 4 * 256);
+        else h.w[k - 1] = *(const u32x4*)(l + wl + j / 4 * 4096 + j % 4 * 256);
+    };
+    auto product = [&](const Acts& a, const uint32_t (&e)[RF], const Half& h, int half, int n) __attribute__((always_inline)) {
+        const int q = n / RF, rf = n % RF, j = half * H + q;
+        if (j % 4 == 0) mx_mfma_acc<BITS, 0>(acc[rf][j], h.w[q], a.x[rf], h.e, e[rf]);
+        if (j % 4 == 1) mx_mfma_acc<BITS, 1>(acc[rf][j], h.w[q], a.x[rf], h.e, e[rf]);
+        if (j % 4 == 2) mx_mfma_acc<BITS, 2>(acc[rf][j], h.w[q], a.x[rf], h.e, e[rf]);
+        if (j % 4 == 3) mx_mfma_acc<BITS, 3>(acc[rf][j], h.w[q], a.x[rf], h.e, e[rf]);
+    };
 
-    // Past the last chunk the transfers are issued all the same (the last chunk's, into a stage that
-    // nobody reads again), so that the counted waits stay the same.
-    const int last = max(ce - 1, 0);
-    issue_scales(cb >> 2);
-    issue_scales((cb >> 2) + 1);
-    issue(min(cb, last), 0);
-    issue(min(cb + 1, last), 1);
-    int stage = 0, ahead = 2;
-    for (int c = cb; c < ce; ++c) {
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(S::kData) : "memory");
-        if ((c & 3) == 1) issue_scales((c >> 2) + 1);   // read from the next multiple of 4 on
-        issue(min(c + 2, last), ahead);
-        compute(c, stage);
-        stage = stage == 2 ? 0 : stage + 1;
-        ahead = ahead == 2 ? 0 : ahead + 1;
+    plane_op(cb, 0);
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s)
+#pragma unroll
+        for (int k = 0; k < S::kData; ++k) issue_op(cb + s, s, s + 1, k);
+    Acts xa, xb;
+    Half lo, hi;
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((ST - 2) * S::kData) : "memory");
+#pragma unroll
+    for (int k = 0; k < kFetchX; ++k) fetch_x_op(0, 0, 1, k, xa);
+#pragma unroll
+    for (int k = 0; k < kFetchW; ++k) fetch_w_op(0, 0, k, lo);
+    // of chunk c; the ring slot after it holds the next chunk's scales, the one before it is refilled
+    int stage = 0, slot = 0;
+    auto turn = [&](int c, const Acts& now, Acts& next) __attribute__((always_inline)) {
+        const int behind = stage == 0 ? ST - 1 : stage - 1, ahead = stage == ST - 1 ? 0 : stage + 1;
+        const int slot_behind = slot == 0 ? S::kRing - 1 : slot - 1, slot1 = slot == S::kRing - 1 ? 0 : slot + 1;
+        const int slot2 = slot1 == S::kRing - 1 ? 0 : slot1 + 1;
+        const bool inside = 4 * c + g < (int)srow;                // past K: elements are zero, the scale 1
+        uint32_t e[RF];
+#pragma unroll
+        for (int rf = 0; rf < RF; ++rf) {
+            e[rf] = inside ? now.e[rf] : 127u;
+            asm volatile("" : "+v"(e[rf]));      // in registers here, not next to their use
+        }
+        asm volatile("s_nop 1");
+        constexpr int ops1 = kFetchW + S::kData;
+#pragma unroll
+        for (int n = 0; n < kMul; ++n) {
+            product(now, e, lo, 0, n);
+#pragma unroll
+            for (int k = 0; k < ops1; ++k) {
+                if (k * kMul / ops1 != n) continue;
+                if (k < kFetchW) fetch_w_op(stage, 1, k, hi);
+                else issue_op(c + ST - 1, behind, slot_behind, k - kFetchW);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((ST - 2) * S::kData) : "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        constexpr int ops2 = kFetchW + kFetchX;
+#pragma unroll
+        for (int n = 0; n < kMul; ++n) {
+            product(now, e, hi, 1, n);
+#pragma unroll
+            for (int k = 0; k < ops2; ++k) {
+                if (k * kMul / ops2 != n) continue;
+                if (k < kFetchW) fetch_w_op(ahead, 0, k, lo);
+                else fetch_x_op(ahead, slot1, slot2, k - kFetchW, next);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        stage = ahead;
+        slot = slot1;
+    };
+    // Two turns at a time: slices are multiples of two chunks, and past K a turn adds zeros.  (Leaving the
+    // loop between turns made the compiler copy the accumulators.)
+    for (int c = cb; c < ce; c += 2) {
+        turn(c, xa, xb);
+        turn(c + 1, xb, xa);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    // the products must not move into the branches below: they need every lane's operands
+    mx_settle();
+    auto settled = [&](int rf) __attribute__((always_inline)) {   // a row fragment's results may be read
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int rf = 0; rf < 4; ++rf)
-#pragma unroll
-        for (int j = 0; j < CF; ++j) asm volatile("" : "+v"(acc[rf][j]));
+        for (int j = 0; j < CF; ++j) mx_pin(acc[rf][j]);
+    };
 
-    auto write_y = [&]() __attribute__((always_inline)) {
+    // Results leave through a buffer resource, where a row past M or a column past N lies outside: a
+    // branch around the stores would let the compiler move products into it, and those need every
+    // lane's operands.
+    const __amdgpu_buffer_rsrc_t yr = rsrc(Y + row0 * N, (int64_t)rows * N * 2);
+    auto write_rows = [&](int rf, const floatx4 (&v)[CF]) __attribute__((always_inline)) {
+        const int r = (wm * RF + rf) * 16 + i;
 #pragma unroll
-        for (int rf = 0; rf < 4; ++rf) {
-            const int r = wm * 64 + rf * 16 + i;
+        for (int j = 0; j < CF; j += 4) {
+            const floatx4 q[4] = {v[j], v[j + 1], v[j + 2], v[j + 3]};
+            u32x4 out[2];
+            mx_rows16(q, out);
+            const int64_t n = t0 * kMxTile + (wn * CF + j) * 16 + 16 * g;
 #pragma unroll
-            for (int j = 0; j < CF; j += 4) {
-                const floatx4 v[4] = {acc[rf][j], acc[rf][j + 1], acc[rf][j + 2], acc[rf][j + 3]};
-                u32x4 out[2];
-                mx_rows16(v, out);
-                const int64_t n = (t0 + wn * (CF / 4) + j / 4) * kMxTile + 16 * g;
-                uint16_t* y = Y + (row0 + r) * N + n;
-                if (r < rows && n < N) *(u32x4*)y = out[0];          // N % 8 == 0
-                if (r < rows && n + 8 < N) *(u32x4*)(y + 8) = out[1];
-            }
+            for (int h = 0; h < 2; ++h)                              // N % 8 == 0
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    out[h], yr, r < rows && n + 8 * h < N ? (uint32_t)(r * N + n + 8 * h) * 2 : kOutside, 0, 0);
         }
     };
     if (nz == 1) {
-        write_y();
+#pragma unroll
+        for (int rf = 0; rf < RF; ++rf) {
+            settled(rf);
+            write_rows(rf, acc[rf]);
+        }
         return;
     }
     // Split over K: float32 partials in fragment order, one per (tile, K slice), written through to the
     // device-coherent level; the workgroup that arrives last adds them in slice order.
     constexpr uint32_t kPart = S::kRows * S::kCols * 4;
-    float* tile_part = part + (int64_t)tile * nz * (kPart / 4);
-    const __amdgpu_buffer_rsrc_t pr =
-        __builtin_amdgcn_make_buffer_rsrc(tile_part, (short)0, (int)(nz * kPart), 0x00020000);
-    auto poff = [&](int s, int rf, int j) { return (uint32_t)(s * kPart + ((wave * 4 + rf) * CF + j) * 1024 + lane * 16); };
+    const __amdgpu_buffer_rsrc_t pr = rsrc(part + (int64_t)tile * nz * (kPart / 4), (int64_t)nz * kPart);
+    auto poff = [&](int s, int rf, int j) { return (uint32_t)(s * kPart + ((wave * RF + rf) * CF + j) * 1024 + lane * 16); };
 #pragma unroll
-    for (int rf = 0; rf < 4; ++rf)
+    for (int rf = 0; rf < RF; ++rf) {
+        settled(rf);
 #pragma unroll
         for (int j = 0; j < CF; ++j) store4_agent(pr, poff(z, rf, j), acc[rf][j]);
+    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wavefront's partial has landed
     __syncthreads();
     uint32_t* arrival = (uint32_t*)lds;
     if (threadIdx.x == 0) *arrival = __hip_atomic_fetch_add(cnt + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
     if (*arrival != (uint32_t)(nz - 1)) return;
+    constexpr int RG = 8 / CF;                   // row fragments at a time: 8 loads in flight (16 were slower)
+#pragma unroll 1
+    for (int r0 = 0; r0 < RF; r0 += RG) {
+        floatx4 sum[RG][CF];
 #pragma unroll
-    for (int rf = 0; rf < 4; ++rf)
+        for (int rf = 0; rf < RG; ++rf)
 #pragma unroll
-        for (int j = 0; j < CF; ++j) acc[rf][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < nz; ++s)
+            for (int j = 0; j < CF; ++j) sum[rf][j] = load4_agent(pr, poff(0, r0 + rf, j));
+#pragma unroll 1
+        for (int s = 1; s < nz; ++s)
 #pragma unroll
-        for (int rf = 0; rf < 4; ++rf) {
+            for (int rf = 0; rf < RG; ++rf)
 #pragma unroll
-            for (int j = 0; j < CF; ++j) acc[rf][j] += load4_agent(pr, poff(s, rf, j));
-            __builtin_amdgcn_sched_barrier(0);   // one row fragment's loads in registers at a time
-        }
-    write_y();
+                for (int j = 0; j < CF; ++j) sum[rf][j] += load4_agent(pr, poff(s, r0 + rf, j));
+#pragma unroll
+        for (int rf = 0; rf < RG; ++rf) write_rows(r0 + rf, sum[rf]);
+    }
     if (threadIdx.x == 0) __hip_atomic_store(cnt + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 }  // namespace
 
-// Rows beyond which the LDS tiles take over from the register kernel.
-constexpr int64_t kTileRows = 64;
 constexpr size_t kCounterBytes = 65536;
 constexpr int kCus = kNumXcd * kCusPerXcd;
+constexpr int kMaxSlices = 16;
 
+// Which kernel, and how many slices of K, by the time that each would take: us on this card, fitted to
+// measured launches (K = 4096 .. 28672, N = 1024 .. 28672, 8-bit activations; 4-bit ones differ by a common
+// factor in the tiles).
+//   register kernel, R fragments of 16 rows: 4 + (64-column chunks per CU) * {.19, .23, .30, .42}[R - 1];
+//     e.g. 64 rows, K = N = 8192: 18.2 us (tiles 22), 64 rows, N = 28672: 51 us (tiles 37);
+//   tiles of 64 wm rows: 4.5 + turns * {.52, .80, 1.57} per round of one workgroup per CU (64-row
+//     tiles: up to two per CU, .84), and 2 + 1.15 wm nz for joining nz slices; not below the time in
+//     which these kernels stream the weights (4 TB/s).  E.g. 257 x 5120 x 13824: 33.6 us with 128
+//     rows a tile, 38 with 64, 66 with 256; 4096 rows: 256-row tiles.
 MxGemmPlan plan_mx_gemm(int64_t M, int64_t K, int64_t N, int bits) {
     MxGemmPlan p{};
-    if (M <= kTileRows) {
+    const int64_t chunks = mx_kb(K) / 4;
+    double best = 1e30;
+    if (M <= 64) {
+        static const double chunk_us[4] = {.19, .23, .30, .42};
         p.wm = 0;
         p.col_tiles = mx_nt(N);
-        p.row_tiles = (M + 15) / 16;
+        p.row_tiles = (M + 15) / 16;             // fragments of the one workgroup row
+        // about one workgroup per CU, and chunks enough for every wavefront's loads in flight
+        const int64_t deep = p.row_tiles == 1 ? 16 : 8;
         p.nz = 1;
-        return p;
+        if (p.col_tiles <= (int64_t)(kCounterBytes / 4))
+            p.nz = (int)std::max<int64_t>(1, std::min<int64_t>({kCus / p.col_tiles, chunks / deep, kMaxSlices}));
+        best = 4 + (double)(p.col_tiles * chunks) / kCus * chunk_us[p.row_tiles - 1];
+        p.cstride = (int)std::max<int64_t>(1, std::min<int64_t>(32, kCounterBytes / 4 / p.col_tiles));
+        p.ws_bytes = p.nz > 1 ? kCounterBytes + (size_t)p.col_tiles * p.nz * p.row_tiles * 4096 : 0;
+        if (M <= 16) return p;
     }
-    p.wm = M > 128 ? 4 : 2;
-    p.row_tiles = (M + 64 * p.wm - 1) / (64 * p.wm);
-    p.col_tiles = (N + 255) / 256;
-    const int64_t tiles = p.row_tiles * p.col_tiles, chunks = mx_kb(K) / 4;
-    int nz = 1;
-    if (tiles < kCus) nz = (int)std::max<int64_t>(1, std::min<int64_t>(kCus / tiles, chunks / 4));
-    p.nz = nz;
-    if (nz > 1) p.ws_bytes = kCounterBytes + (size_t)tiles * nz * 64 * p.wm * 256 * 4;
+    static const double turn_us[3] = {.52, .80, 1.57};
+    const double scale = bits == 8 ? 1. : .72, stream = 4.5 + (double)mx_codes_bytes(K, N) / 4e6;
+    for (int k = 0; k < 3; ++k) {
+        const int wm = 1 << k;
+        const int64_t rt = (M + 64 * wm - 1) / (64 * wm), ct = (N + 255) / 256, tiles = rt * ct;
+        for (int nz = 1; nz <= kMaxSlices; ++nz) {
+            const int64_t turns = ((chunks + nz - 1) / nz + 1) / 2 * 2, groups = tiles * nz;
+            if (nz > 1 && (turns < 4 || groups > 2 * kCus)) break;
+            const double rounds = wm == 1 && groups > kCus ? (double)((groups + 2 * kCus - 1) / (2 * kCus)) * .84 / .52
+                                                           : (double)((groups + kCus - 1) / kCus);
+            const double us = std::max(stream, 4.5 + scale * rounds * turns * turn_us[k]) + (nz > 1 ? 2 + 1.15 * wm * nz : 0);
+            if (us >= best) continue;
+            best = us;
+            p.wm = wm;
+            p.row_tiles = rt;
+            p.col_tiles = ct;
+            p.nz = nz;
+            p.cstride = 1;
+            p.ws_bytes = nz > 1 ? kCounterBytes + (size_t)groups * 64 * wm * 256 * 4 : 0;
+        }
+    }
     return p;
 }
 
-template <int BITS, int WM, int WN>
+template <int BITS, int RF, int NW, int D>
+static hipError_t launch_rows(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, const uint8_t* codes,
+                              const uint8_t* scales, int64_t K, int64_t N, uint16_t* Y, void* ws, const MxGemmPlan& p,
+                              hipStream_t st) {
+    k_mx_gemm_rows<BITS, RF, NW, D><<<dim3((unsigned)p.col_tiles, (unsigned)p.nz), 64 * NW, 0, st>>>(
+        xcodes, xscales, (int)M, codes, scales, K, N, mx_kb(K), Y, (float*)((char*)ws + kCounterBytes), (uint32_t*)ws,
+        p.cstride);
+    return hipGetLastError();
+}
+
+template <int BITS, int WM, int WN, int RF, int CF, int ST>
 static hipError_t launch_tile(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, const uint8_t* codes,
                               const uint8_t* scales, int64_t K, int64_t N, uint16_t* Y, void* ws, const MxGemmPlan& p,
                               hipStream_t st) {
-    using S = TileShape<BITS, WM, WN>;
+    using S = TileShape<BITS, WM, WN, RF, CF, ST>;
     const int64_t total = p.row_tiles * p.col_tiles * p.nz, per_xcd = (total + kNumXcd - 1) / kNumXcd;
-    const auto kernel = k_mx_gemm_tile<BITS, WM, WN>;
+    const auto kernel = k_mx_gemm_tile<BITS, WM, WN, RF, CF, ST>;
     // the limit is a property of the function on the current device; setting it again is harmless
     const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
     if (e != hipSuccess) return e;
@@ -447,15 +662,18 @@ static hipError_t launch_tile(const uint8_t* xcodes, const uint8_t* xscales, int
 hipError_t launch_mx_gemm(const uint8_t* xcodes, const uint8_t* xscales, int bits, int64_t M, const uint8_t* codes,
                           const uint8_t* scales, int64_t K, int64_t N, uint16_t* Y, void* ws, const MxGemmPlan& p,
                           hipStream_t st) {
-    if (p.wm == 0) {
-        const dim3 grid((unsigned)p.col_tiles, (unsigned)p.row_tiles);
-        if (bits == 8) k_mx_gemm<8><<<grid, 256, 0, st>>>(xcodes, xscales, M, codes, scales, K, N, mx_kb(K), Y);
-        else k_mx_gemm<4><<<grid, 256, 0, st>>>(xcodes, xscales, M, codes, scales, K, N, mx_kb(K), Y);
-        return hipGetLastError();
-    }
     const auto run = [&](auto f) { return f(xcodes, xscales, M, codes, scales, K, N, Y, ws, p, st); };
-    if (p.wm == 4) return run(bits == 8 ? launch_tile<8, 4, 2> : launch_tile<4, 4, 2>);
-    return run(bits == 8 ? launch_tile<8, 2, 4> : launch_tile<4, 2, 4>);
+    if (p.wm == 0) {
+        switch (p.row_tiles) {
+            case 1: return run(bits == 8 ? launch_rows<8, 1, 8, 2> : launch_rows<4, 1, 8, 2>);
+            case 2: return run(bits == 8 ? launch_rows<8, 2, 4, 2> : launch_rows<4, 2, 4, 2>);
+            case 3: return run(bits == 8 ? launch_rows<8, 3, 4, 1> : launch_rows<4, 3, 4, 1>);
+            default: return run(bits == 8 ? launch_rows<8, 4, 4, 1> : launch_rows<4, 4, 4, 1>);
+        }
+    }
+    if (p.wm == 4) return run(bits == 8 ? launch_tile<8, 2, 2, 8, 8, 3> : launch_tile<4, 2, 2, 8, 8, 4>);
+    if (p.wm == 2) return run(bits == 8 ? launch_tile<8, 2, 2, 4, 8, 4> : launch_tile<4, 2, 2, 4, 8, 4>);
+    return run(bits == 8 ? launch_tile<8, 1, 4, 4, 4, 3> : launch_tile<4, 1, 4, 4, 4, 3>);
 }
 
 }  // namespace awq
