@@ -313,7 +313,7 @@ int awq_w4a16_gemm_noalloc(const void* X_bf16, int64_t M, const float* s, const 
  *                Blocks past K and columns past N hold zeros (codes and scales), written by
  *                awq_mx_pack and relied on by awq_mx_gemm.
  * K must be a multiple of 32 (of 8 for a norm without codes).  bits is 8 or 4 (AWQ_ERR_UNSUPPORTED
- * otherwise).  s, where it may be NULL, is float32 [K], positive and finite: the input scales of an
+ * otherwise).  s, where it may be NULL, is float32 [K] with values in [2^-120, 2^120]: the input scales of an
  * AWQ search; weights are multiplied by it and activations divided.  Outputs must not overlap
  * inputs or each other (AWQ_ERR_INVALID_ARG) unless a paragraph below says so.  Codes, weights'
  * scales, s and bf16 activations are 16-byte aligned; W needs only its own type's alignment.
@@ -335,7 +335,7 @@ int awq_mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t K, int64_
                   void* stream);
 
 /* Activations into MX blocks: p = x / s_k, or with a gate p = x * g / (1 + e^-g) / s_k (the input of a
- * gated MLP's last layer: x = up, g = gate), evaluated in float32.
+ * gated MLP's last layer: x = up, g = gate), evaluated in float32 (1 / (1 + e^-g) below 2^-126 counts as zero).
  *   X, gate  bf16 [M, K] (gate may be NULL);  s  float32 [K] or NULL (1).
  */
 int awq_mx_quantize(const void* X_bf16, const void* gate_bf16, int64_t M, int64_t K, const float* s, int32_t bits,
@@ -344,7 +344,7 @@ int awq_mx_quantize(const void* X_bf16, const void* gate_bf16, int64_t M, int64_
 /* Root-mean-square norm behind a residual addition, with a quantized output:
  *   h = x + r,   y = h * weight / sqrt(mean_k h^2 + eps),
  * h in float32 (r = 0 when residual is NULL), the squares summed in float64.
- *   X, residual  bf16 [M, K] (residual may be NULL);  weight  bf16 [K];  eps in (0, 1].
+ *   X, residual  bf16 [M, K] (residual may be NULL), M at most 4194303;  weight  bf16 [K];  eps in (0, 1].
  *   residual_out bf16 [M, K] or NULL (NULL when residual is): h rounded to bf16.
  *   Y            bf16 [M, K] or NULL: y rounded to bf16.
  *   codes, scales  y / s_k in MX blocks of `bits` bits, from the float32 y; both or neither.  s

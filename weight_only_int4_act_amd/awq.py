@@ -468,10 +468,32 @@ _SCALE_DTYPES = (torch.uint8, torch.float8_e8m0fnu)   # a scale byte E stands fo
 _MX_BITS = {torch.float8_e4m3fn: 8, torch.uint8: 4}    # activations: e4m3 [.., K], or e2m1 pairs [.., K/2]
 
 
-def _mx_device(fn: str, *tensors: Optional[torch.Tensor]) -> None:
-    """Every tensor contiguous on one device, and that device the current one: the kernels are
-    launched on the current device's stream."""
-    dev = None
+_raw_stream = torch._C._cuda_getCurrentRawStream    # the handle alone: torch.cuda.current_stream builds an object
+
+
+# The checks below are one expression per tensor where it is right and say what is wrong where it is not:
+# these calls serve single tokens, and a call's checks should cost less than its launch.
+def _mx_arg(fn: str, name: str, t: torch.Tensor, dtype, shape) -> int:
+    """The address of a tensor of this dtype and shape (a tuple)."""
+    if t.dtype is not dtype or t.shape != shape:
+        _expect(fn, name, t, dtype, shape)
+    return t.data_ptr()
+
+
+def _mx_opt(fn: str, name: str, t: Optional[torch.Tensor], dtype, shape) -> Optional[int]:
+    return None if t is None else _mx_arg(fn, name, t, dtype, shape)
+
+
+def _mx_scales(fn: str, t: torch.Tensor, shape) -> int:
+    if t.shape != shape or t.dtype not in _SCALE_DTYPES:
+        _expect(fn, "scales", t, _SCALE_DTYPES, shape)
+    return t.data_ptr()
+
+
+def _mx_stream(fn: str, stream, *tensors: Optional[torch.Tensor]) -> int:
+    """The stream to launch on, once every tensor is contiguous on one device and that device is the
+    current one: the kernels are launched on the current device."""
+    dev = tensors[0].get_device()
     for t in tensors:
         if t is None:
             continue
@@ -479,17 +501,13 @@ def _mx_device(fn: str, *tensors: Optional[torch.Tensor]) -> None:
             raise ValueError("libawq takes device tensors")
         if not t.is_contiguous():
             raise ValueError("libawq takes contiguous tensors")
-        d = t.get_device()
-        if dev is None:
-            dev = d
-        elif d != dev:
+        if t.get_device() != dev:
             raise ValueError(f"{fn}: tensors on different devices")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"{fn}: tensors are on device {dev}, which is not the current device")
-
-
-def _mx_ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+    if stream is None:
+        return _raw_stream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _mx_rows(fn: str, K: int, what: int = 32) -> None:
@@ -497,20 +515,18 @@ def _mx_rows(fn: str, K: int, what: int = 32) -> None:
         raise ValueError(f"{fn}: K = {K} must be a positive multiple of {what}")
 
 
-def _mx_weights(fn: str, codes: torch.Tensor, scales: torch.Tensor, K: int, N: int) -> None:
+def _mx_weights(fn: str, codes: torch.Tensor, scales: torch.Tensor, K: int, N: int):
     kb, nt = -(-K // 128) * 4, -(-N // 64)
-    _expect(fn, "codes", codes, torch.uint8, (nt, kb, 64, 16))
-    _expect(fn, "scales", scales, _SCALE_DTYPES, (nt, kb, 64))
+    return (_mx_arg(fn, "codes", codes, torch.uint8, (nt, kb, 64, 16)), _mx_scales(fn, scales, (nt, kb, 64)))
 
 
-def _mx_acts(fn: str, codes: torch.Tensor, scales: torch.Tensor, M: int, K: int) -> int:
+def _mx_acts(fn: str, codes: torch.Tensor, scales: torch.Tensor, M: int, K: int):
     bits = _MX_BITS.get(codes.dtype)
     if bits is None:
         raise ValueError(f"{fn}: activation codes must be torch.float8_e4m3fn (8 bits) or torch.uint8 (4 bits), "
                          f"got {codes.dtype}")
-    _expect(fn, "codes", codes, codes.dtype, (M, K if bits == 8 else K // 2))
-    _expect(fn, "scales", scales, _SCALE_DTYPES, (M, K // 32))
-    return bits
+    return (bits, _mx_arg(fn, "codes", codes, codes.dtype, (M, K if bits == 8 else K // 2)),
+            _mx_scales(fn, scales, (M, K // 32)))
 
 
 def awq_mx_codes_bytes(K: int, N: int) -> int:
@@ -526,10 +542,11 @@ def awq_mx_pack(W: torch.Tensor, s: Optional[torch.Tensor], codes: torch.Tensor,
     fn = "awq_mx_pack"
     K, N = _matrix(fn, "W", W)
     _mx_rows(fn, K)
-    _expect(fn, "s", s, torch.float32, (K,), optional=True)
-    _mx_weights(fn, codes, scales, K, N)
-    _mx_device(fn, W, s, codes, scales)
-    _check(fn, _lib.awq_mx_pack(_mx_ptr(W), K, N, _mx_ptr(s), _mx_ptr(codes), _mx_ptr(scales), _stream(stream)))
+    ps = _mx_opt(fn, "s", s, torch.float32, (K,))
+    pc, pe = _mx_weights(fn, codes, scales, K, N)
+    st = _lib.awq_mx_pack(W.data_ptr(), K, N, ps, pc, pe, _mx_stream(fn, stream, W, s, codes, scales))
+    if st:
+        _check(fn, st)
 
 
 def awq_mx_unpack(codes: torch.Tensor, scales: torch.Tensor, s: Optional[torch.Tensor], W: torch.Tensor,
@@ -537,10 +554,11 @@ def awq_mx_unpack(codes: torch.Tensor, scales: torch.Tensor, s: Optional[torch.T
     fn = "awq_mx_unpack"
     K, N = _matrix(fn, "W", W)
     _mx_rows(fn, K)
-    _expect(fn, "s", s, torch.float32, (K,), optional=True)
-    _mx_weights(fn, codes, scales, K, N)
-    _mx_device(fn, codes, scales, s, W)
-    _check(fn, _lib.awq_mx_unpack(_mx_ptr(codes), _mx_ptr(scales), K, N, _mx_ptr(s), _mx_ptr(W), _stream(stream)))
+    ps = _mx_opt(fn, "s", s, torch.float32, (K,))
+    pc, pe = _mx_weights(fn, codes, scales, K, N)
+    st = _lib.awq_mx_unpack(pc, pe, K, N, ps, W.data_ptr(), _mx_stream(fn, stream, W, s, codes, scales))
+    if st:
+        _check(fn, st)
 
 
 def awq_mx_quantize(X: torch.Tensor, gate: Optional[torch.Tensor], s: Optional[torch.Tensor], codes: torch.Tensor,
@@ -548,32 +566,33 @@ def awq_mx_quantize(X: torch.Tensor, gate: Optional[torch.Tensor], s: Optional[t
     fn = "awq_mx_quantize"
     M, K = _matrix(fn, "X", X)
     _mx_rows(fn, K)
-    _expect(fn, "gate", gate, torch.bfloat16, (M, K), optional=True)
-    _expect(fn, "s", s, torch.float32, (K,), optional=True)
-    bits = _mx_acts(fn, codes, scales, M, K)
-    _mx_device(fn, X, gate, s, codes, scales)
-    _check(fn, _lib.awq_mx_quantize(_mx_ptr(X), _mx_ptr(gate), M, K, _mx_ptr(s), bits, _mx_ptr(codes),
-                                    _mx_ptr(scales), _stream(stream)))
+    pg = _mx_opt(fn, "gate", gate, torch.bfloat16, (M, K))
+    ps = _mx_opt(fn, "s", s, torch.float32, (K,))
+    bits, pc, pe = _mx_acts(fn, codes, scales, M, K)
+    st = _lib.awq_mx_quantize(X.data_ptr(), pg, M, K, ps, bits, pc, pe,
+                              _mx_stream(fn, stream, X, gate, s, codes, scales))
+    if st:
+        _check(fn, st)
 
 
 def awq_rms_norm(X: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor, eps: float,
                  residual_out: Optional[torch.Tensor], Y: Optional[torch.Tensor], s: Optional[torch.Tensor] = None,
                  codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None) -> None:
     fn = "awq_rms_norm"
-    M, K = _matrix(fn, "X", X)
+    M, K = MK = _matrix(fn, "X", X)
     _mx_rows(fn, K, 8 if codes is None else 32)
-    _expect(fn, "residual", residual, torch.bfloat16, (M, K), optional=True)
-    _expect(fn, "weight", weight, torch.bfloat16, (K,))
-    _expect(fn, "residual_out", residual_out, torch.bfloat16, (M, K), optional=True)
-    _expect(fn, "Y", Y, torch.bfloat16, (M, K), optional=True)
-    _expect(fn, "s", s, torch.float32, (K,), optional=True)
+    pr = _mx_opt(fn, "residual", residual, torch.bfloat16, MK)
+    pw = _mx_arg(fn, "weight", weight, torch.bfloat16, (K,))
+    po = _mx_opt(fn, "residual_out", residual_out, torch.bfloat16, MK)
+    py = _mx_opt(fn, "Y", Y, torch.bfloat16, MK)
+    ps = _mx_opt(fn, "s", s, torch.float32, (K,))
     if (codes is None) != (scales is None):
         raise ValueError(f"{fn}: codes and scales are given together or not at all")
-    bits = 8 if codes is None else _mx_acts(fn, codes, scales, M, K)
-    _mx_device(fn, X, residual, weight, residual_out, Y, s, codes, scales)
-    _check(fn, _lib.awq_rms_norm(_mx_ptr(X), _mx_ptr(residual), _mx_ptr(weight), M, K, float(eps),
-                                 _mx_ptr(residual_out), _mx_ptr(Y), _mx_ptr(s), bits, _mx_ptr(codes),
-                                 _mx_ptr(scales), _stream(stream)))
+    bits, pc, pe = (8, None, None) if codes is None else _mx_acts(fn, codes, scales, M, K)
+    st = _lib.awq_rms_norm(X.data_ptr(), pr, pw, M, K, eps, po, py, ps, bits, pc, pe,
+                           _mx_stream(fn, stream, X, residual, weight, residual_out, Y, s, codes, scales))
+    if st:
+        _check(fn, st)
 
 
 def awq_mx_gemm_workspace_size(M: int, K: int, N: int, bits: int) -> int:
@@ -585,11 +604,12 @@ def awq_mx_gemm(xcodes: torch.Tensor, xscales: torch.Tensor, codes: torch.Tensor
     fn = "awq_mx_gemm"
     M, N = _matrix(fn, "Y", Y)
     K = 32 * _matrix(fn, "xscales", xscales, xscales.dtype if xscales.dtype in _SCALE_DTYPES else torch.uint8)[1]
-    bits = _mx_acts(fn, xcodes, xscales, M, K)
-    _mx_weights(fn, codes, scales, K, N)
-    _mx_device(fn, xcodes, xscales, codes, scales, Y, ws)
-    _check(fn, _lib.awq_mx_gemm(_mx_ptr(xcodes), _mx_ptr(xscales), bits, M, _mx_ptr(codes), _mx_ptr(scales), K, N,
-                                _mx_ptr(Y), _mx_ptr(ws), _nbytes(ws), _stream(stream)))
+    bits, px, pxe = _mx_acts(fn, xcodes, xscales, M, K)
+    pc, pe = _mx_weights(fn, codes, scales, K, N)
+    st = _lib.awq_mx_gemm(px, pxe, bits, M, pc, pe, K, N, Y.data_ptr(), None if ws is None else ws.data_ptr(),
+                          _nbytes(ws), _mx_stream(fn, stream, Y, xcodes, xscales, codes, scales, ws))
+    if st:
+        _check(fn, st)
 
 
 @contextlib.contextmanager

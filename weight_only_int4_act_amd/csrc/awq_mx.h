@@ -28,34 +28,45 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
     const int e = (int)(top >> 23);
     return e == 255 ? 255u : (uint32_t)max(e - (BITS == 8 ? 8 : 2), 0);
 }
-// 2^(127 - E), the factor from values to stored elements; E <= 252 for a finite block.
-__device__ __forceinline__ float mx_to_stored(uint32_t E) { return __uint_as_float((254u - E) << 23); }
-// 2^(E - 127), the factor from stored elements to values (E = 0: the subnormal 2^-127; 255: NaN).
-__device__ __forceinline__ float mx_to_value(uint32_t E) {
-    return __uint_as_float(E == 0 ? 0x00400000u : E == 255 ? 0x7fc00000u : E << 23);
-}
-// Eight elements of a block -> packed codes.  e4m3: two words, saturated first (the conversion
-// itself turns what rounds beyond 448 into NaN).  e2m1: one word (the conversion saturates).
-__device__ __forceinline__ uint2 mx_e4m3x8(const float (&q)[8]) {
-    int w[2];
+// The conversions' scale operand: 2^(E - 127) with E in the exponent field (they read that field
+// alone: 0 is 2^-127, 255 turns every element into NaN).
+__device__ __forceinline__ float mx_scale(uint32_t E) { return __uint_as_float(E << 23); }
+// Eight numbers of a block -> packed codes.  e4m3: two words, saturated first (the conversion itself
+// turns what rounds beyond 448 into NaN).  e2m1: one word (the conversion saturates).
+__device__ __forceinline__ uint2 mx_e4m3x8(const float (&p)[8], uint32_t E) {
+    typedef short s16x2 __attribute__((ext_vector_type(2)));
+    const float scale = mx_scale(E), lim = E == 0 ? 0x1.cp-119f : 448.f * scale;
+    uint32_t w[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        int r = 0;
-        r = __builtin_amdgcn_cvt_pk_fp8_f32(__builtin_amdgcn_fmed3f(q[4 * h], -448.f, 448.f),
-                                            __builtin_amdgcn_fmed3f(q[4 * h + 1], -448.f, 448.f), r, false);
-        r = __builtin_amdgcn_cvt_pk_fp8_f32(__builtin_amdgcn_fmed3f(q[4 * h + 2], -448.f, 448.f),
-                                            __builtin_amdgcn_fmed3f(q[4 * h + 3], -448.f, 448.f), r, true);
-        w[h] = r;
+        float q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = __builtin_amdgcn_fmed3f(p[4 * h + i], -lim, lim);
+        s16x2 r = {0, 0};
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, q[0], q[1], scale, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, q[2], q[3], scale, true);
+        w[h] = __builtin_bit_cast(uint32_t, r);
     }
-    return uint2{(uint32_t)w[0], (uint32_t)w[1]};
+    return uint2{w[0], w[1]};
 }
-__device__ __forceinline__ uint32_t mx_e2m1x8(const float (&q)[8]) {
+__device__ __forceinline__ uint32_t mx_e2m1x8(const float (&p)[8], uint32_t E) {
+    const float scale = mx_scale(E);
     uint32_t r = 0;
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, q[0], q[1], 1.f, 0);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, q[2], q[3], 1.f, 1);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, q[4], q[5], 1.f, 2);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, q[6], q[7], 1.f, 3);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, p[0], p[1], scale, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, p[2], p[3], scale, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, p[4], p[5], scale, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, p[6], p[7], scale, 3);
     return r;
+}
+// x / s rounded to float32, for r = mx_recip(s): the quotient's first approximation corrected by its own
+// remainder (three operations where the compiler's division takes ten).  s in [2^-120, 2^120].
+__device__ __forceinline__ float mx_recip(float s) {
+    const float r = __builtin_amdgcn_rcpf(s);
+    return fmaf(fmaf(-s, r, 1.f), r, r);
+}
+__device__ __forceinline__ float mx_div(float x, float s, float r) {
+    const float q = x * r;
+    return fmaf(fmaf(-q, s, x), r, q);
 }
 // The largest |p| (as integer bits) of a block held by four consecutive lanes, eight elements each;
 // all four lanes must be active.
@@ -69,15 +80,14 @@ __device__ __forceinline__ uint32_t mx_block_top(const float (&p)[8]) {
 // Quantizes the eight elements of octet `oct` of a row (block oct / 4) and stores codes and scale.
 template <int BITS>
 __device__ __forceinline__ void mx_store8(const float (&p)[8], uint8_t* codes_row, uint8_t* scales_row, int64_t oct) {
-    const uint32_t top = mx_block_top(p);
-    const uint32_t E = mx_scale_byte<BITS>(top);
-    const bool bad = E == 255;
-    const float f = mx_to_stored(bad ? 127 : E);
-    float q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = bad ? 0.f : p[i] * f;
-    if constexpr (BITS == 8) *(uint2*)(codes_row + oct * 8) = mx_e4m3x8(q);
-    else *(uint32_t*)(codes_row + oct * 4) = mx_e2m1x8(q);
+    const uint32_t E = mx_scale_byte<BITS>(mx_block_top(p));
+    if constexpr (BITS == 8) {
+        const uint2 w = mx_e4m3x8(p, E);
+        *(uint2*)(codes_row + oct * 8) = E == 255 ? uint2{0u, 0u} : w;
+    } else {
+        const uint32_t w = mx_e2m1x8(p, E);
+        *(uint32_t*)(codes_row + oct * 4) = E == 255 ? 0u : w;
+    }
     if ((oct & 3) == 0) scales_row[oct >> 2] = (uint8_t)E;
 }
 // 16 bytes of bf16 -> eight floats

@@ -7,6 +7,7 @@ namespace {
 
 constexpr int64_t kIntMax = 0x7fffffff;
 constexpr int64_t kRowsMax = (int64_t)65535 * 16;        // M of the product
+constexpr int64_t kNormRowsMax = 4194303;                // M of the norm: threads of one launch below 2^32
 constexpr int64_t kColsMax = 4194304;                    // N of the product (32-bit offsets of a row tile of Y)
 constexpr int64_t kWeightMax = (int64_t)1 << 36;         // K * N of packed weights
 
@@ -79,7 +80,7 @@ int awq_rms_norm(const void* X_bf16, const void* residual_bf16, const void* weig
     if (!X_bf16 || !weight_bf16 || (!Y_bf16 && !codes) || !codes != !scales || (residual_out && !residual_bf16) ||
         (s && !codes))
         return AWQ_ERR_INVALID_ARG;
-    if (!in_range(M) || !in_range(K) || K % (codes ? awq::kMxBlock : 8) != 0 || M * K > ((int64_t)1 << 40))
+    if (!in_range(M) || M > kNormRowsMax || !in_range(K) || K % (codes ? awq::kMxBlock : 8) != 0 || M * K > ((int64_t)1 << 40))
         return AWQ_ERR_INVALID_ARG;
     if (!(eps > 0.f && eps <= 1.f)) return AWQ_ERR_INVALID_ARG;      // NaN fails too
     if (codes && bits != 8 && bits != 4) return AWQ_ERR_UNSUPPORTED;
