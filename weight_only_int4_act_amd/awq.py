@@ -493,15 +493,13 @@ def _mx_scales(fn: str, t: torch.Tensor, shape) -> int:
 def _mx_stream(fn: str, stream, *tensors: Optional[torch.Tensor]) -> int:
     """The stream to launch on, once every tensor is contiguous on one device and that device is the
     current one: the kernels are launched on the current device."""
-    dev = tensors[0].get_device()
+    dev = tensors[0].get_device()                   # -1 for a host tensor
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("libawq takes device tensors")
-        if not t.is_contiguous():
-            raise ValueError("libawq takes contiguous tensors")
-        if t.get_device() != dev:
+        if t is not None and (t.get_device() != dev or dev < 0 or not t.is_contiguous()):
+            if not all(u is None or u.is_cuda for u in tensors):
+                raise ValueError("libawq takes device tensors")
+            if not t.is_contiguous():
+                raise ValueError("libawq takes contiguous tensors")
             raise ValueError(f"{fn}: tensors on different devices")
     if dev != torch._C._cuda_getDevice():
         raise ValueError(f"{fn}: tensors are on device {dev}, which is not the current device")

@@ -210,31 +210,38 @@ __device__ __forceinline__ i32x4 byte_rsrc(const void* base, uint32_t bytes) {
                  (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000};
 }
 // 16 (4) bytes per lane from byte voff + soff of the resource to LDS address lds + 16 (4) * lane; a lane
-// whose voff is at or past the resource's end brings zeros.
+// whose voff is at or past the resource's end brings zeros.  M0 holds the LDS address; nothing else in
+// these kernels uses it, and a wait state lies between its write and its use.
 __device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-    uint32_t saved;
     asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %4\n\t"
+        "s_mov_b32 m0, %3\n\t"
         "s_nop 0\n\t"
-        "buffer_load_dwordx4 %1, %2, %3 offen lds\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
+        "buffer_load_dwordx4 %0, %1, %2 offen lds"
+        :
         : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(soff)), "s"(__builtin_amdgcn_readfirstlane(lds))
         : "memory");
 }
 __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-    uint32_t saved;
     asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %4\n\t"
+        "s_mov_b32 m0, %3\n\t"
         "s_nop 0\n\t"
-        "buffer_load_dword %1, %2, %3 offen lds\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
+        "buffer_load_dword %0, %1, %2 offen lds"
+        :
         : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(soff)), "s"(__builtin_amdgcn_readfirstlane(lds))
         : "memory");
 }
+// The next 1 KB after the last dma16, from voff + step + soff.
+__device__ __forceinline__ void dma16_next(i32x4 rsrc, uint32_t voff, uint32_t step, uint32_t soff) {
+    uint32_t off;
+    asm volatile(
+        "s_add_u32 m0, m0, 0x400\n\t"
+        "v_add_u32 %0, %3, %1\n\t"
+        "buffer_load_dwordx4 %0, %2, %4 offen lds"
+        : "=&v"(off)
+        : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(step)), "s"(__builtin_amdgcn_readfirstlane(soff))
+        : "memory", "scc");
+}
+
 // The results of four 16-column fragments for 16 rows (lane (i, g): row i, columns 16j + 4g .. + 3 of
 // fragment j) as bf16, rearranged so that lane (i, g) holds columns 16g .. 16g + 15 of row i: a 4 x 4
 // transposition between fragments and lane groups.
@@ -343,15 +350,16 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     const uint32_t mis = (uint32_t)((uintptr_t)s0 & 3);           // read whole aligned words
     const i32x4 sr = byte_rsrc(s0 - mis, ((uint32_t)rows * srow + mis + 3) / 4 * 4);
 
-    // This lane's piece of the wavefront's first activation unit (the next one is kWaves units further
-    // down, with the same piece), and the piece's first channel within a chunk.  Rows past `rows` and
-    // column tiles past `cts` lie outside the resources: zeros.
+    // A wavefront's units lie together in a stage: kXu of activations, kWu of weights.  This lane's piece of
+    // its first activation unit (the next one is the next rows, with the same piece), and the piece's first
+    // channel within a chunk.  Rows past `rows` and column tiles past `cts` lie outside the resources: zeros.
     constexpr int kUnitRows = BITS == 8 ? 8 : 16, kPieces = BITS == 8 ? 8 : 4;
-    const int ur = wave * kUnitRows + lane / kPieces;
+    const int ur = wave * S::kXu * kUnitRows + lane / kPieces;
     const int us = lane % kPieces;               // slot of the row
     const int up = BITS == 8 ? ((us >> 1) ^ ((ur >> 1) & 3)) + 4 * (us & 1) : us ^ ((ur >> 2) & 3);
-    const uint32_t xoff = (uint32_t)ur * xrow + 16 * up, xstep = S::kWaves * kUnitRows * xrow;
+    const uint32_t xoff = (uint32_t)ur * xrow + 16 * up, xstep = kUnitRows * xrow;
     const int xk = up * (BITS == 8 ? 16 : 32);
+    constexpr uint32_t kOwn = (S::kXu + S::kWu) * 1024;
     const uint32_t woff = wave * 1024 + lane * 16;               // block `wave` of the chunk; one column tile per unit
     const uint32_t foff = wave * ftile + lane * 4;               // one column tile per wavefront
     // activation scales: 64 rows per wavefront (the same rows by several where the tile has fewer)
@@ -372,26 +380,29 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
         if (k == S::kData - 1) return plane_op(c + 1, slot);
         const int left = c < ce ? Kc - c * kMxChunk : 0;
         const uint32_t cc = (uint32_t)(c < chunks ? c : chunks - 1), st = stage * S::kStage;
-        const bool in_x = k > 0 && k <= S::kXu;
-        const int u = in_x ? k - 1 : k - 1 - S::kXu;
-        const uint32_t unit = k == 0 ? (S::kXk + S::kWk) * 1024 + wave * 256
-                                     : ((in_x ? 0 : S::kXk) + u * S::kWaves + wave) * 1024;
+        const uint32_t unit = k == 0 ? (S::kXk + S::kWk) * 1024 + wave * 256 : wave * kOwn + (k - 1) * 1024;
         if constexpr (kLdsPoison) {              // debug build: NaN where this transfer will land
             if (k == 0) ((uint32_t*)lds)[(st + unit) / 4 + lane] = kLdsNan;
             else lds[(st + unit) / 16 + lane] = lds_nan16();
             lds_write_fence();
         }
+        const uint32_t vx = xk < left ? xoff : kOutside, vw = left > 0 ? woff : kOutside;
+        const uint32_t sx = cc * (BITS == 8 ? 128 : 64);
         if (k == 0) dma4(fr, left > 0 ? foff : kOutside, cc * 256, base + st + unit);
-        else if (in_x) dma16(xr, xk < left ? xoff + u * xstep : kOutside, cc * (BITS == 8 ? 128 : 64), base + st + unit);
-        else dma16(wr, left > 0 ? woff + u * wtile : kOutside, cc * 4096, base + st + unit);
+        else if (k == 1) dma16(xr, vx, sx, base + st + unit);
+        else if (k <= S::kXu) dma16_next(xr, vx, (k - 1) * xstep, sx);
+        else dma16_next(wr, vw, (k - 1 - S::kXu) * wtile, cc * 4096);
     };
 
     // LDS byte offsets of this lane's operands within a stage, and of its scale byte of each row fragment
     // within the chunk's words or the next chunk's
-    const uint32_t xl = BITS == 8
-        ? (2 * wm * RF + (i >> 3)) * 1024 + (i & 7) * 128 + ((g ^ ((i >> 1) & 3)) * 32)
-        : wm * RF * 1024 + i * 64 + ((g ^ ((i >> 2) & 3)) * 16);
-    const uint32_t wl = S::kXk * 1024 + g * 1024 + i * 16, fl = (S::kXk + S::kWk) * 1024 + g * 64 + i * 4;
+    constexpr int kFragUnits = BITS == 8 ? 2 : 1;                 // units of a row fragment
+    auto unit_at = [](int e) { return (uint32_t)(e / S::kXu) * kOwn + (uint32_t)(e % S::kXu) * 1024; };
+    static_assert(RF * kFragUnits % S::kXu == 0, "a wavefront's rows are whole wavefronts' units");
+    const uint32_t xl = unit_at(wm * RF * kFragUnits) +
+                        (BITS == 8 ? (i >> 3) * 1024 + (i & 7) * 128 + ((g ^ ((i >> 1) & 3)) * 32)
+                                   : i * 64 + ((g ^ ((i >> 2) & 3)) * 16));
+    const uint32_t wl = g * kOwn + S::kXu * 1024 + i * 16, fl = (S::kXk + S::kWk) * 1024 + g * 64 + i * 4;
     uint32_t sa[RF];
     bool later[RF];
 #pragma unroll
@@ -424,16 +435,16 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
         if (k % 2 == 1) {
             a.e[rf] = lb[sa[rf] + (uint32_t)(later[rf] ? ST * S::kStage + slot1 * S::kPlane : ST * S::kStage + slot * S::kPlane)];
         } else if constexpr (BITS == 8) {        // 32 contiguous bytes
-            a.x[rf] = *(const i32x8_a16*)(lb + stage * S::kStage + xl + rf * 2048);
+            a.x[rf] = *(const i32x8_a16*)(lb + stage * S::kStage + xl + unit_at(2 * rf));
         } else {
-            a.x[rf] = *(const u32x4*)(lb + stage * S::kStage + xl + rf * 1024);
+            a.x[rf] = *(const u32x4*)(lb + stage * S::kStage + xl + unit_at(rf));
         }
     };
     auto fetch_w_op = [&](int stage, int half, int k, Half& h) __attribute__((always_inline)) {
         const int j = wn * CF + half * H + (k > 0 ? k - 1 : 0);   // fragment among the tile's 16
         const uint8_t* l = lb + stage * S::kStage;
         if (k == 0) h.e = *(const uint32_t*)(l + fl + j / 4 * 256);
-        else h.w[k - 1] = *(const u32x4*)(l + wl + j / 4 * 4096 + j % 4 * 256);
+        else h.w[k - 1] = *(const u32x4*)(l + wl + j / 4 * 1024 + j % 4 * 256);
     };
     auto product = [&](const Acts& a, const uint32_t (&e)[RF], const Half& h, int half, int n) __attribute__((always_inline)) {
         const int q = n / RF, rf = n % RF, j = half * H + q;
