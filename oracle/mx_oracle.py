@@ -88,9 +88,10 @@ def weights_layout(c: np.ndarray, E: np.ndarray):
     nt, kb = -(-N // 64), -(-K // 128) * 4
     codes, scales = np.zeros((nt, kb, 64, 16), np.uint8), np.zeros((nt, kb, 64), np.uint8)
     by_column = pair(c.T.copy()).reshape(N, K // BLOCK, 16)
-    for n in range(N):
-        codes[n // 64, :K // BLOCK, n % 64] = by_column[n]
-        scales[n // 64, :K // BLOCK, scale_position(n % 64)] = E[:, n]
+    n = np.arange(N)
+    codes[n // 64, :K // BLOCK, n % 64] = by_column
+    position = np.array([scale_position(v) for v in range(64)])
+    scales[n // 64, :K // BLOCK, position[n % 64]] = E.T
     return codes, scales
 
 

@@ -67,18 +67,19 @@ def product_bound(x, w, y, bits):
     lies in another group).  2^e is at most the largest product of the group, so eight cuts lose less than
     8 2^-13 of it, and all groups together less than 2^-10 S.  e2m1 products are multiples of 1/4 below
     2^6, so nothing of them is cut off."""
-    K, S = x.shape[1], np.abs(x) @ np.abs(w)
-    return 2.0 ** -8 * np.abs(y) + ((K / 32 + 64) * 2.0 ** -23 + (2.0 ** -10 if bits == 8 else 0)) * S + 2.0 ** -126
+    S = x.abs() @ w.abs()
+    return 2.0 ** -8 * y.abs() + ((x.shape[1] / 32 + 64) * 2.0 ** -23 + (2.0 ** -10 if bits == 8 else 0)) * S + 2.0 ** -126
 
 
 def check_product(Y, x, w, bits, label):
-    y = x @ w
-    got = f32(Y).astype(np.float64)
-    nan = np.isnan(y)
-    assert np.array_equal(np.isnan(got), nan), (label, int(np.isnan(got).sum()), int(nan.sum()))
-    x, w, y = np.nan_to_num(x), np.nan_to_num(w), np.where(nan, 0, y)
-    bad = ~nan & ~(np.abs(got - y) <= product_bound(x, w, y, bits))
-    assert not bad.any(), (label, int(bad.sum()), np.argwhere(bad)[:4], got[bad][:4], y[bad][:4])
+    """Y against the product of the float64 values x [M, K] and w [K, N] (numpy), computed in float64."""
+    x, w = torch.from_numpy(x).to(Y.device), torch.from_numpy(w).to(Y.device)
+    y, got = x @ w, Y.double()
+    nan = torch.isnan(y)
+    assert torch.equal(torch.isnan(got), nan), (label, int(torch.isnan(got).sum()), int(nan.sum()))
+    x, w, y = (torch.nan_to_num(v, nan=0.0) for v in (x, w, y))
+    bad = ~nan & ~((got - y).abs() <= product_bound(x, w, y, bits))
+    assert not bad.any(), (label, int(bad.sum()), bad.nonzero()[:4].tolist(), got[bad][:4].tolist(), y[bad][:4].tolist())
 
 
 def act_buffers(M, K, bits):

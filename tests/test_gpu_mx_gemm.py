@@ -23,8 +23,36 @@ def test_product(M, K, N, bits):
     check_product(product(xc, xs, wc, wsc, M, K, N), x, w, bits, (M, K, N, bits))
 
 
+# 128- and 256-row tiles, with and without a split of K, scales that start on a 4-byte boundary (K a multiple
+# of 128) and that do not, an odd number of 128-channel chunks, ragged rows and columns
+LARGE = [(2459, 224, 1568), (2390, 640, 1560), (1800, 608, 4432), (1576, 384, 6776), (340, 4960, 5560),
+         (388, 5760, 4976), (1659, 7648, 2440), (2345, 8576, 1552), (111, 4288, 16), (84, 4352, 16), (27, 6656, 8)]
+
+
 @pytest.mark.parametrize("bits", [8, 4])
-@pytest.mark.parametrize("M,K,N", [(1, 4096, 512), (5, 1024, 192), (40, 1120, 256), (300, 512, 520), (600, 1024, 776)])
+@pytest.mark.parametrize("M,K,N", LARGE)
+def test_product_in_large_tiles(M, K, N, bits):
+    xc, xs, x = random_acts(M, K, bits, M + K + N)
+    wc, wsc, w = random_weights(K, N, M + K + N + 1)
+    check_product(product(xc, xs, wc, wsc, M, K, N), x, w, bits, (M, K, N, bits))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("offset", [1, 2, 3])
+@pytest.mark.parametrize("M,K,N", [(5, 256, 64), (70, 512, 128), (1600, 384, 6776)])
+def test_scales_at_any_address(M, K, N, bits, offset):
+    """Scales of the activations that start 1 to 3 bytes past a 4-byte boundary: the same bits."""
+    xc, xs, _ = random_acts(M, K, bits, 1)
+    wc, wsc, _ = random_weights(K, N, 2)
+    room = torch.full((xs.numel() + 8,), 0xFF, dtype=torch.uint8, device=DEV)
+    moved = room[offset:offset + xs.numel()].view(M, -1)
+    moved.copy_(xs)
+    a, b = product(xc, xs, wc, wsc, M, K, N), product(xc, moved, wc, wsc, M, K, N)
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 512), (5, 1024, 192), (40, 1120, 256), (300, 512, 520), (600, 1024, 776), (1800, 512, 4440), (2390, 160, 1560)])
 def test_integers_are_exact(M, K, N, bits):
     """Elements that are small integers under scales of 1: every partial sum is a float32 integer, so the
     product is the bf16 rounding of the exact one, whatever the order of its sums."""
@@ -40,7 +68,7 @@ def test_integers_are_exact(M, K, N, bits):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
-@pytest.mark.parametrize("M,K,N", [(1, 256, 128), (6, 1024, 72), (100, 384, 264), (400, 512, 520)])
+@pytest.mark.parametrize("M,K,N", [(1, 256, 128), (6, 1024, 72), (100, 384, 264), (400, 512, 520), (1800, 544, 4432), (2390, 160, 1560)])
 def test_one_element_at_a_time(M, K, N, bits):
     """Each row of x has one nonzero element, with its block's own scale: row m of Y is one row of W times a
     power of two, exactly.  A block or a scale taken from another place shows."""
@@ -58,7 +86,7 @@ def test_one_element_at_a_time(M, K, N, bits):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
-@pytest.mark.parametrize("M,K,N", [(1, 1024, 128), (20, 256, 64), (300, 640, 264)])
+@pytest.mark.parametrize("M,K,N", [(1, 1024, 128), (20, 256, 64), (300, 640, 264), (1800, 608, 4432), (2390, 160, 1560)])
 def test_nan_blocks_and_extreme_scales(M, K, N, bits):
     xc, xs, _ = random_acts(M, K, bits, 1)
     wc, wsc, _ = random_weights(K, N, 2)
@@ -78,7 +106,7 @@ def test_nan_blocks_and_extreme_scales(M, K, N, bits):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
-@pytest.mark.parametrize("M,K,N", [(1, 1024, 136), (9, 96, 72), (70, 128, 200), (300, 512, 264)])
+@pytest.mark.parametrize("M,K,N", [(1, 1024, 136), (9, 96, 72), (70, 128, 200), (300, 512, 264), (130, 96, 72), (1800, 608, 4432), (2459, 160, 1568)])
 def test_nothing_else_is_written_or_read(M, K, N, bits):
     """Y lies between guard rows; the activations are followed by NaN codes and NaN scales, which no row
     may see (K = 96 ends inside a 128-channel chunk)."""
@@ -103,7 +131,8 @@ def test_nothing_else_is_written_or_read(M, K, N, bits):
 @pytest.mark.parametrize("bits", [8, 4])
 def test_repeated_calls_agree_on_one_workspace(bits):
     """One workspace for every shape in turn, three rounds: equal bits each time, counters left at zero."""
-    shapes = [(1, 8192, 1024), (13, 4096, 520), (64, 2048, 256), (300, 1024, 776), (1, 1024, 64), (129, 4096, 264)]
+    shapes = [(1, 8192, 1024), (13, 4096, 520), (64, 2048, 256), (300, 1024, 776), (1, 1024, 64), (129, 4096, 264),
+              (340, 4960, 5560), (30, 2240, 8), (1800, 608, 4432)]
     ops = [(random_acts(M, K, bits, i)[:2], random_weights(K, N, i)[:2]) for i, (M, K, N) in enumerate(shapes)]
     ws = A.workspace(max(A.awq_mx_gemm_workspace_size(*s, bits) for s in shapes), DEV)
     first = None

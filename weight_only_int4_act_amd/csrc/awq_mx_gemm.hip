@@ -192,9 +192,11 @@ __global__ __launch_bounds__(64 * NW) void k_mx_gemm_rows(
 //                piece g at 16-byte slot g ^ (row/4 % 4).  So a transfer reads whole lines, and lanes
 //                reading the same piece of eight rows hit different banks;
 //   weights      the packed order: 1 KB per block of 64 columns, read 256 contiguous bytes at a time;
-//   scales       weights: 64 bytes per block and 64 columns; activations: one 4-byte word per row and
-//                chunk, from the 4-byte boundary at or before the chunk's bytes, in a ring of their own: a
-//                row whose scales do not start on a boundary takes bytes from the next chunk's word, too.
+//   scales       of four chunks at a time, two such groups deep: weights 1 KB per column tile;
+//                activations 16 bytes per row, from the 4-byte boundary at or before the group's first
+//                byte (ALIGNED: at it), so that a row whose scales do not start on a boundary takes the
+//                last bytes of a group's fourth chunk from the next group.  Chunk by chunk the gather of
+//                4 bytes a row took a fifth of the transfers' time.
 // Every transfer is issued from inline asm and waited for with counted vmcnt waits (transfers of a
 // wavefront complete in order).  A turn multiplies one chunk in two halves of CF/2 column fragments,
 // each product followed by its share of everything else, because a wavefront issues in order and a
@@ -209,23 +211,14 @@ __device__ __forceinline__ i32x4 byte_rsrc(const void* base, uint32_t bytes) {
                  (int)(__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)) & 0xffff),
                  (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000};
 }
-// 16 (4) bytes per lane from byte voff + soff of the resource to LDS address lds + 16 (4) * lane; a lane
-// whose voff is at or past the resource's end brings zeros.  M0 holds the LDS address; nothing else in
+// 16 bytes per lane from byte voff + soff of the resource to LDS address lds + 16 * lane; a lane whose
+// voff is at or past the resource's end brings zeros.  M0 holds the LDS address; nothing else in
 // these kernels uses it, and a wait state lies between its write and its use.
 __device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
     asm volatile(
         "s_mov_b32 m0, %3\n\t"
         "s_nop 0\n\t"
         "buffer_load_dwordx4 %0, %1, %2 offen lds"
-        :
-        : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(soff)), "s"(__builtin_amdgcn_readfirstlane(lds))
-        : "memory");
-}
-__device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-    asm volatile(
-        "s_mov_b32 m0, %3\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dword %0, %1, %2 offen lds"
         :
         : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(soff)), "s"(__builtin_amdgcn_readfirstlane(lds))
         : "memory");
@@ -304,16 +297,16 @@ struct TileShape {
     static constexpr int kXk = kRows * BITS / 64;                 // 1 KB units of activations per chunk
     static constexpr int kWk = kCols / 64 * 4;                    // 1 KB units of weights per chunk
     static constexpr int kXu = kXk / kWaves, kWu = kWk / kWaves;  // per wavefront
-    static constexpr int kData = kXu + kWu + 2;                   // and a share of the scales
+    static constexpr int kData = kXu + kWu;
     static_assert(kXk % kWaves == 0 && kWk % kWaves == 0 && kWaves == 4, "even shares");
-    static constexpr int kStage = (kXk + kWk + 1) * 1024;         // with 1 KB of weight scales
-    static constexpr int kRing = ST + 1, kPlane = kRows * 4;      // words of activation scales
-    static constexpr int kLds = ST * kStage + kRing * kPlane;
+    static constexpr int kStage = (kXk + kWk) * 1024;
+    static constexpr int kFs = 4096, kXs = kRows * 16;            // scales of a group: weights, activations
+    static constexpr int kScales = ST * kStage, kLds = kScales + 2 * (kFs + kXs);
     static_assert(kLds <= 160 * 1024, "LDS of a CU");
-    static_assert(ST >= 3 && (ST - 1) * kData + 1 < 64, "counted waits");
+    static_assert(ST >= 3 && ST <= 5 && (ST - 1) * kData + 4 < 64, "counted waits; a group is requested 3 turns early");
 };
 
-template <int BITS, int WM, int WN, int RF, int CF, int ST>
+template <int BITS, int WM, int WN, int RF, int CF, int ST, bool ALIGNED>
 __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     const uint8_t* __restrict__ xcodes, const uint8_t* __restrict__ xscales, int64_t M,
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t K, int64_t N, int64_t kb_all,
@@ -361,55 +354,52 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     const int xk = up * (BITS == 8 ? 16 : 32);
     constexpr uint32_t kOwn = (S::kXu + S::kWu) * 1024;
     const uint32_t woff = wave * 1024 + lane * 16;               // block `wave` of the chunk; one column tile per unit
-    const uint32_t foff = wave * ftile + lane * 4;               // one column tile per wavefront
-    // activation scales: 64 rows per wavefront (the same rows by several where the tile has fewer)
+    // The scales of chunks 4q .. 4q+3: one column tile, and 64 rows (the same rows by several wavefronts
+    // where the tile has fewer), per wavefront.  Past K: whatever lies there, or zeros; not used.
     constexpr int kParts = S::kRows / 64;
     const int part64 = wave % kParts;
+    const uint32_t foff = wave * ftile + lane * 16;
     const uint32_t soff = ((uint32_t)(part64 * 64 + lane) * srow + mis) & ~3u;
-    auto plane_op = [&](int c, int slot) __attribute__((always_inline)) {
-        const uint32_t dst = ST * S::kStage + slot * S::kPlane + part64 * 256;
+    auto issue_scales = [&](int q) __attribute__((always_inline)) {
+        const uint32_t f = S::kScales + (q & 1) * S::kFs + wave * 1024, x = S::kScales + 2 * S::kFs + (q & 1) * S::kXs + part64 * 1024;
         if constexpr (kLdsPoison) {              // debug build: scales of about 2^120 where these will land
-            ((uint32_t*)lds)[dst / 4 + lane] = kLdsNan;
+            lds[f / 16 + lane] = lds_nan16();
+            lds[x / 16 + lane] = lds_nan16();
             lds_write_fence();
         }
-        dma4(sr, 4 * c < (int)srow + 4 ? soff + 4 * c : kOutside, 0, base + dst);
+        dma16(fr, foff + q * 1024, 0, base + f);
+        dma16(sr, soff + q * 16, 0, base + x);
     };
-    // transfer k of chunk c's batch (the activation scales are the next chunk's); a chunk past the slice
-    // brings zeros (no traffic), so that the counted waits stay the same
-    auto issue_op = [&](int c, int stage, int slot, int k) __attribute__((always_inline)) {
-        if (k == S::kData - 1) return plane_op(c + 1, slot);
+    // transfer k of chunk c's batch; a chunk past the slice brings zeros (no traffic), so that the counted
+    // waits stay the same
+    auto issue_op = [&](int c, int stage, int k) __attribute__((always_inline)) {
         const int left = c < ce ? Kc - c * kMxChunk : 0;
-        const uint32_t cc = (uint32_t)(c < chunks ? c : chunks - 1), st = stage * S::kStage;
-        const uint32_t unit = k == 0 ? (S::kXk + S::kWk) * 1024 + wave * 256 : wave * kOwn + (k - 1) * 1024;
+        const uint32_t cc = (uint32_t)(c < chunks ? c : chunks - 1), st = stage * S::kStage + wave * kOwn;
         if constexpr (kLdsPoison) {              // debug build: NaN where this transfer will land
-            if (k == 0) ((uint32_t*)lds)[(st + unit) / 4 + lane] = kLdsNan;
-            else lds[(st + unit) / 16 + lane] = lds_nan16();
+            lds[st / 16 + k * 64 + lane] = lds_nan16();
             lds_write_fence();
         }
         const uint32_t vx = xk < left ? xoff : kOutside, vw = left > 0 ? woff : kOutside;
         const uint32_t sx = cc * (BITS == 8 ? 128 : 64);
-        if (k == 0) dma4(fr, left > 0 ? foff : kOutside, cc * 256, base + st + unit);
-        else if (k == 1) dma16(xr, vx, sx, base + st + unit);
-        else if (k <= S::kXu) dma16_next(xr, vx, (k - 1) * xstep, sx);
-        else dma16_next(wr, vw, (k - 1 - S::kXu) * wtile, cc * 4096);
+        if (k == 0) dma16(xr, vx, sx, base + st);
+        else if (k < S::kXu) dma16_next(xr, vx, k * xstep, sx);
+        else dma16_next(wr, vw, (k - S::kXu) * wtile, cc * 4096);
     };
 
-    // LDS byte offsets of this lane's operands within a stage, and of its scale byte of each row fragment
-    // within the chunk's words or the next chunk's
+    // LDS byte offsets of this lane's operands within a stage; of its weight scales and of its scale byte of
+    // each row fragment within a group
     constexpr int kFragUnits = BITS == 8 ? 2 : 1;                 // units of a row fragment
     auto unit_at = [](int e) { return (uint32_t)(e / S::kXu) * kOwn + (uint32_t)(e % S::kXu) * 1024; };
     static_assert(RF * kFragUnits % S::kXu == 0, "a wavefront's rows are whole wavefronts' units");
     const uint32_t xl = unit_at(wm * RF * kFragUnits) +
                         (BITS == 8 ? (i >> 3) * 1024 + (i & 7) * 128 + ((g ^ ((i >> 1) & 3)) * 32)
                                    : i * 64 + ((g ^ ((i >> 2) & 3)) * 16));
-    const uint32_t wl = g * kOwn + S::kXu * 1024 + i * 16, fl = (S::kXk + S::kWk) * 1024 + g * 64 + i * 4;
-    uint32_t sa[RF];
-    bool later[RF];
+    const uint32_t wl = g * kOwn + S::kXu * 1024 + i * 16, fl = g * 64 + i * 4;
+    uint32_t sl[ALIGNED ? 1 : RF];
 #pragma unroll
-    for (int rf = 0; rf < RF; ++rf) {
-        const int r = (wm * RF + rf) * 16 + i, b = (int)(((uint32_t)r * srow + mis) & 3) + g;
-        sa[rf] = r * 4 + (b & 3);
-        later[rf] = b >= 4;
+    for (int rf = 0; rf < (ALIGNED ? 1 : RF); ++rf) {
+        const int r = (wm * RF + rf) * 16 + i;
+        sl[rf] = r * 16 + (ALIGNED ? 0 : (((uint32_t)r * srow + mis) & 3)) + g;
     }
 
     floatx4 acc[RF][CF];
@@ -429,22 +419,27 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     };
     constexpr int H = CF / 2, kFetchX = RF * 2, kFetchW = H + 1, kMul = RF * H;
     const uint8_t* const lb = (const uint8_t*)lds;
-    // LDS reads, one at a time: activations (slots: of the chunk's scales and the next chunk's)
-    auto fetch_x_op = [&](int stage, int slot, int slot1, int k, Acts& a) __attribute__((always_inline)) {
+    // LDS reads of chunk c, one at a time
+    auto fetch_x_op = [&](int c, int stage, int k, Acts& a) __attribute__((always_inline)) {
         const int rf = k / 2;
         if (k % 2 == 1) {
-            a.e[rf] = lb[sa[rf] + (uint32_t)(later[rf] ? ST * S::kStage + slot1 * S::kPlane : ST * S::kStage + slot * S::kPlane)];
+            const uint32_t q = c >> 2, in = 4 * (c & 3), xs = S::kScales + 2 * S::kFs;
+            if constexpr (ALIGNED) {
+                a.e[rf] = lb[xs + (q & 1) * S::kXs + in + sl[0] + rf * 256];
+            } else {                             // 16 bytes a row; past them the next group's first ones
+                const uint32_t b = (sl[rf] & 15) + in;
+                a.e[rf] = lb[xs + (b >= 16 ? (~q & 1) * S::kXs - 16 : (q & 1) * S::kXs) + sl[rf] + in];
+            }
         } else if constexpr (BITS == 8) {        // 32 contiguous bytes
             a.x[rf] = *(const i32x8_a16*)(lb + stage * S::kStage + xl + unit_at(2 * rf));
         } else {
             a.x[rf] = *(const u32x4*)(lb + stage * S::kStage + xl + unit_at(rf));
         }
     };
-    auto fetch_w_op = [&](int stage, int half, int k, Half& h) __attribute__((always_inline)) {
+    auto fetch_w_op = [&](int c, int stage, int half, int k, Half& h) __attribute__((always_inline)) {
         const int j = wn * CF + half * H + (k > 0 ? k - 1 : 0);   // fragment among the tile's 16
-        const uint8_t* l = lb + stage * S::kStage;
-        if (k == 0) h.e = *(const uint32_t*)(l + fl + j / 4 * 256);
-        else h.w[k - 1] = *(const u32x4*)(l + wl + j / 4 * 1024 + j % 4 * 256);
+        if (k == 0) h.e = *(const uint32_t*)(lb + S::kScales + ((c >> 2) & 1) * S::kFs + (c & 3) * 256 + fl + j / 4 * 1024);
+        else h.w[k - 1] = *(const u32x4*)(lb + stage * S::kStage + wl + j / 4 * 1024 + j % 4 * 256);
     };
     auto product = [&](const Acts& a, const uint32_t (&e)[RF], const Half& h, int half, int n) __attribute__((always_inline)) {
         const int q = n / RF, rf = n % RF, j = half * H + q;
@@ -454,31 +449,35 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
         if (j % 4 == 3) mx_mfma_acc<BITS, 3>(acc[rf][j], h.w[q], a.x[rf], h.e, e[rf]);
     };
 
-    plane_op(cb, 0);
+    issue_scales(cb >> 2);
+    issue_scales((cb >> 2) + 1);
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s)
 #pragma unroll
-        for (int k = 0; k < S::kData; ++k) issue_op(cb + s, s, s + 1, k);
+        for (int k = 0; k < S::kData; ++k) issue_op(cb + s, s, k);
     Acts xa, xb;
     Half lo, hi;
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((ST - 2) * S::kData) : "memory");
 #pragma unroll
-    for (int k = 0; k < kFetchX; ++k) fetch_x_op(0, 0, 1, k, xa);
+    for (int k = 0; k < kFetchX; ++k) fetch_x_op(cb, 0, k, xa);
 #pragma unroll
-    for (int k = 0; k < kFetchW; ++k) fetch_w_op(0, 0, k, lo);
-    // of chunk c; the ring slot after it holds the next chunk's scales, the one before it is refilled
-    int stage = 0, slot = 0;
+    for (int k = 0; k < kFetchW; ++k) fetch_w_op(cb, 0, 0, k, lo);
+    int stage = 0;                               // of chunk c
     auto turn = [&](int c, const Acts& now, Acts& next) __attribute__((always_inline)) {
         const int behind = stage == 0 ? ST - 1 : stage - 1, ahead = stage == ST - 1 ? 0 : stage + 1;
-        const int slot_behind = slot == 0 ? S::kRing - 1 : slot - 1, slot1 = slot == S::kRing - 1 ? 0 : slot + 1;
-        const int slot2 = slot1 == S::kRing - 1 ? 0 : slot1 + 1;
-        const bool inside = 4 * c + g < (int)srow;                // past K: elements are zero, the scale 1
+        // Group c/4 + 1 takes the place of group c/4 - 1, whose last bytes were in registers before the last
+        // barrier.  Before the batch's kData transfers, so that the counted waits cover it.
+        if ((c & 3) == 0) issue_scales((c >> 2) + 1);
+        // past K: elements are zero, the scales 1 (what was read for them may say NaN)
+        const bool inside = 4 * c + g < (int)srow;
         uint32_t e[RF];
 #pragma unroll
         for (int rf = 0; rf < RF; ++rf) {
             e[rf] = inside ? now.e[rf] : 127u;
             asm volatile("" : "+v"(e[rf]));      // in registers here, not next to their use
         }
+        lo.e = c < chunks ? lo.e : 0x7f7f7f7fu;
+        asm volatile("" : "+v"(lo.e));
         asm volatile("s_nop 1");
         constexpr int ops1 = kFetchW + S::kData;
 #pragma unroll
@@ -487,13 +486,16 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
 #pragma unroll
             for (int k = 0; k < ops1; ++k) {
                 if (k * kMul / ops1 != n) continue;
-                if (k < kFetchW) fetch_w_op(stage, 1, k, hi);
-                else issue_op(c + ST - 1, behind, slot_behind, k - kFetchW);
+                if (k < kFetchW) fetch_w_op(c, stage, 1, k, hi);
+                else issue_op(c + ST - 1, behind, k - kFetchW);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((ST - 2) * S::kData) : "memory");
         __builtin_amdgcn_sched_barrier(0);
+        hi.e = c < chunks ? hi.e : 0x7f7f7f7fu;
+        asm volatile("" : "+v"(hi.e));
+        asm volatile("s_nop 1");
         constexpr int ops2 = kFetchW + kFetchX;
 #pragma unroll
         for (int n = 0; n < kMul; ++n) {
@@ -501,13 +503,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
 #pragma unroll
             for (int k = 0; k < ops2; ++k) {
                 if (k * kMul / ops2 != n) continue;
-                if (k < kFetchW) fetch_w_op(ahead, 0, k, lo);
-                else fetch_x_op(ahead, slot1, slot2, k - kFetchW, next);
+                if (k < kFetchW) fetch_w_op(c + 1, ahead, 0, k, lo);
+                else fetch_x_op(c + 1, ahead, k - kFetchW, next);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
         stage = ahead;
-        slot = slot1;
     };
     // Two turns at a time: slices are multiples of two chunks, and past K a turn adds zeros.  (Leaving the
     // loop between turns made the compiler copy the accumulators.)
@@ -593,14 +594,13 @@ constexpr int kCus = kNumXcd * kCusPerXcd;
 constexpr int kMaxSlices = 16;
 
 // Which kernel, and how many slices of K, by the time that each would take: us on this card, fitted to
-// measured launches (K = 4096 .. 28672, N = 1024 .. 28672, 8-bit activations; 4-bit ones differ by a common
-// factor in the tiles).
+// measured launches (K = 4096 .. 28672, N = 1024 .. 28672):
 //   register kernel, R fragments of 16 rows: 4 + (64-column chunks per CU) * {.19, .23, .30, .42}[R - 1];
-//     e.g. 64 rows, K = N = 8192: 18.2 us (tiles 22), 64 rows, N = 28672: 51 us (tiles 37);
-//   tiles of 64 wm rows: 4.5 + turns * {.52, .80, 1.57} per round of one workgroup per CU (64-row
-//     tiles: up to two per CU, .84), and 2 + 1.15 wm nz for joining nz slices; not below the time in
-//     which these kernels stream the weights (4 TB/s).  E.g. 257 x 5120 x 13824: 33.6 us with 128
-//     rows a tile, 38 with 64, 66 with 256; 4096 rows: 256-row tiles.
+//     e.g. 64 rows, K = N = 8192: 18 us (tiles 20), 64 rows, N = 28672: 51 us (tiles 33);
+//   tiles of 64 wm rows: 4.5 + turns * turn_us per round of one workgroup per CU, and 2 + 1.15 wm nz for
+//     joining nz slices; not below the time in which these kernels stream the weights (4 TB/s).  E.g.
+//     257 x 5120 x 13824: 32 us with 128 rows a tile, 44 with 64, 54 with 256; 100 x 8192 x 8192, 64-row
+//     tiles: 33, 24, 21, 21 us with 1, 2, 3, 4 slices.
 MxGemmPlan plan_mx_gemm(int64_t M, int64_t K, int64_t N, int bits) {
     MxGemmPlan p{};
     const int64_t chunks = mx_kb(K) / 4;
@@ -620,17 +620,17 @@ MxGemmPlan plan_mx_gemm(int64_t M, int64_t K, int64_t N, int bits) {
         p.ws_bytes = p.nz > 1 ? kCounterBytes + (size_t)p.col_tiles * p.nz * p.row_tiles * 4096 : 0;
         if (M <= 16) return p;
     }
-    static const double turn_us[3] = {.52, .80, 1.57};
-    const double scale = bits == 8 ? 1. : .72, stream = 4.5 + (double)mx_codes_bytes(K, N) / 4e6;
+    static const double turn_us[2][3] = {{.42, .56, 1.0}, {.48, .72, 1.36}};   // 4 bits, 8 bits
+    const double stream = 4.5 + (double)mx_codes_bytes(K, N) / 4e6;
     for (int k = 0; k < 3; ++k) {
         const int wm = 1 << k;
         const int64_t rt = (M + 64 * wm - 1) / (64 * wm), ct = (N + 255) / 256, tiles = rt * ct;
         for (int nz = 1; nz <= kMaxSlices; ++nz) {
             const int64_t turns = ((chunks + nz - 1) / nz + 1) / 2 * 2, groups = tiles * nz;
-            if (nz > 1 && (turns < 4 || groups > 2 * kCus)) break;
-            const double rounds = wm == 1 && groups > kCus ? (double)((groups + 2 * kCus - 1) / (2 * kCus)) * .84 / .52
-                                                           : (double)((groups + kCus - 1) / kCus);
-            const double us = std::max(stream, 4.5 + scale * rounds * turns * turn_us[k]) + (nz > 1 ? 2 + 1.15 * wm * nz : 0);
+            if (nz > 1 && (turns < 4 || groups > kCus)) break;
+            const double rounds = (double)((groups + kCus - 1) / kCus);
+            const double us = std::max(stream, 4.5 + rounds * turns * turn_us[bits == 8][k]) +
+                              (nz > 1 ? 2 + 1.15 * wm * nz : 0);
             if (us >= best) continue;
             best = us;
             p.wm = wm;
@@ -660,7 +660,8 @@ static hipError_t launch_tile(const uint8_t* xcodes, const uint8_t* xscales, int
                               hipStream_t st) {
     using S = TileShape<BITS, WM, WN, RF, CF, ST>;
     const int64_t total = p.row_tiles * p.col_tiles * p.nz, per_xcd = (total + kNumXcd - 1) / kNumXcd;
-    const auto kernel = k_mx_gemm_tile<BITS, WM, WN, RF, CF, ST>;
+    const bool aligned = K % kMxChunk == 0 && (uintptr_t)xscales % 4 == 0;
+    const auto kernel = aligned ? k_mx_gemm_tile<BITS, WM, WN, RF, CF, ST, true> : k_mx_gemm_tile<BITS, WM, WN, RF, CF, ST, false>;
     // the limit is a property of the function on the current device; setting it again is harmless
     const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
     if (e != hipSuccess) return e;
@@ -684,7 +685,7 @@ hipError_t launch_mx_gemm(const uint8_t* xcodes, const uint8_t* xscales, int bit
     }
     if (p.wm == 4) return run(bits == 8 ? launch_tile<8, 2, 2, 8, 8, 3> : launch_tile<4, 2, 2, 8, 8, 4>);
     if (p.wm == 2) return run(bits == 8 ? launch_tile<8, 2, 2, 4, 8, 4> : launch_tile<4, 2, 2, 4, 8, 4>);
-    return run(bits == 8 ? launch_tile<8, 1, 4, 4, 4, 3> : launch_tile<4, 1, 4, 4, 4, 3>);
+    return run(bits == 8 ? launch_tile<8, 1, 4, 4, 4, 5> : launch_tile<4, 1, 4, 4, 4, 5>);
 }
 
 }  // namespace awq
