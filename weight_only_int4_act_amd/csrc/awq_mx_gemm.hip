@@ -176,9 +176,17 @@ __global__ __launch_bounds__(64 * NW) void k_mx_gemm_rows(
     if (arrival != (uint32_t)(nz - 1)) return;
 #pragma unroll
     for (int q = 0; q < RP; ++q) sum[q] = floatx4{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < nz; ++s)
+    for (int s = 0; s < nz; s += 8) {            // eight slices' loads in flight; past the last: zeros
+        floatx4 v[8][RP];
 #pragma unroll
-        for (int q = 0; q < RP; ++q) sum[q] += load4_agent(pr, poff(s, q));
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+            for (int q = 0; q < RP; ++q) v[u][q] = load4_agent(pr, s + u < nz ? poff(s + u, q) : kOutside);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+            for (int q = 0; q < RP; ++q) sum[q] += v[u][q];
+    }
     write_y();
     if (threadIdx.x == 0) __hip_atomic_store(cnt + tile * cstride, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -310,7 +318,7 @@ template <int BITS, int WM, int WN, int RF, int CF, int ST, bool ALIGNED>
 __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     const uint8_t* __restrict__ xcodes, const uint8_t* __restrict__ xscales, int64_t M,
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t K, int64_t N, int64_t kb_all,
-    uint16_t* __restrict__ Y, float* __restrict__ part, uint32_t* __restrict__ cnt, int row_tiles, int col_tiles,
+    uint16_t* __restrict__ Y, float* __restrict__ part, int row_tiles, int col_tiles,
     int nz, int total, int per_xcd) {
     using S = TileShape<BITS, WM, WN, RF, CF, ST>;
     extern __shared__ u32x4 lds[];
@@ -550,41 +558,48 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
         }
         return;
     }
-    // Split over K: float32 partials in fragment order, one per (tile, K slice), written through to the
-    // device-coherent level; the workgroup that arrives last adds them in slice order.
+    // Split over K: float32 partials in fragment order, one per (tile, K slice), that k_mx_join adds.
     constexpr uint32_t kPart = S::kRows * S::kCols * 4;
     const __amdgpu_buffer_rsrc_t pr = rsrc(part + (int64_t)tile * nz * (kPart / 4), (int64_t)nz * kPart);
-    auto poff = [&](int s, int rf, int j) { return (uint32_t)(s * kPart + ((wave * RF + rf) * CF + j) * 1024 + lane * 16); };
 #pragma unroll
     for (int rf = 0; rf < RF; ++rf) {
         settled(rf);
 #pragma unroll
-        for (int j = 0; j < CF; ++j) store4_agent(pr, poff(z, rf, j), acc[rf][j]);
+        for (int j = 0; j < CF; ++j)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[rf][j]), pr,
+                                                   z * kPart + ((wave * RF + rf) * CF + j) * 1024 + lane * 16, 0, 0);
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wavefront's partial has landed
-    __syncthreads();
-    uint32_t* arrival = (uint32_t*)lds;
-    if (threadIdx.x == 0) *arrival = __hip_atomic_fetch_add(cnt + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (*arrival != (uint32_t)(nz - 1)) return;
-    constexpr int RG = 8 / CF;                   // row fragments at a time: 8 loads in flight (16 were slower)
-#pragma unroll 1
-    for (int r0 = 0; r0 < RF; r0 += RG) {
-        floatx4 sum[RG][CF];
+}
+
+// Adds the slices of the tiles above: a wavefront takes one fragment (stored by wavefront, row fragment, column
+// fragment) of every slice, in slice order, eight loads in flight.  Bound by the partials' bytes, which the
+// caches hold.  A launch of its own, because the last workgroup of a tile alone reads a slice of it in
+// 1.15 WM us: 128 x 4096 x 4096, 3 slices of 64 x 256, 15.5 -> 14.4 us; 99 x 22432 x 832, 8 slices, 23.4 -> 16.9.
+template <int WM, int WN, int RF, int CF>
+__global__ __launch_bounds__(256) void k_mx_join(const float* __restrict__ part, int64_t M, int64_t N, int row_tiles,
+                                                 int col_tiles, int nz, uint16_t* __restrict__ Y) {
+    constexpr int kFrags = WM * WN * RF * CF, kRows = 16 * RF * WM;
+    constexpr uint32_t kPart = kFrags * 1024;
+    const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+    const int f = (blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) % kFrags;
+    const int tile = blockIdx.x * 4 / kFrags;
+    const int panel = tile / (8 * col_tiles), in = tile % (8 * col_tiles), prow = min(8, row_tiles - 8 * panel);
+    const int rt = 8 * panel + in % prow, ct = in / prow;
+    const int wave = f / (RF * CF), rf = f / CF % RF, j = f % CF;
+    const float* p = part + (int64_t)tile * nz * (kPart / 4) + f * 256 + lane * 4;
+    floatx4 sum = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < nz; s += 8) {
+        floatx4 v[8];
 #pragma unroll
-        for (int rf = 0; rf < RG; ++rf)
+        for (int u = 0; u < 8; ++u) v[u] = *(const floatx4*)(p + (int64_t)min(s + u, nz - 1) * (kPart / 4));
 #pragma unroll
-            for (int j = 0; j < CF; ++j) sum[rf][j] = load4_agent(pr, poff(0, r0 + rf, j));
-#pragma unroll 1
-        for (int s = 1; s < nz; ++s)
-#pragma unroll
-            for (int rf = 0; rf < RG; ++rf)
-#pragma unroll
-                for (int j = 0; j < CF; ++j) sum[rf][j] += load4_agent(pr, poff(s, r0 + rf, j));
-#pragma unroll
-        for (int rf = 0; rf < RG; ++rf) write_rows(r0 + rf, sum[rf]);
+        for (int u = 0; u < 8; ++u)
+            if (s + u < nz) sum += v[u];
     }
-    if (threadIdx.x == 0) __hip_atomic_store(cnt + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int64_t m = (int64_t)rt * kRows + (wave / WN * RF + rf) * 16 + i;
+    const int64_t n = (int64_t)ct * 256 + (wave % WN * CF + j) * 16 + 4 * g;
+    if (m < M && n < N)                          // N % 8 == 0: n < N implies n + 3 < N
+        *(uint2*)(Y + m * N + n) = uint2{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
 }
 
 }  // namespace
@@ -597,8 +612,9 @@ constexpr int kMaxSlices = 16;
 // measured launches (K = 4096 .. 28672, N = 1024 .. 28672):
 //   register kernel, R fragments of 16 rows: 4 + (64-column chunks per CU) * {.19, .23, .30, .42}[R - 1];
 //     e.g. 64 rows, K = N = 8192: 18 us (tiles 20), 64 rows, N = 28672: 51 us (tiles 33);
-//   tiles of 64 wm rows: 4.5 + turns * turn_us per round of one workgroup per CU, and 2 + 1.15 wm nz for
-//     joining nz slices; not below the time in which these kernels stream the weights (4 TB/s).  E.g.
+//   tiles of 64 wm rows: 4.5 + turns * turn_us per round of one workgroup per CU, and for
+//     joining slices 2 + .35 per MB of partials; not below the time in which these kernels stream the
+//     weights (4 TB/s).  E.g.
 //     257 x 5120 x 13824: 32 us with 128 rows a tile, 44 with 64, 54 with 256; 100 x 8192 x 8192, 64-row
 //     tiles: 33, 24, 21, 21 us with 1, 2, 3, 4 slices.
 MxGemmPlan plan_mx_gemm(int64_t M, int64_t K, int64_t N, int bits) {
@@ -611,7 +627,7 @@ MxGemmPlan plan_mx_gemm(int64_t M, int64_t K, int64_t N, int bits) {
         p.col_tiles = mx_nt(N);
         p.row_tiles = (M + 15) / 16;             // fragments of the one workgroup row
         // about one workgroup per CU, and chunks enough for every wavefront's loads in flight
-        const int64_t deep = p.row_tiles == 1 ? 16 : 8;
+        const int64_t deep = p.row_tiles == 1 ? 12 : 8;
         p.nz = 1;
         if (p.col_tiles <= (int64_t)(kCounterBytes / 4))
             p.nz = (int)std::max<int64_t>(1, std::min<int64_t>({kCus / p.col_tiles, chunks / deep, kMaxSlices}));
@@ -630,14 +646,13 @@ MxGemmPlan plan_mx_gemm(int64_t M, int64_t K, int64_t N, int bits) {
             if (nz > 1 && (turns < 4 || groups > kCus)) break;
             const double rounds = (double)((groups + kCus - 1) / kCus);
             const double us = std::max(stream, 4.5 + rounds * turns * turn_us[bits == 8][k]) +
-                              (nz > 1 ? 2 + 1.15 * wm * nz : 0);
+                              (nz == 1 ? 0 : 2 + .35e-6 * (double)(groups * 64 * wm * 256 * 4));
             if (us >= best) continue;
             best = us;
             p.wm = wm;
             p.row_tiles = rt;
             p.col_tiles = ct;
             p.nz = nz;
-            p.cstride = 1;
             p.ws_bytes = nz > 1 ? kCounterBytes + (size_t)groups * 64 * wm * 256 * 4 : 0;
         }
     }
@@ -666,8 +681,12 @@ static hipError_t launch_tile(const uint8_t* xcodes, const uint8_t* xscales, int
     const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
     if (e != hipSuccess) return e;
     kernel<<<(unsigned)(per_xcd * kNumXcd), 64 * S::kWaves, S::kLds, st>>>(
-        xcodes, xscales, M, codes, scales, K, N, mx_kb(K), Y, (float*)((char*)ws + kCounterBytes), (uint32_t*)ws,
+        xcodes, xscales, M, codes, scales, K, N, mx_kb(K), Y, (float*)((char*)ws + kCounterBytes),
         (int)p.row_tiles, (int)p.col_tiles, p.nz, (int)total, (int)per_xcd);
+    const hipError_t launched = hipGetLastError();
+    if (launched != hipSuccess || p.nz == 1) return launched;
+    k_mx_join<WM, WN, RF, CF><<<(unsigned)(p.row_tiles * p.col_tiles * (S::kWaves * RF * CF / 4)), 256, 0, st>>>(
+        (const float*)((char*)ws + kCounterBytes), M, N, (int)p.row_tiles, (int)p.col_tiles, p.nz, Y);
     return hipGetLastError();
 }
 

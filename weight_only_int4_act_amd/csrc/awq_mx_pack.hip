@@ -77,18 +77,28 @@ __global__ __launch_bounds__(256) void k_mx_pack(const uint16_t* __restrict__ W,
     const int64_t kb = (int64_t)blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t n0 = ((int64_t)blockIdx.x * 64 + lane) * 4, k0 = kb * kMxBlock;
     const bool in_k = k0 < K;                    // K % 32 == 0: a block is inside or outside as a whole
+    // The last columns of a row are read as the last four and shifted (what lies outside is zero).
+    const int64_t n1 = max((int64_t)0, min(n0, N - 4));
+    const uint32_t past = (uint32_t)min(n0 - n1, (int64_t)4);
     uint2 w[32];
-    if (in_k && n0 + 3 < N) {
+    if (in_k && N >= 4) {
 #pragma unroll
-        for (int r = 0; r < 32; ++r) w[r] = ((const Quad*)(W + (k0 + r) * N + n0))->v;
-    } else {                                     // the last columns, and what lies outside (zeros)
+        for (int r = 0; r < 32; ++r) w[r] = ((const Quad*)(W + (k0 + r) * N + n1))->v;
+        if (__any(past != 0)) {
+#pragma unroll
+            for (int r = 0; r < 32; ++r) {
+                const uint64_t q = past > 3 ? 0 : ((uint64_t)w[r].x | ((uint64_t)w[r].y << 32)) >> (16 * past);
+                w[r] = uint2{(uint32_t)q, (uint32_t)(q >> 32)};
+            }
+        }
+    } else {
 #pragma unroll
         for (int r = 0; r < 32; ++r) {
-            uint32_t v[4] = {0, 0, 0, 0};
+            uint32_t v[3] = {0, 0, 0};           // fewer than four columns
             if (in_k)
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 3; ++c)
                     if (n0 + c < N) v[c] = W[(k0 + r) * N + n0 + c];
-            w[r] = uint2{v[0] | (v[1] << 16), v[2] | (v[3] << 16)};
+            w[r] = uint2{v[0] | (v[1] << 16), v[2]};
         }
     }
     uint32_t top[4] = {0, 0, 0, 0};              // largest |p| of each column, as float32 bits
