@@ -16,7 +16,8 @@ from tests.mx_util import A, bf16, check_product, check_quantized, dev, f32, pro
 
 for bits in (8, 4):
     for M, K, N in ((1, 4096, 256), (13, 2080, 136), (30, 2240, 8), (48, 1024, 264), (64, 224, 1032), (130, 1056, 264),
-                    (300, 4096, 1024), (2390, 640, 1560), (1800, 608, 4432), (1576, 1152, 6776), (340, 4960, 5560)):
+                    (300, 4096, 1024), (2390, 640, 1560), (1800, 608, 4432), (1576, 1152, 6776), (340, 4960, 5560), (70, 4640, 264),
+                    (2390, 1504, 1560)):
         print(f"[poison] product {M} {K} {N} {bits}", flush=True)
         xc, xs, x = random_acts(M, K, bits, M)
         wc, wsc, w = random_weights(K, N, N)

@@ -37,6 +37,20 @@ def test_product_in_large_tiles(M, K, N, bits):
     check_product(product(xc, xs, wc, wsc, M, K, N), x, w, bits, (M, K, N, bits))
 
 
+# K cut into slices, up to sixteen, in the register kernel and in tiles of 64, 128 and 256 rows; slices of four
+# chunks and more, of which the last has one to four; and 128-row tiles of four and twelve chunks
+SPLIT = [(20, 24000, 8), (70, 11008, 264), (70, 11040, 264), (150, 6176, 8), (2000, 16416, 520), (2000, 16512, 520),
+         (2000, 17888, 2056), (2000, 17920, 2056), (2390, 512, 1560), (2390, 1504, 1560)]
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("M,K,N", SPLIT)
+def test_product_in_slices(M, K, N, bits):
+    xc, xs, x = random_acts(M, K, bits, M + K + N)
+    wc, wsc, w = random_weights(K, N, M + K + N + 1)
+    check_product(product(xc, xs, wc, wsc, M, K, N), x, w, bits, (M, K, N, bits))
+
+
 @pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("offset", [1, 2, 3])
 @pytest.mark.parametrize("M,K,N", [(5, 256, 64), (70, 512, 128), (1600, 384, 6776)])

@@ -231,15 +231,14 @@ __device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t voff, uint32_t soff, 
         : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(soff)), "s"(__builtin_amdgcn_readfirstlane(lds))
         : "memory");
 }
-// The next 1 KB after the last dma16, from voff + step + soff.
-__device__ __forceinline__ void dma16_next(i32x4 rsrc, uint32_t voff, uint32_t step, uint32_t soff) {
-    uint32_t off;
+// The same to the next 1 KB after the last dma16.
+__device__ __forceinline__ void dma16_next(i32x4 rsrc, uint32_t voff, uint32_t soff) {
     asm volatile(
         "s_add_u32 m0, m0, 0x400\n\t"
-        "v_add_u32 %0, %3, %1\n\t"
-        "buffer_load_dwordx4 %0, %2, %4 offen lds"
-        : "=&v"(off)
-        : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(step)), "s"(__builtin_amdgcn_readfirstlane(soff))
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %0, %1, %2 offen lds"
+        :
+        : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(soff))
         : "memory", "scc");
 }
 
@@ -311,7 +310,7 @@ struct TileShape {
     static constexpr int kFs = 4096, kXs = kRows * 16;            // scales of a group: weights, activations
     static constexpr int kScales = ST * kStage, kLds = kScales + 2 * (kFs + kXs);
     static_assert(kLds <= 160 * 1024, "LDS of a CU");
-    static_assert(ST >= 3 && ST <= 5 && (ST - 1) * kData + 4 < 64, "counted waits; a group is requested 3 turns early");
+    static_assert((ST == 3 || ST == 4) && (ST - 1) * kData + 4 < 64, "counted waits; a group is requested 3 turns early");
 };
 
 template <int BITS, int WM, int WN, int RF, int CF, int ST, bool ALIGNED>
@@ -358,16 +357,19 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     const int ur = wave * S::kXu * kUnitRows + lane / kPieces;
     const int us = lane % kPieces;               // slot of the row
     const int up = BITS == 8 ? ((us >> 1) ^ ((ur >> 1) & 3)) + 4 * (us & 1) : us ^ ((ur >> 2) & 3);
-    const uint32_t xoff = (uint32_t)ur * xrow + 16 * up, xstep = kUnitRows * xrow;
     const int xk = up * (BITS == 8 ? 16 : 32);
     constexpr uint32_t kOwn = (S::kXu + S::kWu) * 1024;
-    const uint32_t woff = wave * 1024 + lane * 16;               // block `wave` of the chunk; one column tile per unit
-    // The scales of chunks 4q .. 4q+3: one column tile, and 64 rows (the same rows by several wavefronts
+    uint32_t xoff[S::kXu], woff[S::kWu];
+#pragma unroll
+    for (int k = 0; k < S::kXu; ++k) xoff[k] = (uint32_t)(ur + k * kUnitRows) * xrow + 16 * up;
+#pragma unroll
+    for (int k = 0; k < S::kWu; ++k) woff[k] = wave * 1024 + lane * 16 + k * wtile;   // block `wave` of column tile k
+    // The scales of the slice's chunks 4q .. 4q+3: one column tile, and 64 rows (the same rows by several wavefronts
     // where the tile has fewer), per wavefront.  Past K: whatever lies there, or zeros; not used.
     constexpr int kParts = S::kRows / 64;
     const int part64 = wave % kParts;
-    const uint32_t foff = wave * ftile + lane * 16;
-    const uint32_t soff = ((uint32_t)(part64 * 64 + lane) * srow + mis) & ~3u;
+    const uint32_t foff = wave * ftile + lane * 16 + cb * 256;
+    const uint32_t soff = (((uint32_t)(part64 * 64 + lane) * srow + mis) & ~3u) + cb * 4;
     auto issue_scales = [&](int q) __attribute__((always_inline)) {
         const uint32_t f = S::kScales + (q & 1) * S::kFs + wave * 1024, x = S::kScales + 2 * S::kFs + (q & 1) * S::kXs + part64 * 1024;
         if constexpr (kLdsPoison) {              // debug build: scales of about 2^120 where these will land
@@ -378,20 +380,21 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
         dma16(fr, foff + q * 1024, 0, base + f);
         dma16(sr, soff + q * 16, 0, base + x);
     };
-    // transfer k of chunk c's batch; a chunk past the slice brings zeros (no traffic), so that the counted
-    // waits stay the same
+    // transfer k of chunk c's batch; for a chunk past the slice the resources are empty, which brings zeros
+    // (no traffic), so that the counted waits stay the same
     auto issue_op = [&](int c, int stage, int k) __attribute__((always_inline)) {
-        const int left = c < ce ? Kc - c * kMxChunk : 0;
-        const uint32_t cc = (uint32_t)(c < chunks ? c : chunks - 1), st = stage * S::kStage + wave * kOwn;
+        const bool in = c < ce;
+        const uint32_t st = stage * S::kStage + wave * kOwn;
         if constexpr (kLdsPoison) {              // debug build: NaN where this transfer will land
             lds[st / 16 + k * 64 + lane] = lds_nan16();
             lds_write_fence();
         }
-        const uint32_t vx = xk < left ? xoff : kOutside, vw = left > 0 ? woff : kOutside;
-        const uint32_t sx = cc * (BITS == 8 ? 128 : 64);
-        if (k == 0) dma16(xr, vx, sx, base + st);
-        else if (k < S::kXu) dma16_next(xr, vx, k * xstep, sx);
-        else dma16_next(wr, vw, (k - S::kXu) * wtile, cc * 4096);
+        const i32x4 xc = {xr[0], xr[1], in ? xr[2] : 0, xr[3]}, wc = {wr[0], wr[1], in ? wr[2] : 0, wr[3]};
+        const uint32_t past = ALIGNED || xk < Kc - c * kMxChunk ? 0 : kOutside;       // a piece past K
+        const uint32_t sx = c * (BITS == 8 ? 128 : 64);
+        if (k == 0) dma16(xc, xoff[0] | past, sx, base + st);
+        else if (k < S::kXu) dma16_next(xc, xoff[k] | past, sx);
+        else dma16_next(wc, woff[k - S::kXu], c * 4096);
     };
 
     // LDS byte offsets of this lane's operands within a stage; of its weight scales and of its scale byte of
@@ -409,6 +412,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
         const int r = (wm * RF + rf) * 16 + i;
         sl[rf] = r * 16 + (ALIGNED ? 0 : (((uint32_t)r * srow + mis) & 3)) + g;
     }
+    uint32_t slot = 0;                           // of the group that is read
 
     floatx4 acc[RF][CF];
 #pragma unroll
@@ -427,16 +431,16 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     };
     constexpr int H = CF / 2, kFetchX = RF * 2, kFetchW = H + 1, kMul = RF * H;
     const uint8_t* const lb = (const uint8_t*)lds;
-    // LDS reads of chunk c, one at a time
-    auto fetch_x_op = [&](int c, int stage, int k, Acts& a) __attribute__((always_inline)) {
+    // LDS reads of the slice's chunk u modulo 4, one at a time
+    auto fetch_x_op = [&](int u, int stage, int k, Acts& a) __attribute__((always_inline)) {
         const int rf = k / 2;
         if (k % 2 == 1) {
-            const uint32_t q = c >> 2, in = 4 * (c & 3), xs = S::kScales + 2 * S::kFs;
+            const uint32_t xs = S::kScales + 2 * S::kFs + 4 * u;
             if constexpr (ALIGNED) {
-                a.e[rf] = lb[xs + (q & 1) * S::kXs + in + sl[0] + rf * 256];
+                a.e[rf] = lb[xs + slot * S::kXs + sl[0] + rf * 256];
             } else {                             // 16 bytes a row; past them the next group's first ones
-                const uint32_t b = (sl[rf] & 15) + in;
-                a.e[rf] = lb[xs + (b >= 16 ? (~q & 1) * S::kXs - 16 : (q & 1) * S::kXs) + sl[rf] + in];
+                const bool over = u == 3 && (sl[rf] & 15) >= 4;
+                a.e[rf] = lb[xs + (over ? (slot ^ 1) * S::kXs - 16 : slot * S::kXs) + sl[rf]];
             }
         } else if constexpr (BITS == 8) {        // 32 contiguous bytes
             a.x[rf] = *(const i32x8_a16*)(lb + stage * S::kStage + xl + unit_at(2 * rf));
@@ -444,9 +448,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
             a.x[rf] = *(const u32x4*)(lb + stage * S::kStage + xl + unit_at(rf));
         }
     };
-    auto fetch_w_op = [&](int c, int stage, int half, int k, Half& h) __attribute__((always_inline)) {
+    auto fetch_w_op = [&](int u, int stage, int half, int k, Half& h) __attribute__((always_inline)) {
         const int j = wn * CF + half * H + (k > 0 ? k - 1 : 0);   // fragment among the tile's 16
-        if (k == 0) h.e = *(const uint32_t*)(lb + S::kScales + ((c >> 2) & 1) * S::kFs + (c & 3) * 256 + fl + j / 4 * 1024);
+        if (k == 0) h.e = *(const uint32_t*)(lb + S::kScales + slot * S::kFs + u * 256 + fl + j / 4 * 1024);
         else h.w[k - 1] = *(const u32x4*)(lb + stage * S::kStage + wl + j / 4 * 1024 + j % 4 * 256);
     };
     auto product = [&](const Acts& a, const uint32_t (&e)[RF], const Half& h, int half, int n) __attribute__((always_inline)) {
@@ -457,8 +461,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
         if (j % 4 == 3) mx_mfma_acc<BITS, 3>(acc[rf][j], h.w[q], a.x[rf], h.e, e[rf]);
     };
 
-    issue_scales(cb >> 2);
-    issue_scales((cb >> 2) + 1);
+    issue_scales(0);
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s)
 #pragma unroll
@@ -467,25 +470,33 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     Half lo, hi;
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((ST - 2) * S::kData) : "memory");
 #pragma unroll
-    for (int k = 0; k < kFetchX; ++k) fetch_x_op(cb, 0, k, xa);
+    for (int k = 0; k < kFetchX; ++k) fetch_x_op(0, 0, k, xa);
 #pragma unroll
-    for (int k = 0; k < kFetchW; ++k) fetch_w_op(cb, 0, 0, k, lo);
-    int stage = 0;                               // of chunk c
-    auto turn = [&](int c, const Acts& now, Acts& next) __attribute__((always_inline)) {
-        const int behind = stage == 0 ? ST - 1 : stage - 1, ahead = stage == ST - 1 ? 0 : stage + 1;
-        // Group c/4 + 1 takes the place of group c/4 - 1, whose last bytes were in registers before the last
+    for (int k = 0; k < kFetchW; ++k) fetch_w_op(0, 0, 0, k, lo);
+    int stage3 = 0;                              // of chunk c, with three stages
+    // Chunk c, the slice's chunk u modulo 4; EDGE: it may reach past K.
+    auto turn = [&](auto EDGE, int u, int c, const Acts& now, Acts& next) __attribute__((always_inline)) {
+        constexpr bool edge = decltype(EDGE)::value;
+        const int v = (u + 1) % 4, stage = ST == 4 ? u : stage3;
+        const int behind = ST == 4 ? (u + 3) % 4 : stage == 0 ? ST - 1 : stage - 1;
+        const int ahead = ST == 4 ? v : stage == ST - 1 ? 0 : stage + 1;
+        // The next group takes the place of the one before, whose last bytes were in registers before the last
         // barrier.  Before the batch's kData transfers, so that the counted waits cover it.
-        if ((c & 3) == 0) issue_scales((c >> 2) + 1);
-        // past K: elements are zero, the scales 1 (what was read for them may say NaN)
-        const bool inside = 4 * c + g < (int)srow;
+        if (u == 0) issue_scales((c - cb) / 4 + 1);
         uint32_t e[RF];
+        if constexpr (edge) {                    // past K: elements are zero, the scales 1 (what was read may say NaN)
+            const bool inside = 4 * c + g < (int)srow;
 #pragma unroll
-        for (int rf = 0; rf < RF; ++rf) {
-            e[rf] = inside ? now.e[rf] : 127u;
-            asm volatile("" : "+v"(e[rf]));      // in registers here, not next to their use
+            for (int rf = 0; rf < RF; ++rf) {
+                e[rf] = inside ? now.e[rf] : 127u;
+                asm volatile("" : "+v"(e[rf]));  // in registers here, not next to their use
+            }
+            lo.e = c < chunks ? lo.e : 0x7f7f7f7fu;
+            asm volatile("" : "+v"(lo.e));
+        } else {
+#pragma unroll
+            for (int rf = 0; rf < RF; ++rf) e[rf] = now.e[rf];
         }
-        lo.e = c < chunks ? lo.e : 0x7f7f7f7fu;
-        asm volatile("" : "+v"(lo.e));
         asm volatile("s_nop 1");
         constexpr int ops1 = kFetchW + S::kData;
 #pragma unroll
@@ -494,16 +505,19 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
 #pragma unroll
             for (int k = 0; k < ops1; ++k) {
                 if (k * kMul / ops1 != n) continue;
-                if (k < kFetchW) fetch_w_op(c, stage, 1, k, hi);
+                if (k < kFetchW) fetch_w_op(u, stage, 1, k, hi);
                 else issue_op(c + ST - 1, behind, k - kFetchW);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((ST - 2) * S::kData) : "memory");
         __builtin_amdgcn_sched_barrier(0);
-        hi.e = c < chunks ? hi.e : 0x7f7f7f7fu;
-        asm volatile("" : "+v"(hi.e));
+        if constexpr (edge) {
+            hi.e = c < chunks ? hi.e : 0x7f7f7f7fu;
+            asm volatile("" : "+v"(hi.e));
+        }
         asm volatile("s_nop 1");
+        if (u == 3) slot ^= 1;
         constexpr int ops2 = kFetchW + kFetchX;
 #pragma unroll
         for (int n = 0; n < kMul; ++n) {
@@ -511,18 +525,49 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
 #pragma unroll
             for (int k = 0; k < ops2; ++k) {
                 if (k * kMul / ops2 != n) continue;
-                if (k < kFetchW) fetch_w_op(c + 1, ahead, 0, k, lo);
-                else fetch_x_op(c + 1, ahead, k - kFetchW, next);
+                if (k < kFetchW) fetch_w_op(v, ahead, 0, k, lo);
+                else fetch_x_op(v, ahead, k - kFetchW, next);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        stage = ahead;
+        stage3 = ahead;
     };
-    // Two turns at a time: slices are multiples of two chunks, and past K a turn adds zeros.  (Leaving the
-    // loop between turns made the compiler copy the accumulators.)
-    for (int c = cb; c < ce; c += 2) {
-        turn(c, xa, xb);
-        turn(c + 1, xb, xa);
+    // Before a place where the compiler may copy the accumulators: the ways into and out of a branch.
+    auto join = [&]() __attribute__((always_inline)) {
+        mx_settle();
+#pragma unroll
+        for (int rf = 0; rf < RF; ++rf)
+#pragma unroll
+            for (int j = 0; j < CF; ++j) mx_pin(acc[rf][j]);
+    };
+    constexpr std::false_type kWhole{};
+    constexpr std::true_type kEdge{};
+    int c = cb;
+    if constexpr (RF * CF < 64) {
+        // Four turns at a time, so that the LDS addresses are constants (60 instructions a turn beside the
+        // products instead of 168: 257 x 5120 x 13824, 4 bits, 28.5 -> 23.0 us); then the last one to four chunks.
+        for (; c + 4 < ce; c += 4) {
+            turn(kWhole, 0, c, xa, xb);
+            turn(kWhole, 1, c + 1, xb, xa);
+            turn(kWhole, 2, c + 2, xa, xb);
+            turn(kWhole, 3, c + 3, xb, xa);
+        }
+        join();
+        turn(kEdge, 0, c, xa, xb);
+        turn(kEdge, 1, c + 1, xb, xa);
+        join();
+        if (c + 2 < ce) {
+            turn(kEdge, 2, c + 2, xa, xb);
+            turn(kEdge, 3, c + 3, xb, xa);
+            join();
+        }
+    } else {
+        // All accumulation registers are taken, and with more than one loop, or a way out between turns, the
+        // compiler copies them.  64 products a wavefront cover the other instructions of a turn.
+        for (; c < ce; c += 2) {
+            turn(kEdge, (c - cb) & 3, c, xa, xb);
+            turn(kEdge, (c - cb + 1) & 3, c + 1, xb, xa);
+        }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     mx_settle();
@@ -611,12 +656,11 @@ constexpr int kMaxSlices = 16;
 // Which kernel, and how many slices of K, by the time that each would take: us on this card, fitted to
 // measured launches (K = 4096 .. 28672, N = 1024 .. 28672):
 //   register kernel, R fragments of 16 rows: 4 + (64-column chunks per CU) * {.19, .23, .30, .42}[R - 1];
-//     e.g. 64 rows, K = N = 8192: 18 us (tiles 20), 64 rows, N = 28672: 51 us (tiles 33);
-//   tiles of 64 wm rows: 4.5 + turns * turn_us per round of one workgroup per CU, and for
-//     joining slices 2 + .35 per MB of partials; not below the time in which these kernels stream the
-//     weights (4 TB/s).  E.g.
-//     257 x 5120 x 13824: 32 us with 128 rows a tile, 44 with 64, 54 with 256; 100 x 8192 x 8192, 64-row
-//     tiles: 33, 24, 21, 21 us with 1, 2, 3, 4 slices.
+//     e.g. 64 rows, K = N = 8192: 18 us (tiles 14), 20 x 9792 x 680: 6.7 us;
+//   tiles of 64 wm rows: 1.5 + rounds of one workgroup per CU * (start_us + turns * turn_us), and for joining
+//     slices 2 + .35 per MB of partials; the rounds not below the time in which these kernels stream the
+//     weights (4 TB/s).  E.g. 257 x 5120 x 13824, 4 bits: 23 us with 128 rows a tile, 30 with 64, 41 with 256;
+//     128 x 4096 x 4096, 8 bits, 64-row tiles: 14.7, 14.0, 13.4, 13.9 us with 1, 2, 3, 4 slices.
 MxGemmPlan plan_mx_gemm(int64_t M, int64_t K, int64_t N, int bits) {
     MxGemmPlan p{};
     const int64_t chunks = mx_kb(K) / 4;
@@ -636,8 +680,8 @@ MxGemmPlan plan_mx_gemm(int64_t M, int64_t K, int64_t N, int bits) {
         p.ws_bytes = p.nz > 1 ? kCounterBytes + (size_t)p.col_tiles * p.nz * p.row_tiles * 4096 : 0;
         if (M <= 16) return p;
     }
-    static const double turn_us[2][3] = {{.42, .56, 1.0}, {.48, .72, 1.36}};   // 4 bits, 8 bits
-    const double stream = 4.5 + (double)mx_codes_bytes(K, N) / 4e6;
+    static const double start_us[3] = {4, 6, 8.5}, turn_us[2][3] = {{.31, .45, .80}, {.39, .63, 1.18}};   // 4, 8 bits
+    const double stream = 2 + (double)mx_codes_bytes(K, N) / 4e6;
     for (int k = 0; k < 3; ++k) {
         const int wm = 1 << k;
         const int64_t rt = (M + 64 * wm - 1) / (64 * wm), ct = (N + 255) / 256, tiles = rt * ct;
@@ -645,7 +689,7 @@ MxGemmPlan plan_mx_gemm(int64_t M, int64_t K, int64_t N, int bits) {
             const int64_t turns = ((chunks + nz - 1) / nz + 1) / 2 * 2, groups = tiles * nz;
             if (nz > 1 && (turns < 4 || groups > kCus)) break;
             const double rounds = (double)((groups + kCus - 1) / kCus);
-            const double us = std::max(stream, 4.5 + rounds * turns * turn_us[bits == 8][k]) +
+            const double us = std::max(stream, 1.5 + rounds * (start_us[k] + turns * turn_us[bits == 8][k])) +
                               (nz == 1 ? 0 : 2 + .35e-6 * (double)(groups * 64 * wm * 256 * 4));
             if (us >= best) continue;
             best = us;
@@ -704,7 +748,7 @@ hipError_t launch_mx_gemm(const uint8_t* xcodes, const uint8_t* xscales, int bit
     }
     if (p.wm == 4) return run(bits == 8 ? launch_tile<8, 2, 2, 8, 8, 3> : launch_tile<4, 2, 2, 8, 8, 4>);
     if (p.wm == 2) return run(bits == 8 ? launch_tile<8, 2, 2, 4, 8, 4> : launch_tile<4, 2, 2, 4, 8, 4>);
-    return run(bits == 8 ? launch_tile<8, 1, 4, 4, 4, 5> : launch_tile<4, 1, 4, 4, 4, 5>);
+    return run(bits == 8 ? launch_tile<8, 1, 4, 4, 4, 4> : launch_tile<4, 1, 4, 4, 4, 4>);
 }
 
 }  // namespace awq
