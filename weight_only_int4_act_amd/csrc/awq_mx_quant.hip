@@ -13,9 +13,9 @@ __device__ __forceinline__ u32x4 pack_bf16x8(const float (&v)[8]) {
 // ---------------------------------------------------------------- quantizer
 // p = x, or x g / (1 + e^-g), divided by s per channel.  Bound by HBM: 2 (4 with a gate) bytes read and
 // 1.03 or 0.53 written per element.  A workgroup takes 64 octets of channels (512) and 4 R rows; a
-// wavefront walks its R rows with the reciprocals of s in registers, four rows' loads in flight.
+// wavefront walks its R rows with the reciprocals of s in registers, two rows' loads in flight.
 // Four consecutive lanes hold a block.
-constexpr int kRowsInFlight = 4;
+constexpr int kRowsInFlight = 2;
 
 template <int BITS, bool GATE, bool SCALED>
 __global__ __launch_bounds__(256) void k_mx_quantize(const uint16_t* __restrict__ X,
@@ -230,9 +230,11 @@ hipError_t norm(const NormArgs& a, hipStream_t st) {
 
 hipError_t launch_mx_quantize(const uint16_t* X, const uint16_t* gate, int64_t M, int64_t K, const float* s, int bits,
                               uint8_t* codes, uint8_t* scales, hipStream_t st) {
-    // rows per wavefront: eight, fewer where that would leave less than four workgroups per CU
+    // Rows per wavefront: one while that gives no more than two workgroups per CU (64 x 8192: 2.36 us, with
+    // two rows 2.62), else two (257 x 5120, 4 bits: 2.65 us, with one row 2.90; 8192 x 11008 with a gate: 83 us,
+    // 88 with four rows, 92 with eight).
     const int64_t cols = (K / 8 + 63) / 64, quads = (M + 3) / 4;
-    int R = (int)std::max<int64_t>(1, std::min<int64_t>(8, cols * quads / (4 * kNumXcd * kCusPerXcd)));
+    int R = cols * quads > 2 * kNumXcd * kCusPerXcd ? 2 : 1;
     while ((quads + R - 1) / R > 65535) R *= 2;
     const dim3 grid((unsigned)cols, (unsigned)((quads + R - 1) / R));
     auto go = [&](auto kernel) {
@@ -252,13 +254,16 @@ hipError_t launch_rms_norm(const uint16_t* X, const uint16_t* residual, const ui
                            uint8_t* scales, hipStream_t st) {
     const NormArgs a{X, residual, weight, M, K, (double)eps, 1. / (double)K, residual_out, Y, s, bits, codes, scales};
     const int64_t octs = K / 8;
-    // Few rows: as many threads as the row has octets.  Many: more octets per thread, so that the sum's
-    // fixed cost is shared by more of them.
-    const bool few = M <= 2 * kNumXcd * kCusPerXcd;
+    // As many threads as the row has octets, because the sum's chain of float64 additions grows with the
+    // octets of a thread; but two or four octets for the longer rows once every CU has a row, so that several
+    // rows share a CU.  256 x 8192: 4.44 us with one octet, 4.62 with two; 4096 x 8192: 53.2 and 45.0, 50.3 with
+    // four; 200 x 16384: 7.2 us with two, 7.9 with four; 4096 x 16384: 97 and 92; 2000 x 4096: 10.8 us with one,
+    // 11.5 with two.
+    const bool few = M <= kNumXcd * kCusPerXcd;
     if (octs <= 64) return norm<64, 1>(a, st);
-    if (octs <= 256) return few ? norm<256, 1>(a, st) : norm<64, 4>(a, st);
-    if (octs <= 512) return few ? norm<512, 1>(a, st) : norm<256, 2>(a, st);
-    if (octs <= 1024) return few ? norm<1024, 1>(a, st) : norm<256, 4>(a, st);
+    if (octs <= 256) return norm<256, 1>(a, st);
+    if (octs <= 512) return norm<512, 1>(a, st);
+    if (octs <= 1024) return few ? norm<1024, 1>(a, st) : norm<512, 2>(a, st);
     if (octs <= 2048) return few ? norm<1024, 2>(a, st) : norm<512, 4>(a, st);
     if (octs <= 4096) return norm<1024, 4>(a, st);
     k_rms_norm_long<<<(unsigned)M, 1024, 0, st>>>(a);
