@@ -39,7 +39,6 @@ __device__ __forceinline__ floatx4 load4_agent(__amdgpu_buffer_rsrc_t r, uint32_
     return __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kCpolAgent));
 }
 
-
 // ---------------------------------------------------------------- up to 64 rows: weights streamed once
 // Bound by the weights' bytes.  A workgroup owns 64 columns (one tile of packed weights, contiguous
 // in memory) and a slice of K; its NW wavefronts take every NW-th 128-channel chunk and keep D of
@@ -47,8 +46,8 @@ __device__ __forceinline__ floatx4 load4_agent(__amdgpu_buffer_rsrc_t r, uint32_
 // elements and scale bytes (16 RF rows, repeated reads that the caches serve).  A load past the slice,
 // past K or past the last row lies outside its buffer resource: it brings zeros and costs no traffic,
 // so the loop needs no branch between a load and its use.  The wavefronts' sums meet in LDS in a fixed
-// order; with several slices the last workgroup to arrive adds the
-// float32 partials in slice order.
+// order; with several slices the last workgroup to arrive adds the float32 partials in slice order.
+// 13 x 28672 x 8192: 25 us (5.0 TB/s; with both operands staged in LDS 109 us); 1 x 8192 x 10240: 11 us.
 template <int BITS, int RF, int NW, int D>
 __global__ __launch_bounds__(64 * NW) void k_mx_gemm_rows(
     const uint8_t* __restrict__ xcodes, const uint8_t* __restrict__ xscales, int rows,
@@ -211,7 +210,14 @@ __global__ __launch_bounds__(64 * NW) void k_mx_gemm_rows(
 // product keeps its matrix core busy for 32 cycles: during the first half the transfers of chunk
 // c + ST - 1 are issued and the second half's weights are read from LDS; then a barrier says that chunk c
 // is in every wavefront's registers and chunk c + 1 has landed; during the second half the next chunk's
-// activations and first weights are read.
+// activations and first weights are read.  (Both operands of a whole chunk a turn ahead in registers: no
+// faster, and too many of them for 256 rows.)
+//
+// What bounds it.  256 rows: the power that the matrix cores take; 4096 x 8192 x 28672 runs at 2.9 PFLOP/s
+// with 8 bits (664 us) and 4096 x 28672 x 8192 at 4.3 with 4 (446 us), the 8-bit products without any
+// transfer or read at 3.0.  64 and 128 rows: one wavefront per SIMD issues everything, and products,
+// transfers and LDS reads overlap in part (257 x 5120 x 13824, 4 bits, 23 us: products alone 10, transfers
+// alone 10, LDS reads 4, prologue and epilogue 6).
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ i32x4 byte_rsrc(const void* base, uint32_t bytes) {
     const uint64_t a = (uint64_t)(uintptr_t)base;
@@ -371,7 +377,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     const uint32_t foff = wave * ftile + lane * 16 + cb * 256;
     const uint32_t soff = (((uint32_t)(part64 * 64 + lane) * srow + mis) & ~3u) + cb * 4;
     auto issue_scales = [&](int q) __attribute__((always_inline)) {
-        const uint32_t f = S::kScales + (q & 1) * S::kFs + wave * 1024, x = S::kScales + 2 * S::kFs + (q & 1) * S::kXs + part64 * 1024;
+        const uint32_t f = S::kScales + (q & 1) * S::kFs + wave * 1024;
+        const uint32_t x = S::kScales + 2 * S::kFs + (q & 1) * S::kXs + part64 * 1024;
         if constexpr (kLdsPoison) {              // debug build: scales of about 2^120 where these will land
             lds[f / 16 + lane] = lds_nan16();
             lds[x / 16 + lane] = lds_nan16();
@@ -720,7 +727,8 @@ static hipError_t launch_tile(const uint8_t* xcodes, const uint8_t* xscales, int
     using S = TileShape<BITS, WM, WN, RF, CF, ST>;
     const int64_t total = p.row_tiles * p.col_tiles * p.nz, per_xcd = (total + kNumXcd - 1) / kNumXcd;
     const bool aligned = K % kMxChunk == 0 && (uintptr_t)xscales % 4 == 0;
-    const auto kernel = aligned ? k_mx_gemm_tile<BITS, WM, WN, RF, CF, ST, true> : k_mx_gemm_tile<BITS, WM, WN, RF, CF, ST, false>;
+    const auto kernel = aligned ? k_mx_gemm_tile<BITS, WM, WN, RF, CF, ST, true>
+                                : k_mx_gemm_tile<BITS, WM, WN, RF, CF, ST, false>;
     // the limit is a property of the function on the current device; setting it again is harmless
     const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
     if (e != hipSuccess) return e;
