@@ -194,10 +194,12 @@ __global__ __launch_bounds__(64 * NW) void k_mx_gemm_rows(
 // 16 RF WM rows x 256 columns per workgroup, WM x WN wavefronts, each with RF x CF fragments of 16 x 16
 // results in registers.  Per 128-channel chunk both operands are copied once per workgroup straight
 // into LDS, ST chunks deep, in the order in which the matrix core's lanes read them back:
-//   activations  1 KB units.  8 bits: 8 rows of 128 bytes; the two 16-byte pieces g and g + 4 that one
-//                lane needs lie together, at 32-byte slot g ^ (row/2 % 4).  4 bits: 16 rows of 64 bytes,
-//                piece g at 16-byte slot g ^ (row/4 % 4).  So a transfer reads whole lines, and lanes
-//                reading the same piece of eight rows hit different banks;
+//   activations  1 KB units.  8 bits: 8 rows of 128 bytes; the two 16-byte pieces g and g + 4 that one lane
+//                needs share the 32-byte slot g ^ 2 (row/8 % 2), the first of them at its half row/2 % 2.
+//                4 bits: 16 rows of 64 bytes, piece g at 16-byte slot g ^ 2 (row/8 % 2).  So a transfer
+//                reads whole lines, and the lanes that a 16-byte read serves together (0-3, 12-15, 20-27
+//                and 4-11, 16-19, 28-31 of either half) hit different banks: conflicts per LDS instruction
+//                2.36 -> 0.47 (8 bits), 1.33 -> 0.44 (4 bits), against swizzling by row/2 and row/4;
 //   weights      the packed order: 1 KB per block of 64 columns, read 256 contiguous bytes at a time;
 //   scales       of four chunks at a time, two such groups deep: weights 1 KB per column tile;
 //                activations 16 bytes per row, from the 4-byte boundary at or before the group's first
@@ -300,8 +302,9 @@ __device__ __forceinline__ void mx_pin(floatx4& acc) {
     asm volatile("" : "+a"(acc));
 #endif
 }
-// No result of mx_mfma_acc is read before this many wait states (18 cover the longest product).
-__device__ __forceinline__ void mx_settle() { asm volatile("s_nop 15\n\ts_nop 7"); }
+// No result of mx_mfma_acc is read before this (the compiler puts 12 and 8 wait states after its own products).
+template <int BITS>
+__device__ __forceinline__ void mx_settle() { asm volatile("s_nop %0" ::"n"(BITS == 8 ? 13 : 9)); }
 
 template <int BITS, int WM, int WN, int RF, int CF, int ST>
 struct TileShape {
@@ -361,13 +364,19 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     // channel within a chunk.  Rows past `rows` and column tiles past `cts` lie outside the resources: zeros.
     constexpr int kUnitRows = BITS == 8 ? 8 : 16, kPieces = BITS == 8 ? 8 : 4;
     const int ur = wave * S::kXu * kUnitRows + lane / kPieces;
-    const int us = lane % kPieces;               // slot of the row
-    const int up = BITS == 8 ? ((us >> 1) ^ ((ur >> 1) & 3)) + 4 * (us & 1) : us ^ ((ur >> 2) & 3);
-    const int xk = up * (BITS == 8 ? 16 : 32);
+    const int us = lane % kPieces;               // 16-byte slot of the row
+    const int ub = wave * S::kXu & 1;            // 8 bits: bit 3 of the first unit's rows
+    auto piece = [&](int k) {                    // at slot us of unit k's rows
+        if constexpr (BITS == 4) return us ^ (2 * (ur >> 3 & 1));
+        else return ((us >> 1) ^ (2 * ((ub + k) & 1))) + 4 * ((us ^ (ur >> 1)) & 1);
+    };
+    int xk[2];                                   // first channel of the piece, units of either parity
+#pragma unroll
+    for (int k = 0; k < 2; ++k) xk[k] = piece(k) * (BITS == 8 ? 16 : 32);
     constexpr uint32_t kOwn = (S::kXu + S::kWu) * 1024;
     uint32_t xoff[S::kXu], woff[S::kWu];
 #pragma unroll
-    for (int k = 0; k < S::kXu; ++k) xoff[k] = (uint32_t)(ur + k * kUnitRows) * xrow + 16 * up;
+    for (int k = 0; k < S::kXu; ++k) xoff[k] = (uint32_t)(ur + k * kUnitRows) * xrow + 16 * piece(k);
 #pragma unroll
     for (int k = 0; k < S::kWu; ++k) woff[k] = wave * 1024 + lane * 16 + k * wtile;   // block `wave` of column tile k
     // The scales of the slice's chunks 4q .. 4q+3: one column tile, and 64 rows (the same rows by several wavefronts
@@ -397,7 +406,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
             lds_write_fence();
         }
         const i32x4 xc = {xr[0], xr[1], in ? xr[2] : 0, xr[3]}, wc = {wr[0], wr[1], in ? wr[2] : 0, wr[3]};
-        const uint32_t past = ALIGNED || xk < Kc - c * kMxChunk ? 0 : kOutside;       // a piece past K
+        const uint32_t past = ALIGNED || xk[k & 1] < Kc - c * kMxChunk ? 0 : kOutside;   // a piece past K
         const uint32_t sx = c * (BITS == 8 ? 128 : 64);
         if (k == 0) dma16(xc, xoff[0] | past, sx, base + st);
         else if (k < S::kXu) dma16_next(xc, xoff[k] | past, sx);
@@ -410,8 +419,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     auto unit_at = [](int e) { return (uint32_t)(e / S::kXu) * kOwn + (uint32_t)(e % S::kXu) * 1024; };
     static_assert(RF * kFragUnits % S::kXu == 0, "a wavefront's rows are whole wavefronts' units");
     const uint32_t xl = unit_at(wm * RF * kFragUnits) +
-                        (BITS == 8 ? (i >> 3) * 1024 + (i & 7) * 128 + ((g ^ ((i >> 1) & 3)) * 32)
-                                   : i * 64 + ((g ^ ((i >> 2) & 3)) * 16));
+                        (BITS == 8 ? (i >> 3) * 1024 + (i & 7) * 128 + (g ^ (2 * (i >> 3))) * 32 + (i >> 1 & 1) * 16
+                                   : i * 64 + (g ^ (2 * (i >> 3))) * 16);
+    const uint32_t xh = xl ^ 16;                 // 8 bits: the second piece
     const uint32_t wl = g * kOwn + S::kXu * 1024 + i * 16, fl = g * 64 + i * 4;
     uint32_t sl[ALIGNED ? 1 : RF];
 #pragma unroll
@@ -427,7 +437,6 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
 #pragma unroll
         for (int j = 0; j < CF; ++j) acc[rf][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-    typedef int i32x8_a16 __attribute__((ext_vector_type(8), aligned(16)));
     struct Acts {
         XFrag<BITS> x[RF];
         uint32_t e[RF];
@@ -449,8 +458,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
                 const bool over = u == 3 && (sl[rf] & 15) >= 4;
                 a.e[rf] = lb[xs + (over ? (slot ^ 1) * S::kXs - 16 : slot * S::kXs) + sl[rf]];
             }
-        } else if constexpr (BITS == 8) {        // 32 contiguous bytes
-            a.x[rf] = *(const i32x8_a16*)(lb + stage * S::kStage + xl + unit_at(2 * rf));
+        } else if constexpr (BITS == 8) {
+            const u32x4 p = *(const u32x4*)(lb + stage * S::kStage + xl + unit_at(2 * rf));
+            const u32x4 q = *(const u32x4*)(lb + stage * S::kStage + xh + unit_at(2 * rf));
+            a.x[rf] = i32x8{(int)p[0], (int)p[1], (int)p[2], (int)p[3], (int)q[0], (int)q[1], (int)q[2], (int)q[3]};
         } else {
             a.x[rf] = *(const u32x4*)(lb + stage * S::kStage + xl + unit_at(rf));
         }
@@ -539,9 +550,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
         }
         stage3 = ahead;
     };
-    // Before a place where the compiler may copy the accumulators: the ways into and out of a branch.
+    // On both sides of every place where the compiler may copy or read accumulators, the ways into and out of
+    // a loop or branch: no product is in flight before, and none starts right after.  (A product keeps its
+    // matrix core for most of this wait anyway.)
     auto join = [&]() __attribute__((always_inline)) {
-        mx_settle();
+        mx_settle<BITS>();
 #pragma unroll
         for (int rf = 0; rf < RF; ++rf)
 #pragma unroll
@@ -558,12 +571,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
             turn(kWhole, 1, c + 1, xb, xa);
             turn(kWhole, 2, c + 2, xa, xb);
             turn(kWhole, 3, c + 3, xb, xa);
+            join();
         }
         join();
         turn(kEdge, 0, c, xa, xb);
         turn(kEdge, 1, c + 1, xb, xa);
         join();
         if (c + 2 < ce) {
+            join();
             turn(kEdge, 2, c + 2, xa, xb);
             turn(kEdge, 3, c + 3, xb, xa);
             join();
@@ -574,11 +589,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
         for (; c < ce; c += 2) {
             turn(kEdge, (c - cb) & 3, c, xa, xb);
             turn(kEdge, (c - cb + 1) & 3, c + 1, xb, xa);
+            join();
         }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    mx_settle();
-    auto settled = [&](int rf) __attribute__((always_inline)) {   // a row fragment's results may be read
+    auto settled = [&](int rf) __attribute__((always_inline)) {   // one row fragment's results at a time
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < CF; ++j) mx_pin(acc[rf][j]);
