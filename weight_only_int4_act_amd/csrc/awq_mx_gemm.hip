@@ -41,14 +41,15 @@ __device__ __forceinline__ floatx4 load4_agent(__amdgpu_buffer_rsrc_t r, uint32_
 
 // ---------------------------------------------------------------- up to 64 rows: weights streamed once
 // Bound by the weights' bytes.  A workgroup owns 64 columns (one tile of packed weights, contiguous
-// in memory) and a slice of K; its NW wavefronts take every NW-th 128-channel chunk and keep D of
-// them in flight in registers: 4 KB of codes by non-temporal loads, the scale words, and the rows'
-// elements and scale bytes (16 RF rows, repeated reads that the caches serve).  A load past the slice,
+// in memory) and a slice of K; its NW wavefronts take every NW-th 128-channel chunk, one in flight each,
+// in registers: 4 KB of codes by non-temporal loads, the scale words, and the rows'
+// elements and scale bytes (16 RF rows, repeated reads that the caches serve).  (Two chunks in flight were
+// slower: 1 x 8192 x 10240 12.2 against 10.0 us, 20 x 9792 x 680 6.4 against 6.0.)  A load past the slice,
 // past K or past the last row lies outside its buffer resource: it brings zeros and costs no traffic,
 // so the loop needs no branch between a load and its use.  The wavefronts' sums meet in LDS in a fixed
 // order; with several slices the last workgroup to arrive adds the float32 partials in slice order.
-// 13 x 28672 x 8192: 25 us (5.0 TB/s; with both operands staged in LDS 109 us); 1 x 8192 x 10240: 11 us.
-template <int BITS, int RF, int NW, int D>
+// 13 x 28672 x 8192: 23 us (5.5 TB/s; with both operands staged in LDS 109 us); 1 x 8192 x 10240: 10 us.
+template <int BITS, int RF, int NW>
 __global__ __launch_bounds__(64 * NW) void k_mx_gemm_rows(
     const uint8_t* __restrict__ xcodes, const uint8_t* __restrict__ xscales, int rows,
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t K, int64_t N, int64_t kb_all,
@@ -115,16 +116,11 @@ __global__ __launch_bounds__(64 * NW) void k_mx_gemm_rows(
             acc[rf][3] = mx_mfma<BITS, 3>(b.w[3], x[rf], acc[rf][3], b.we, b.xe[rf]);
         }
     };
-    Buf buf[D];
-#pragma unroll
-    for (int d = 0; d < D; ++d) issue(cb + wave + NW * d, buf[d]);
-    for (int c = cb + wave; c < ce; c += NW * D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            __builtin_amdgcn_sched_barrier(0);   // keep the loads of D chunks ahead of their products
-            consume(buf[d]);
-            issue(c + NW * (D + d), buf[d]);
-        }
+    Buf buf;
+    issue(cb + wave, buf);
+    for (int c = cb + wave; c < ce; c += NW) {
+        consume(buf);
+        issue(c + NW, buf);
     }
     // the products must not move into the branches below: they need every lane's operands
 #pragma unroll
@@ -677,29 +673,34 @@ constexpr int kMaxSlices = 16;
 
 // Which kernel, and how many slices of K, by the time that each would take: us on this card, fitted to
 // measured launches (K = 4096 .. 28672, N = 1024 .. 28672):
-//   register kernel, R fragments of 16 rows: 4 + (64-column chunks per CU) * {.19, .23, .30, .42}[R - 1];
-//     e.g. 64 rows, K = N = 8192: 18 us (tiles 14), 20 x 9792 x 680: 6.7 us;
+//   register kernel: 2.3 + .045 + .0037 M for each 128-channel chunk that a CU takes (64 columns), the
+//     weights at 8 TB/s (the caches hold a part of them) and the rows, read by every column tile, at 14,
+//     and for joining slices .9 + .035 M + nz (.08 + .003 M); no more workgroups than CUs once K is cut.
+//     E.g. 1 x 8192 x 1024, 1, 2, 4, 8 slices: 5.6, 5.5, 4.8, 4.4 us; 1 x 8192 x 10240, 1 and 2: 10.1, 13.4;
+//     50 x 9792 x 680, 1, 4, 8, 16: 20.1, 10.4, 8.9, 10.6 (tiles 9.5);
 //   tiles of 64 wm rows: 1.5 + rounds of one workgroup per CU * (start_us + turns * turn_us), and for joining
 //     slices 2 + .35 per MB of partials; the rounds not below the time in which these kernels stream the
 //     weights (4 TB/s).  E.g. 257 x 5120 x 13824, 4 bits: 23 us with 128 rows a tile, 30 with 64, 41 with 256;
 //     128 x 4096 x 4096, 8 bits, 64-row tiles: 14.7, 14.0, 13.4, 13.9 us with 1, 2, 3, 4 slices.
 MxGemmPlan plan_mx_gemm(int64_t M, int64_t K, int64_t N, int bits) {
-    MxGemmPlan p{};
+    MxGemmPlan p{};                              // wm = 0: the register kernel
     const int64_t chunks = mx_kb(K) / 4;
     double best = 1e30;
     if (M <= 64) {
-        static const double chunk_us[4] = {.19, .23, .30, .42};
-        p.wm = 0;
         p.col_tiles = mx_nt(N);
         p.row_tiles = (M + 15) / 16;             // fragments of the one workgroup row
-        // about one workgroup per CU, and chunks enough for every wavefront's loads in flight
-        const int64_t deep = p.row_tiles == 1 ? 12 : 8;
-        p.nz = 1;
-        if (p.col_tiles <= (int64_t)(kCounterBytes / 4))
-            p.nz = (int)std::max<int64_t>(1, std::min<int64_t>({kCus / p.col_tiles, chunks / deep, kMaxSlices}));
-        best = 4 + (double)(p.col_tiles * chunks) / kCus * chunk_us[p.row_tiles - 1];
         p.cstride = (int)std::max<int64_t>(1, std::min<int64_t>(32, kCounterBytes / 4 / p.col_tiles));
-        p.ws_bytes = p.nz > 1 ? kCounterBytes + (size_t)p.col_tiles * p.nz * p.row_tiles * 4096 : 0;
+        const int64_t most = p.col_tiles > (int64_t)(kCounterBytes / 4) ? 1 : std::min<int64_t>(kMaxSlices, chunks);
+        const double stream = (double)mx_codes_bytes(K, N) / 8e6 + (double)(p.col_tiles * M) * (double)(K * bits / 8) / 14e6;
+        for (int nz = 1; nz <= most && (nz == 1 || p.col_tiles * nz <= kCus); ++nz) {
+            const double per_cu = std::max((double)((chunks + nz - 1) / nz), (double)(p.col_tiles * chunks) / kCus);
+            const double us = 2.3 + per_cu * (.045 + .0037 * (double)M) + stream +
+                              (nz == 1 ? 0 : .9 + .035 * (double)M + nz * (.08 + .003 * (double)M));
+            if (us >= best) continue;
+            best = us;
+            p.nz = nz;
+            p.ws_bytes = nz > 1 ? kCounterBytes + (size_t)p.col_tiles * nz * p.row_tiles * 4096 : 0;
+        }
         if (M <= 16) return p;
     }
     static const double start_us[3] = {4, 6, 8.5}, turn_us[2][3] = {{.31, .45, .80}, {.39, .63, 1.18}};   // 4, 8 bits
@@ -725,11 +726,11 @@ MxGemmPlan plan_mx_gemm(int64_t M, int64_t K, int64_t N, int bits) {
     return p;
 }
 
-template <int BITS, int RF, int NW, int D>
+template <int BITS, int RF, int NW>
 static hipError_t launch_rows(const uint8_t* xcodes, const uint8_t* xscales, int64_t M, const uint8_t* codes,
                               const uint8_t* scales, int64_t K, int64_t N, uint16_t* Y, void* ws, const MxGemmPlan& p,
                               hipStream_t st) {
-    k_mx_gemm_rows<BITS, RF, NW, D><<<dim3((unsigned)p.col_tiles, (unsigned)p.nz), 64 * NW, 0, st>>>(
+    k_mx_gemm_rows<BITS, RF, NW><<<dim3((unsigned)p.col_tiles, (unsigned)p.nz), 64 * NW, 0, st>>>(
         xcodes, xscales, (int)M, codes, scales, K, N, mx_kb(K), Y, (float*)((char*)ws + kCounterBytes), (uint32_t*)ws,
         p.cstride);
     return hipGetLastError();
@@ -763,10 +764,10 @@ hipError_t launch_mx_gemm(const uint8_t* xcodes, const uint8_t* xscales, int bit
     const auto run = [&](auto f) { return f(xcodes, xscales, M, codes, scales, K, N, Y, ws, p, st); };
     if (p.wm == 0) {
         switch (p.row_tiles) {
-            case 1: return run(bits == 8 ? launch_rows<8, 1, 8, 2> : launch_rows<4, 1, 8, 2>);
-            case 2: return run(bits == 8 ? launch_rows<8, 2, 4, 2> : launch_rows<4, 2, 4, 2>);
-            case 3: return run(bits == 8 ? launch_rows<8, 3, 4, 1> : launch_rows<4, 3, 4, 1>);
-            default: return run(bits == 8 ? launch_rows<8, 4, 4, 1> : launch_rows<4, 4, 4, 1>);
+            case 1: return run(bits == 8 ? launch_rows<8, 1, 8> : launch_rows<4, 1, 8>);
+            case 2: return run(bits == 8 ? launch_rows<8, 2, 4> : launch_rows<4, 2, 4>);
+            case 3: return run(bits == 8 ? launch_rows<8, 3, 4> : launch_rows<4, 3, 4>);
+            default: return run(bits == 8 ? launch_rows<8, 4, 4> : launch_rows<4, 4, 4>);
         }
     }
     if (p.wm == 4) return run(bits == 8 ? launch_tile<8, 2, 2, 8, 8, 3> : launch_tile<4, 2, 2, 8, 8, 4>);
