@@ -39,8 +39,8 @@ def test_product_in_large_tiles(M, K, N, bits):
 
 # K cut into slices, up to sixteen, in the register kernel and in tiles of 64, 128 and 256 rows; slices of four
 # chunks and more, of which the last has one to four; and 128-row tiles of four and twelve chunks
-SPLIT = [(5, 25056, 72), (20, 24000, 8), (40, 11008, 8), (60, 6848, 8), (70, 11008, 264), (70, 11040, 264), (150, 6176, 8), (2000, 16416, 520),
-         (2000, 16512, 520), (2000, 17888, 2056), (2000, 17920, 2056), (2390, 512, 1560), (2390, 1504, 1560)]
+SPLIT = [(5, 25056, 72), (20, 24000, 8), (40, 11008, 8), (60, 6848, 8), (70, 11008, 264), (70, 11040, 264),
+         (150, 6176, 8), (2000, 16416, 520), (2000, 16512, 520), (2000, 17888, 2056), (2000, 17920, 2056), (2390, 512, 1560), (2390, 1504, 1560)]
 
 
 @pytest.mark.parametrize("bits", [8, 4])
