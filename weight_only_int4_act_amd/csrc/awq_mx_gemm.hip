@@ -48,7 +48,7 @@ __device__ __forceinline__ floatx4 load4_agent(__amdgpu_buffer_rsrc_t r, uint32_
 // past K or past the last row lies outside its buffer resource: it brings zeros and costs no traffic,
 // so the loop needs no branch between a load and its use.  The wavefronts' sums meet in LDS in a fixed
 // order; with several slices the last workgroup to arrive adds the float32 partials in slice order.
-// 13 x 28672 x 8192: 23 us (5.5 TB/s; with both operands staged in LDS 109 us); 1 x 8192 x 10240: 10 us.
+// 13 x 28672 x 8192: 23 us (5.4 TB/s; with both operands staged in LDS 109 us); 1 x 8192 x 10240: 10 us.
 template <int BITS, int RF, int NW>
 __global__ __launch_bounds__(64 * NW) void k_mx_gemm_rows(
     const uint8_t* __restrict__ xcodes, const uint8_t* __restrict__ xscales, int rows,

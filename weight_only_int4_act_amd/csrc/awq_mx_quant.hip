@@ -73,7 +73,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize(const uint16_t* __restrict_
 // float64, so that no finite row overflows and the rounding is that of the result, in one fixed order:
 // thread, lanes, wavefronts.  Weights, and weights over s, are formed while the row is on its way.
 // Bound by HBM for many rows (7 bytes per element with the residual and 8-bit codes): 4096 x 8192 takes
-// 45 us (5.2 TB/s).  For few by the trip to memory and the sum: one row of 8192 3.1 us, where a kernel
+// 45 us (5.2 TB/s), 49 with s.  For few by the trip to memory and the sum: one row of 8192 3.1 us, where a kernel
 // that read the row twice took 6.3.
 
 // The sum over a wavefront, in every lane: within rows of 16 lanes and then across them.
