@@ -40,7 +40,8 @@ def test_product_in_large_tiles(M, K, N, bits):
 # K cut into slices, up to sixteen, in the register kernel and in tiles of 64, 128 and 256 rows; slices of four
 # chunks and more, of which the last has one to four; and 128-row tiles of four and twelve chunks
 SPLIT = [(5, 25056, 72), (20, 24000, 8), (40, 11008, 8), (60, 6848, 8), (70, 11008, 264), (70, 11040, 264),
-         (150, 6176, 8), (2000, 16416, 520), (2000, 16512, 520), (2000, 17888, 2056), (2000, 17920, 2056), (2390, 512, 1560), (2390, 1504, 1560)]
+         (150, 6176, 8), (2000, 16416, 520), (2000, 16512, 520), (2000, 17888, 2056), (2000, 17920, 2056),
+         (2390, 512, 1560), (2390, 1504, 1560)]
 
 
 @pytest.mark.parametrize("bits", [8, 4])
@@ -169,3 +170,54 @@ def test_rows_do_not_depend_on_their_neighbours():
         xp = xc.view(torch.uint8)[p].contiguous()
         Z = product(xp.view(xc.dtype), xs[p].contiguous(), wc, wsc, M, K, N)
         assert torch.equal(Y[p].view(torch.int16), Z.view(torch.int16))
+
+
+def small_integers(M, K, bits, seed):
+    """Activations -2 .. 2 under scales of 1 (every sum of up to 2^19 products with e2m1 elements is exact)."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    v = torch.randint(-2, 3, (M, K), device=DEV, generator=g, dtype=torch.int8)
+    E = torch.full((M, K // 32), 127, dtype=torch.uint8, device=DEV)
+    if bits == 8:
+        return v.to(torch.float8_e4m3fn), E
+    c = torch.where(v < 0, 8, 0).to(torch.uint8) | (v.abs().to(torch.uint8) << 1)     # 1 -> 2, 2 -> 4
+    return c[:, ::2] | (c[:, 1::2] << 4), E
+
+
+def test_weights_past_32_bits():
+    """Codes of more than 4 GiB: the last columns of a product equal those of their tiles alone."""
+    K, N = 16384, 64 * 8320
+    g = torch.Generator(device=DEV).manual_seed(1)
+    wc = torch.zeros((N // 64, K // 32, 64, 16), dtype=torch.uint8, device=DEV)
+    assert wc.numel() > 2 ** 32
+    wc[-9:] = torch.randint(0, 256, wc[-9:].shape, dtype=torch.uint8, device=DEV, generator=g)
+    ws = torch.full((N // 64, K // 32, 64), 127, dtype=torch.uint8, device=DEV)
+    for M, bits in ((1, 8), (70, 4), (300, 8)):
+        xc, xs = small_integers(M, K, bits, M)
+        Y = product(xc, xs, wc, ws, M, K, N)
+        Z = product(xc, xs, wc[-9:].contiguous(), ws[-9:].contiguous(), M, K, 576)
+        assert torch.equal(Y[:, -576:], Z) and Z.any() and not Y[:, :-576].any()
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_rows_past_32_bits(bits):
+    """Activations, and then a result, of more than 4 GiB: the last rows equal those of a product of their own."""
+    wc, ws, _ = random_weights(16384, 8, 3)
+    ws.fill_(127)
+    M = 2 ** 32 * 8 // bits // 16384 + 70
+    xc, xs = small_integers(64, 16384, bits, 4)
+    big = torch.zeros((M, xc.shape[1]), dtype=torch.uint8, device=DEV)
+    big[-64:] = xc.view(torch.uint8)
+    E = torch.full((M, 512), 127, dtype=torch.uint8, device=DEV)
+    Y = product(big.view(xc.dtype), E, wc, ws, M, 16384, 8)
+    assert torch.equal(Y[-64:], product(xc, xs, wc, ws, 64, 16384, 8)) and not Y[:-64].any() and Y[-64:].any()
+    del big, E
+    M, N = 4099, 64 * 8320
+    wc = torch.randint(0, 256, (N // 64, 4, 64, 16), dtype=torch.uint8, device=DEV,
+                       generator=torch.Generator(device=DEV).manual_seed(5))
+    wc[:, 3:] = 0                                # past K
+    ws = torch.full((N // 64, 4, 64), 127, dtype=torch.uint8, device=DEV)
+    ws[:, 3:] = 0
+    xc, xs = small_integers(M, 96, bits, 6)
+    Y = product(xc, xs, wc, ws, M, 96, N)
+    assert Y.numel() * 2 > 2 ** 32
+    assert torch.equal(Y[-64:], product(xc[-64:].contiguous(), xs[-64:].contiguous(), wc, ws, 64, 96, N)) and Y[-64:].any()

@@ -66,7 +66,8 @@ def test_pack_and_unpack_keep_what_lies_behind_them():
     assert not s.view(2, 4, 16, 4).transpose(2, 3).reshape(2, 4, 64)[1, :, 6:].any()
 
 
-@pytest.mark.parametrize("M,K", [(1, 32), (1, 8192), (3, 96), (5, 2080), (16, 28672), (129, 512), (700, 160)])
+@pytest.mark.parametrize("M,K", [(1, 32), (1, 8192), (3, 96), (5, 2080), (16, 28672), (129, 512), (700, 160),
+                                 (257, 5120), (2051, 512)])
 @pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("scaled", [False, True])
 def test_quantize_matches_the_oracle_bit_for_bit(M, K, bits, scaled):
@@ -114,7 +115,7 @@ def test_gate_at_its_ends():
 
 
 @pytest.mark.parametrize("M,K", [(1, 32), (1, 8192), (2, 96), (7, 5120), (333, 512), (3, 28672), (2, 33024), (600, 64),
-                                 (5, 4064), (9, 16416)])
+                                 (5, 4064), (9, 16416), (300, 5120), (257, 8192), (300, 9088), (257, 16384)])
 @pytest.mark.parametrize("bits,residual,scaled", [(8, True, False), (4, True, True), (8, False, True), (4, False, False)])
 def test_rms_norm(M, K, bits, residual, scaled):
     eps = 1e-5
@@ -226,3 +227,32 @@ def test_offsets_past_32_bits():
     c2, s2 = act_buffers(4, K, 8)
     A.awq_rms_norm(tail, None, w, 1e-5, None, None, None, c2, s2)
     assert torch.equal(codes[-4:].view(torch.uint8), c2.view(torch.uint8)) and torch.equal(scales[-4:], s2)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_more_rows_than_a_grid_has(bits):
+    """A wavefront takes more than two rows where the grid's second dimension would not hold their number."""
+    M, K = 65535 * 8 + 5, 32
+    X = dev(rows(64, K, 1)).repeat(M // 64 + 1, 1)[:M].contiguous()
+    a = A.mx_quantize(X, bits=bits)
+    b = A.mx_quantize(X[:64].contiguous(), bits=bits)
+    c, d = a.codes.view(torch.uint8), b.codes.view(torch.uint8)
+    n = M // 64
+    assert torch.equal(c[:64 * n].view(n, 64, -1), d.expand(n, -1, -1)) and torch.equal(c[64 * n:], d[:M - 64 * n])
+    c, d = a.scales.view(torch.uint8), b.scales.view(torch.uint8)
+    assert torch.equal(c[:64 * n].view(n, 64, -1), d.expand(n, -1, -1)) and torch.equal(c[64 * n:], d[:M - 64 * n])
+
+
+def test_pack_past_32_bits():
+    """Weights of more than 16 GiB, whose codes take more than 4: the last columns pack and unpack as alone."""
+    K, N, n = 16384, 64 * 8320 - 7, 64 * 9 - 7
+    W = torch.zeros((K, N), dtype=torch.bfloat16, device=DEV)
+    assert K * N > 2 ** 33
+    tail = torch.randn((K, n), device=DEV, generator=torch.Generator(device=DEV).manual_seed(1)).bfloat16()
+    W[:, -n:] = tail
+    q, t = A.mx_pack(W), A.mx_pack(tail)
+    del W
+    assert torch.equal(q.codes[-9:], t.codes) and torch.equal(q.scales[-9:].view(torch.uint8), t.scales.view(torch.uint8))
+    assert t.codes.any() and not q.codes[:-9].any()
+    back = A.mx_unpack(q)
+    assert torch.equal(back[:, -n:], A.mx_unpack(t)) and not back[:, :-n].any()
