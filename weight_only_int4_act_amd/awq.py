@@ -469,6 +469,7 @@ _MX_BITS = {torch.float8_e4m3fn: 8, torch.uint8: 4}    # activations: e4m3 [.., 
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream    # the handle alone: torch.cuda.current_stream builds an object
+_current_device = torch._C._cuda_getDevice
 
 
 # The checks below are one expression per tensor where it is right and say what is wrong where it is not:
@@ -478,10 +479,6 @@ def _mx_arg(fn: str, name: str, t: torch.Tensor, dtype, shape) -> int:
     if t.dtype is not dtype or t.shape != shape:
         _expect(fn, name, t, dtype, shape)
     return t.data_ptr()
-
-
-def _mx_opt(fn: str, name: str, t: Optional[torch.Tensor], dtype, shape) -> Optional[int]:
-    return None if t is None else _mx_arg(fn, name, t, dtype, shape)
 
 
 def _mx_scales(fn: str, t: torch.Tensor, shape) -> int:
@@ -501,7 +498,7 @@ def _mx_stream(fn: str, stream, *tensors: Optional[torch.Tensor]) -> int:
             if not t.is_contiguous():
                 raise ValueError("libawq takes contiguous tensors")
             raise ValueError(f"{fn}: tensors on different devices")
-    if dev != torch._C._cuda_getDevice():
+    if dev != _current_device():
         raise ValueError(f"{fn}: tensors are on device {dev}, which is not the current device")
     if stream is None:
         return _raw_stream(dev)
@@ -540,7 +537,7 @@ def awq_mx_pack(W: torch.Tensor, s: Optional[torch.Tensor], codes: torch.Tensor,
     fn = "awq_mx_pack"
     K, N = _matrix(fn, "W", W)
     _mx_rows(fn, K)
-    ps = _mx_opt(fn, "s", s, torch.float32, (K,))
+    ps = None if s is None else _mx_arg(fn, "s", s, torch.float32, (K,))
     pc, pe = _mx_weights(fn, codes, scales, K, N)
     st = _lib.awq_mx_pack(W.data_ptr(), K, N, ps, pc, pe, _mx_stream(fn, stream, W, s, codes, scales))
     if st:
@@ -552,7 +549,7 @@ def awq_mx_unpack(codes: torch.Tensor, scales: torch.Tensor, s: Optional[torch.T
     fn = "awq_mx_unpack"
     K, N = _matrix(fn, "W", W)
     _mx_rows(fn, K)
-    ps = _mx_opt(fn, "s", s, torch.float32, (K,))
+    ps = None if s is None else _mx_arg(fn, "s", s, torch.float32, (K,))
     pc, pe = _mx_weights(fn, codes, scales, K, N)
     st = _lib.awq_mx_unpack(pc, pe, K, N, ps, W.data_ptr(), _mx_stream(fn, stream, W, s, codes, scales))
     if st:
@@ -564,8 +561,8 @@ def awq_mx_quantize(X: torch.Tensor, gate: Optional[torch.Tensor], s: Optional[t
     fn = "awq_mx_quantize"
     M, K = _matrix(fn, "X", X)
     _mx_rows(fn, K)
-    pg = _mx_opt(fn, "gate", gate, torch.bfloat16, (M, K))
-    ps = _mx_opt(fn, "s", s, torch.float32, (K,))
+    pg = None if gate is None else _mx_arg(fn, "gate", gate, torch.bfloat16, (M, K))
+    ps = None if s is None else _mx_arg(fn, "s", s, torch.float32, (K,))
     bits, pc, pe = _mx_acts(fn, codes, scales, M, K)
     st = _lib.awq_mx_quantize(X.data_ptr(), pg, M, K, ps, bits, pc, pe,
                               _mx_stream(fn, stream, X, gate, s, codes, scales))
@@ -579,11 +576,11 @@ def awq_rms_norm(X: torch.Tensor, residual: Optional[torch.Tensor], weight: torc
     fn = "awq_rms_norm"
     M, K = MK = _matrix(fn, "X", X)
     _mx_rows(fn, K, 8 if codes is None else 32)
-    pr = _mx_opt(fn, "residual", residual, torch.bfloat16, MK)
+    pr = None if residual is None else _mx_arg(fn, "residual", residual, torch.bfloat16, MK)
     pw = _mx_arg(fn, "weight", weight, torch.bfloat16, (K,))
-    po = _mx_opt(fn, "residual_out", residual_out, torch.bfloat16, MK)
-    py = _mx_opt(fn, "Y", Y, torch.bfloat16, MK)
-    ps = _mx_opt(fn, "s", s, torch.float32, (K,))
+    po = None if residual_out is None else _mx_arg(fn, "residual_out", residual_out, torch.bfloat16, MK)
+    py = None if Y is None else _mx_arg(fn, "Y", Y, torch.bfloat16, MK)
+    ps = None if s is None else _mx_arg(fn, "s", s, torch.float32, (K,))
     if (codes is None) != (scales is None):
         raise ValueError(f"{fn}: codes and scales are given together or not at all")
     bits, pc, pe = (8, None, None) if codes is None else _mx_acts(fn, codes, scales, M, K)
