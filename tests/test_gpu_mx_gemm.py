@@ -26,7 +26,8 @@ def test_product(M, K, N, bits):
 # 128- and 256-row tiles, with and without a split of K, scales that start on a 4-byte boundary (K a multiple
 # of 128) and that do not, an odd number of 128-channel chunks, ragged rows and columns
 LARGE = [(2459, 224, 1568), (2390, 640, 1560), (1800, 608, 4432), (1576, 384, 6776), (340, 4960, 5560),
-         (388, 5760, 4976), (1659, 7648, 2440), (2345, 8576, 1552), (111, 4288, 16), (84, 4352, 16), (27, 6656, 8)]
+         (388, 5760, 4976), (1659, 7648, 2440), (2345, 8576, 1552), (111, 4288, 16), (84, 4352, 16), (27, 6656, 8),
+         (1576, 736, 6776), (1576, 1024, 6776), (1576, 1152, 6776), (1576, 1280, 6776)]
 
 
 @pytest.mark.parametrize("bits", [8, 4])

@@ -209,11 +209,14 @@ __global__ __launch_bounds__(64 * NW) void k_mx_gemm_rows(
 // c + ST - 1 are issued and the second half's weights are read from LDS; then a barrier says that chunk c
 // is in every wavefront's registers and chunk c + 1 has landed; during the second half the next chunk's
 // activations and first weights are read.  (Both operands of a whole chunk a turn ahead in registers: no
-// faster, and too many of them for 256 rows.)
+// faster, and too many of them for 256 rows.)  128 rows are four wavefronts, one per SIMD (eight with a
+// quarter of the columns each were 2 % slower); 256 rows are eight of 64 rows (four with twice the rows each,
+// which leave no register for the four-turn loop, took 643 instead of 640 us for 4096 x 8192 x 28672 with 8 bits,
+// 438 instead of 424 for 4096 x 28672 x 8192 with 4).
 //
-// What bounds it.  256 rows: the power that the matrix cores take; 4096 x 8192 x 28672 runs at 2.9 PFLOP/s
-// with 8 bits (664 us) and 4096 x 28672 x 8192 at 4.3 with 4 (446 us), the 8-bit products without any
-// transfer or read at 3.0.  64 and 128 rows: one wavefront per SIMD issues everything, and products,
+// What bounds it.  256 rows: the power that the matrix cores take; 4096 x 8192 x 28672 runs at 2.8 to 3.0
+// PFLOP/s with 8 bits (640 to 700 us, with the clock that a card holds) and 4096 x 28672 x 8192 at 4.2 to 4.5
+// with 4 (424 to 459 us), the 8-bit products without any transfer or read at 3.0.  64 and 128 rows: one wavefront per SIMD issues everything, and products,
 // transfers and LDS reads overlap in part (257 x 5120 x 13824, 4 bits, 23 us: products alone 10, transfers
 // alone 10, LDS reads 4, prologue and epilogue 6).
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -271,7 +274,7 @@ __device__ __forceinline__ void mx_rows16(const floatx4 (&v)[4], u32x4 (&out)[2]
 
 // acc += weights x activations in place, in accumulation registers; J: the byte of the weights' scale
 // word.  (From the builtin the compiler makes products that write other registers than they read, and
-// copies 256 accumulators around every turn.)  The compiler does not see a product in this: what the
+// copies the accumulators around every turn.)  The compiler does not see a product in this: what the
 // operands come from must be two instructions away, and results are read after mx_settle.
 template <int BITS>
 using XFrag = std::conditional_t<BITS == 8, i32x8, u32x4>;      // a lane's elements of a row fragment
@@ -310,7 +313,7 @@ struct TileShape {
     static constexpr int kWk = kCols / 64 * 4;                    // 1 KB units of weights per chunk
     static constexpr int kXu = kXk / kWaves, kWu = kWk / kWaves;  // per wavefront
     static constexpr int kData = kXu + kWu;
-    static_assert(kXk % kWaves == 0 && kWk % kWaves == 0 && kWaves == 4, "even shares");
+    static_assert(kXk % kWaves == 0 && kWk % kWaves == 0 && kWaves % 4 == 0, "even shares");
     static constexpr int kStage = (kXk + kWk) * 1024;
     static constexpr int kFs = 4096, kXs = kRows * 16;            // scales of a group: weights, activations
     static constexpr int kScales = ST * kStage, kLds = kScales + 2 * (kFs + kXs);
@@ -374,15 +377,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
 #pragma unroll
     for (int k = 0; k < S::kXu; ++k) xoff[k] = (uint32_t)(ur + k * kUnitRows) * xrow + 16 * piece(k);
 #pragma unroll
-    for (int k = 0; k < S::kWu; ++k) woff[k] = wave * 1024 + lane * 16 + k * wtile;   // block `wave` of column tile k
-    // The scales of the slice's chunks 4q .. 4q+3: one column tile, and 64 rows (the same rows by several wavefronts
-    // where the tile has fewer), per wavefront.  Past K: whatever lies there, or zeros; not used.
+    for (int k = 0; k < S::kWu; ++k) woff[k] = (wave & 3) * 1024 + lane * 16 + (wave / 4 * S::kWu + k) * wtile;   // block wave % 4 of kWu column tiles
+    // The scales of the slice's chunks 4q .. 4q+3: one column tile, and 64 rows (the same ones by several wavefronts
+    // where there are fewer), per wavefront.  Past K: whatever lies there, or zeros; not used.
     constexpr int kParts = S::kRows / 64;
     const int part64 = wave % kParts;
-    const uint32_t foff = wave * ftile + lane * 16 + cb * 256;
+    const uint32_t foff = (wave & 3) * ftile + lane * 16 + cb * 256;
     const uint32_t soff = (((uint32_t)(part64 * 64 + lane) * srow + mis) & ~3u) + cb * 4;
     auto issue_scales = [&](int q) __attribute__((always_inline)) {
-        const uint32_t f = S::kScales + (q & 1) * S::kFs + wave * 1024;
+        const uint32_t f = S::kScales + (q & 1) * S::kFs + (wave & 3) * 1024;
         const uint32_t x = S::kScales + 2 * S::kFs + (q & 1) * S::kXs + part64 * 1024;
         if constexpr (kLdsPoison) {              // debug build: scales of about 2^120 where these will land
             lds[f / 16 + lane] = lds_nan16();
@@ -419,6 +422,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
                                    : i * 64 + (g ^ (2 * (i >> 3))) * 16);
     const uint32_t xh = xl ^ 16;                 // 8 bits: the second piece
     const uint32_t wl = g * kOwn + S::kXu * 1024 + i * 16, fl = g * 64 + i * 4;
+    auto tile_at = [](int c) { return (uint32_t)(c / S::kWu) * 4 * kOwn + (uint32_t)(c % S::kWu) * 1024; };   // column tile
     uint32_t sl[ALIGNED ? 1 : RF];
 #pragma unroll
     for (int rf = 0; rf < (ALIGNED ? 1 : RF); ++rf) {
@@ -465,7 +469,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     auto fetch_w_op = [&](int u, int stage, int half, int k, Half& h) __attribute__((always_inline)) {
         const int j = wn * CF + half * H + (k > 0 ? k - 1 : 0);   // fragment among the tile's 16
         if (k == 0) h.e = *(const uint32_t*)(lb + S::kScales + slot * S::kFs + u * 256 + fl + j / 4 * 1024);
-        else h.w[k - 1] = *(const u32x4*)(lb + stage * S::kStage + wl + j / 4 * 1024 + j % 4 * 256);
+        else h.w[k - 1] = *(const u32x4*)(lb + stage * S::kStage + wl + tile_at(j / 4) + j % 4 * 256);
     };
     auto product = [&](const Acts& a, const uint32_t (&e)[RF], const Half& h, int half, int n) __attribute__((always_inline)) {
         const int q = n / RF, rf = n % RF, j = half * H + q;
@@ -559,34 +563,24 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     constexpr std::false_type kWhole{};
     constexpr std::true_type kEdge{};
     int c = cb;
-    if constexpr (RF * CF < 64) {
-        // Four turns at a time, so that the LDS addresses are constants (60 instructions a turn beside the
-        // products instead of 168: 257 x 5120 x 13824, 4 bits, 28.5 -> 23.0 us); then the last one to four chunks.
-        for (; c + 4 < ce; c += 4) {
-            turn(kWhole, 0, c, xa, xb);
-            turn(kWhole, 1, c + 1, xb, xa);
-            turn(kWhole, 2, c + 2, xa, xb);
-            turn(kWhole, 3, c + 3, xb, xa);
-            join();
-        }
+    // Four turns at a time, so that the LDS addresses are constants (60 instructions a turn beside the
+    // products instead of 168: 257 x 5120 x 13824, 4 bits, 28.5 -> 23.0 us); then the last one to four chunks.
+    for (; c + 4 < ce; c += 4) {
+        turn(kWhole, 0, c, xa, xb);
+        turn(kWhole, 1, c + 1, xb, xa);
+        turn(kWhole, 2, c + 2, xa, xb);
+        turn(kWhole, 3, c + 3, xb, xa);
         join();
-        turn(kEdge, 0, c, xa, xb);
-        turn(kEdge, 1, c + 1, xb, xa);
+    }
+    join();
+    turn(kEdge, 0, c, xa, xb);
+    turn(kEdge, 1, c + 1, xb, xa);
+    join();
+    if (c + 2 < ce) {
         join();
-        if (c + 2 < ce) {
-            join();
-            turn(kEdge, 2, c + 2, xa, xb);
-            turn(kEdge, 3, c + 3, xb, xa);
-            join();
-        }
-    } else {
-        // All accumulation registers are taken, and with more than one loop, or a way out between turns, the
-        // compiler copies them.  64 products a wavefront cover the other instructions of a turn.
-        for (; c < ce; c += 2) {
-            turn(kEdge, (c - cb) & 3, c, xa, xb);
-            turn(kEdge, (c - cb + 1) & 3, c + 1, xb, xa);
-            join();
-        }
+        turn(kEdge, 2, c + 2, xa, xb);
+        turn(kEdge, 3, c + 3, xb, xa);
+        join();
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     auto settled = [&](int rf) __attribute__((always_inline)) {   // one row fragment's results at a time
@@ -681,6 +675,7 @@ constexpr int kMaxSlices = 16;
 //   tiles of 64 wm rows: 1.5 + rounds of one workgroup per CU * (start_us + turns * turn_us), and for joining
 //     slices 2 + .35 per MB of partials; the rounds not below the time in which these kernels stream the
 //     weights (4 TB/s).  E.g. 257 x 5120 x 13824, 4 bits: 23 us with 128 rows a tile, 30 with 64, 41 with 256;
+//     2048 x 8192 x 8192, 8 bits, 101 us with 256 rows, 116 with 128;
 //     128 x 4096 x 4096, 8 bits, 64-row tiles: 14.7, 14.0, 13.4, 13.9 us with 1, 2, 3, 4 slices.
 MxGemmPlan plan_mx_gemm(int64_t M, int64_t K, int64_t N, int bits) {
     MxGemmPlan p{};                              // wm = 0: the register kernel
@@ -703,7 +698,7 @@ MxGemmPlan plan_mx_gemm(int64_t M, int64_t K, int64_t N, int bits) {
         }
         if (M <= 16) return p;
     }
-    static const double start_us[3] = {4, 6, 8.5}, turn_us[2][3] = {{.31, .45, .80}, {.39, .63, 1.18}};   // 4, 8 bits
+    static const double start_us[3] = {4, 6, 8.5}, turn_us[2][3] = {{.31, .45, .72}, {.39, .63, 1.10}};   // 4, 8 bits
     const double stream = 2 + (double)mx_codes_bytes(K, N) / 4e6;
     for (int k = 0; k < 3; ++k) {
         const int wm = 1 << k;
@@ -770,7 +765,7 @@ hipError_t launch_mx_gemm(const uint8_t* xcodes, const uint8_t* xscales, int bit
             default: return run(bits == 8 ? launch_rows<8, 4, 4> : launch_rows<4, 4, 4>);
         }
     }
-    if (p.wm == 4) return run(bits == 8 ? launch_tile<8, 2, 2, 8, 8, 3> : launch_tile<4, 2, 2, 8, 8, 4>);
+    if (p.wm == 4) return run(bits == 8 ? launch_tile<8, 4, 2, 4, 8, 3> : launch_tile<4, 4, 2, 4, 8, 4>);
     if (p.wm == 2) return run(bits == 8 ? launch_tile<8, 2, 2, 4, 8, 4> : launch_tile<4, 2, 2, 4, 8, 4>);
     return run(bits == 8 ? launch_tile<8, 1, 4, 4, 4, 4> : launch_tile<4, 1, 4, 4, 4, 4>);
 }
