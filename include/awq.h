@@ -328,14 +328,15 @@ size_t awq_mx_scales_bytes(int64_t K, int64_t N);
  */
 int awq_mx_pack(const void* W_bf16, int64_t K, int64_t N, const float* s, uint8_t* codes, uint8_t* scales,
                 void* stream);
-/* And back: w_kn = element * 2^(E - 127) / s_k, rounded to bf16 once (exact for s = NULL), for
- * scoring a packing or feeding a bf16 product.
+/* And back: w_kn = element * 2^(E - 127) / s_k in float32 (infinite where it passes the largest
+ * number), rounded to bf16; for s = NULL nothing is rounded.  For scoring a packing or feeding a bf16 product.
  */
 int awq_mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t K, int64_t N, const float* s, void* W_bf16,
                   void* stream);
 
 /* Activations into MX blocks: p = x / s_k, or with a gate p = x * g / (1 + e^-g) / s_k (the input of a
- * gated MLP's last layer: x = up, g = gate), evaluated in float32 (1 / (1 + e^-g) below 2^-126 counts as zero).
+ * gated MLP's last layer: x = up, g = gate), evaluated in float32 (1 / (1 + e^-g) below 2^-126 counts as zero; the
+ * division by s_k is correctly rounded).
  *   X, gate  bf16 [M, K] (gate may be NULL);  s  float32 [K] or NULL (1).
  */
 int awq_mx_quantize(const void* X_bf16, const void* gate_bf16, int64_t M, int64_t K, const float* s, int32_t bits,

@@ -58,15 +58,31 @@ __device__ __forceinline__ uint32_t mx_e2m1x8(const float (&p)[8], uint32_t E) {
     r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, p[6], p[7], scale, 3);
     return r;
 }
-// x / s rounded to float32, for r = mx_recip(s): the quotient's first approximation corrected by its own
-// remainder (three operations where the compiler's division takes ten).  s in [2^-120, 2^120].
+// Division by the input scales, s in [2^-120, 2^120]: x / s rounded to float32.
+//
+// Activations: (float)(x r) with r = 1 / s to 53 bits (the float32 approximation's error e, below 2^-22, taken out to the
+// third order: r (1 + e + e^2)).  r and the product are each off by at most 2^-53 of their size, but a quotient of two
+// 24-bit numbers lies either on a border between two float32 numbers, which only subnormal ones can, or at least 2^-49
+// of its size away from it: the difference is a whole number over the 24-bit divisor times a 25-bit border.  So the result is the
+// rounded quotient, infinite where it overflows, subnormal below 2^-126 (there an exact tie may go to either
+// side), with the sign of a zero.
+__device__ __forceinline__ double mx_recip64(float s) {
+    const double d = s, r = __builtin_amdgcn_rcpf(s), e = fma(-d, r, 1.);
+    return fma(r, fma(e, e, e), r);
+}
+__device__ __forceinline__ float mx_div(float x, double r) { return (float)((double)x * r); }
+// Elements of weights (.5 <= |x| <= 6, or 0): float32 alone, which is faster where a divisor serves few elements.  r is 1 / s
+// rounded (checked on gfx950 for every mantissa), q = x r at most 1.5 of its steps away from the quotient, and
+// its remainder exact: R / S steps, S the 24-bit divisor and R a whole number.  The correction R / S (1 + e), |e| <= 2^-24,
+// misses R / S by less than its distance from every border, at least 1 / (2 S), so the result is the rounded
+// quotient.  (For other x a remainder below 2^-149 would be lost, and a quotient that overflows would become NaN.)
 __device__ __forceinline__ float mx_recip(float s) {
     const float r = __builtin_amdgcn_rcpf(s);
     return fmaf(fmaf(-s, r, 1.f), r, r);
 }
-__device__ __forceinline__ float mx_div(float x, float s, float r) {
+__device__ __forceinline__ float mx_div_element(float x, float s, float r) {
     const float q = x * r;
-    return fmaf(fmaf(-q, s, x), r, q);
+    return fmaf(-fmaf(q, s, -x), r, q);          // signs such that -0 stays -0
 }
 // The largest |p| (as integer bits) of a block held by four consecutive lanes, eight elements each;
 // all four lanes must be active.

@@ -180,9 +180,13 @@ __global__ __launch_bounds__(256) void k_mx_unpack(const uint8_t* __restrict__ c
     for (int c = 0; c < 4; ++c) w[c] = *(const u32x4*)(codes + (base + (n0 % kMxTile) + c) * 16);
     const uint32_t word = transpose_scales(*(const uint32_t*)(scales + base + scale_word(lane)), lane);
     if (n0 >= N) return;
-    float scale[4];
+    float scale[4], power[4];                    // with scales the block's power of two comes after the division
 #pragma unroll
-    for (int c = 0; c < 4; ++c) scale[c] = mx_scale((word >> (8 * c)) & 255u);
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t E = (word >> (8 * c)) & 255u;
+        scale[c] = SCALED && E < 255 ? 1.f : mx_scale(E);
+        power[c] = E == 0 ? 0x1p-127f : mx_scale(min(E, 254u));
+    }
     auto store = [&](int r, uint2 v) {
         uint16_t* row = W + (k0 + r) * N + n0;
         if (n0 + 3 < N) {
@@ -199,13 +203,14 @@ __global__ __launch_bounds__(256) void k_mx_unpack(const uint8_t* __restrict__ c
         for (int h = 0; h < 4; ++h) {
             const int r = 8 * q + 2 * h;
             if constexpr (SCALED) {
+                // .5 <= |element| <= 6: no quotient by s leaves float32, so that only the last product may
                 const float s0 = s[k0 + r], s1 = s[k0 + r + 1], r0 = mx_recip(s0), r1 = mx_recip(s1);
                 float a[4], b[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const f32x2 v = fp4_to_f32(w[c][q], scale[c], h);
-                    a[c] = mx_div(v[0], s0, r0);
-                    b[c] = mx_div(v[1], s1, r1);
+                    a[c] = mx_div_element(v[0], s0, r0) * power[c];
+                    b[c] = mx_div_element(v[1], s1, r1) * power[c];
                 }
                 store(r, uint2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])});
                 store(r + 1, uint2{pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])});

@@ -27,13 +27,10 @@ __global__ __launch_bounds__(256) void k_mx_quantize(const uint16_t* __restrict_
     if (oct >= K / 8) return;                    // K / 8 is a multiple of 4: a block's four lanes leave together
     const int64_t m0 = ((int64_t)blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * R;
     const int64_t m1 = min(m0 + R, M);
-    float sv[8], sr[8];
+    double sr[8];
     if constexpr (SCALED) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            sv[i] = s[oct * 8 + i];
-            sr[i] = mx_recip(sv[i]);
-        }
+        for (int i = 0; i < 8; ++i) sr[i] = mx_recip64(s[oct * 8 + i]);
     }
     for (int64_t m = m0; m < m1; m += kRowsInFlight) {
         u32x4 xv[kRowsInFlight], gv[kRowsInFlight];
@@ -60,7 +57,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize(const uint16_t* __restrict_
             }
             if constexpr (SCALED) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = mx_div(x[i], sv[i], sr[i]);
+                for (int i = 0; i < 8; ++i) x[i] = mx_div(x[i], sr[i]);
             }
             mx_store8<BITS>(x, codes + (m + u) * (BITS == 8 ? K : K / 2), scales + (m + u) * (K / kMxBlock), oct);
         }
