@@ -1,11 +1,12 @@
 """Division by the input scales at the ends of their range, on the GPU, against float64: quotients that
-overflow, that fall below the smallest normal float32, and that lie next to the border of two codes."""
+overflow, that fall below the smallest normal float32, that lie next to the border of two codes, and
+norm weights whose quotient by a scale overflows although the result does not."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import mx_oracle as O
-from tests.mx_util import A, DEV, bf16, dev, f32, host_acts
+from tests.mx_util import A, DEV, EPS32, act_buffers, bf16, check_quantized, dev, f32, host_acts
 
 pytestmark = pytest.mark.gpu
 
@@ -84,6 +85,62 @@ def test_quantize_next_to_borders(bits, tiny):
         assert np.array_equal(E, wE)
         assert np.array_equal(c & (127 if bits == 8 else 7), wc & (127 if bits == 8 else 7)), \
             int((c != wc).sum())
+
+
+def norm_of_ones(w: torch.Tensor, s: np.ndarray, bits: int):
+    """The norm's codes of a row of +-1 (root mean square 1, eps below every rounding): y = +-w exactly."""
+    K = w.numel()
+    X = bf16(np.where(np.arange(K) % 3 == 0, -1.0, 1.0)[None])
+    codes, scales = act_buffers(1, K, bits)
+    A.awq_rms_norm(dev(X), None, dev(w), 1e-30, None, None, torch.from_numpy(s).to(DEV), codes, scales)
+    return f32(X) * f32(w)[None], host_acts(codes, scales)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("tiny", [False, True])
+@pytest.mark.parametrize("K", [512, 4096, 8192, 16384, 32768, 36864])
+def test_norm_codes_next_to_borders(K, bits, tiny):
+    """y / s is the float32 quotient that the quantizer forms, in every kernel of the norm."""
+    p, s = (np.concatenate(v, -1) for v in zip(*[(f32(a), b) for a, b in (border_columns(tiny, i, bits) for i in range(9))]))
+    w, s = bf16(p[0, :K]), s[:K].copy()
+    y, (c, E, _) = norm_of_ones(w, s, bits)
+    wc, wE = O.quantize(quotient(y, s).astype(np.float64), bits)
+    assert np.array_equal(E, wE)
+    assert np.array_equal(c & (127 if bits == 8 else 7), wc & (127 if bits == 8 else 7)), int((c != wc).sum())
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("M,K", [(3, 256), (3, 4096), (300, 8192), (2, 16384), (2, 40000)])
+def test_norm_where_weight_over_scale_overflows(M, K, bits):
+    """|w| / s beyond float32 in every channel, y / s inside it: small rows beside one large element, and zeros."""
+    X = np.full((M, K), 2.0 ** -12)
+    X[:, 0] = 2.0 ** 14
+    X[1] = 0
+    X[:, 64:128] = 0
+    w, s = bf16(np.where(np.arange(K) == 0, 2.0 ** -40, 256.0)), np.full(K, 2.0 ** -120, np.float32)
+    codes, scales = act_buffers(M, K, bits)
+    A.awq_rms_norm(dev(bf16(X)), None, dev(w), 1e-5, None, None, torch.from_numpy(s).to(DEV), codes, scales)
+    y = O.rms_norm(X, None, f32(w).astype(np.float64), 1e-5) / s
+    assert np.abs(y).max() < 2.0 ** 127
+    c, E, _ = host_acts(codes, scales)
+    assert (E < 255).all(), int((E == 255).sum())
+    assert not E[1].any() and not c[1].any() and not E[:, 2:4].any()
+    check_quantized(codes, scales, y, 8 * EPS32, (M, K, bits))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("scale", [2.0 ** -120, 2.0 ** 120])
+def test_norm_at_the_ends_of_the_scales(scale, bits):
+    """The smallest and largest scales with weights to either side: the float32 quotient, subnormal or
+    infinite where it is."""
+    K = 512
+    rng = np.random.default_rng(1)
+    w = (1 + rng.integers(0, 128, K) / 128) * 2.0 ** np.repeat(rng.integers(-16, 12, K // 32), 32)
+    y, (c, E, _) = norm_of_ones(bf16(w), np.full(K, scale, np.float32), bits)
+    q = quotient(y, np.full(K, scale, np.float32)).astype(np.float64)
+    wc, wE = O.quantize(q, bits)
+    assert np.array_equal(E, wE) and (scale > 1 or (wE == 255).any())
+    assert np.array_equal(c & (127 if bits == 8 else 7), wc & (127 if bits == 8 else 7))
 
 
 @pytest.mark.parametrize("bits", [8, 4])

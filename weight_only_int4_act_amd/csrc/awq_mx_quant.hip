@@ -65,13 +65,15 @@ __global__ __launch_bounds__(256) void k_mx_quantize(const uint16_t* __restrict_
 }
 
 // ---------------------------------------------------------------- root-mean-square norm
-// h = x + r, y = h * rsqrt(mean h^2 + eps) * weight; the codes hold y / s.  One pass over the row: T
+// h = x + r, y = h * rsqrt(mean h^2 + eps) * weight; the codes hold y / s, the float32 quotient that the quantizer
+// forms of the same y.  It is a true division: y and s share no exponent (weight / s may overflow where
+// y / s does not), and a divisor serves one element, so that a reciprocal of its own costs as much (one row of 8192 with s:
+// 3.4 us, by 53-bit reciprocals 3.4; 4096 x 8192 50.7 and 54.4).  One pass over the row: T
 // threads of a row keep it in registers (U octets of channels each).  The squares are summed in
 // float64, so that no finite row overflows and the rounding is that of the result, in one fixed order:
-// thread, lanes, wavefronts.  Weights, and weights over s, are formed while the row is on its way.
-// Bound by HBM for many rows (7 bytes per element with the residual and 8-bit codes): 4096 x 8192 takes
-// 45 us (5.2 TB/s), 49 with s.  For few by the trip to memory and the sum: one row of 8192 3.1 us, where a kernel
-// that read the row twice took 6.3.
+// thread, lanes, wavefronts.  Bound by HBM for many rows (7 bytes per element with the residual and 8-bit codes):
+// 4096 x 8192 takes 44 us (5.3 TB/s), 51 with s.  For few by the trip to memory and the sum: one row of 8192
+// 2.7 us, where a kernel that read the row twice took 6.3.
 
 // The sum over a wavefront, in every lane: within rows of 16 lanes and then across them.
 __device__ __forceinline__ double wave_sum_f64(double v) {
@@ -105,34 +107,40 @@ struct NormArgs {
     uint8_t *codes, *scales;
 };
 
-// the outputs of one octet: h, and y formed from w = weight and, for the codes, v = weight / s
+// the weights and divisors of one octet
+template <bool SCALED>
+struct NormCols {
+    u32x4 w;
+    floatx4 s[SCALED ? 2 : 1];
+    __device__ __forceinline__ void load(const NormArgs& a, int64_t oct) {
+        w = *(const u32x4*)(a.weight + oct * 8);
+        if constexpr (SCALED) s[0] = *(const floatx4*)(a.s + oct * 8), s[1] = *(const floatx4*)(a.s + oct * 8 + 4);
+    }
+    // In registers from here on: behind a store, the wait for these loads would be one for the store, too.
+    __device__ __forceinline__ void arrive() {
+        asm volatile("" : "+v"(w));
+        if constexpr (SCALED) asm volatile("" : "+v"(s[0]), "+v"(s[1]));
+    }
+};
+
+// the outputs of one octet: h, y, and the codes of y or of the float32 quotient y / s that the quantizer forms
+template <bool SCALED>
 __device__ __forceinline__ void norm_store(const NormArgs& a, int64_t m, int64_t oct, const float (&h)[8], float rstd,
-                                           const float (&w)[8], const float (&v)[8]) {
+                                           const NormCols<SCALED>& cols) {
     const int64_t at = m * a.K + oct * 8;
     if (a.residual_out) *(u32x4*)(a.residual_out + at) = pack_bf16x8(h);
-    float n[8], y[8];
+    float w[8], y[8];
+    bf16x8_to_f32(cols.w, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) n[i] = h[i] * rstd;
-    if (a.Y) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = n[i] * w[i];
-        *(u32x4*)(a.Y + at) = pack_bf16x8(y);
-    }
+    for (int i = 0; i < 8; ++i) y[i] = h[i] * rstd * w[i];
+    if (a.Y) *(u32x4*)(a.Y + at) = pack_bf16x8(y);
     if (!a.codes) return;
+    if constexpr (SCALED) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = n[i] * v[i];
+        for (int i = 0; i < 8; ++i) y[i] /= cols.s[i / 4][i % 4];
+    }
     if (a.bits == 8) mx_store8<8>(y, a.codes + m * a.K, a.scales + m * (a.K / kMxBlock), oct);
     else mx_store8<4>(y, a.codes + m * (a.K / 2), a.scales + m * (a.K / kMxBlock), oct);
-}
-__device__ __forceinline__ void norm_weights(const NormArgs& a, int64_t oct, float (&w)[8], float (&v)[8]) {
-    bf16x8_to_f32(*(const u32x4*)(a.weight + oct * 8), w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = w[i];
-    if (a.s) {
-        const floatx4 s0 = *(const floatx4*)(a.s + oct * 8), s1 = *(const floatx4*)(a.s + oct * 8 + 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = w[i] * __builtin_amdgcn_rcpf(i < 4 ? s0[i & 3] : s1[i & 3]);
-    }
 }
 __device__ __forceinline__ void norm_load(const NormArgs& a, int64_t m, int64_t oct, u32x4& x, u32x4& r) {
     x = *(const u32x4*)(a.X + m * a.K + oct * 8);
@@ -152,7 +160,7 @@ __device__ __forceinline__ double norm_square(const NormArgs& a, const u32x4& x,
 }
 
 // T threads per row (64 or more), U octets per thread, max(1, 256 / T) rows per workgroup.
-template <int T, int U>
+template <int T, int U, bool SCALED>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void k_rms_norm(NormArgs a) {
     constexpr int kRows = T < 256 ? 256 / T : 1, NW = T / 64;
     __shared__ double part[NW];
@@ -162,14 +170,16 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_rms_norm(NormArgs a) {
     if (T < 256 && m >= a.M) return;             // T = 64: whole wavefronts, no barrier below
     const int64_t octs = a.K / 8;
     u32x4 x[U], r[U];
-    float w[U][8], v[U][8], h[U][8];
+    float h[U][8];
+    NormCols<SCALED> cols[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t oct = min((int64_t)(u * T + t), octs - 1);
         norm_load(a, m, oct, x[u], r[u]);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) norm_weights(a, min((int64_t)(u * T + t), octs - 1), w[u], v[u]);
+    for (int u = 0; u < U; ++u) cols[u].load(a, min((int64_t)(u * T + t), octs - 1));
+    __builtin_amdgcn_sched_barrier(0);           // every load is on its way before the first is waited for
     double sum = 0.;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -177,6 +187,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_rms_norm(NormArgs a) {
         if (u * T + t < octs) sum += q;
     }
     sum = wave_sum_f64(sum);
+#pragma unroll
+    for (int u = 0; u < U; ++u) cols[u].arrive();
     if constexpr (NW > 1) {
         if ((t & 63) == 0) part[t >> 6] = sum;
         __syncthreads();
@@ -187,10 +199,11 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_rms_norm(NormArgs a) {
     const float rstd = rsqrt_f64(sum * a.inv_k + a.eps);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-        if (u * T + t < octs) norm_store(a, m, u * T + t, h[u], rstd, w[u], v[u]);
+        if (u * T + t < octs) norm_store(a, m, u * T + t, h[u], rstd, cols[u]);
 }
 
 // Rows of more than 32768 channels: a workgroup reads its row twice.
+template <bool SCALED>
 __global__ __launch_bounds__(1024) void k_rms_norm_long(NormArgs a) {
     __shared__ double part[16];
     lds_poison_start(&part[0], 16);
@@ -210,18 +223,21 @@ __global__ __launch_bounds__(1024) void k_rms_norm_long(NormArgs a) {
     const float rstd = rsqrt_f64(sum * a.inv_k + a.eps);
     for (int64_t oct = threadIdx.x; oct < octs; oct += 1024) {
         u32x4 x, r;
-        float h[8], w[8], v[8];
+        float h[8];
+        NormCols<SCALED> cols;
         norm_load(a, m, oct, x, r);
         norm_square(a, x, r, h);
-        norm_weights(a, oct, w, v);
-        norm_store(a, m, oct, h, rstd, w, v);
+        cols.load(a, oct);
+        norm_store(a, m, oct, h, rstd, cols);
     }
 }
 
 template <int T, int U>
 hipError_t norm(const NormArgs& a, hipStream_t st) {
     constexpr int rows = T < 256 ? 256 / T : 1;
-    k_rms_norm<T, U><<<(unsigned)((a.M + rows - 1) / rows), T < 256 ? 256 : T, 0, st>>>(a);
+    const dim3 grid((unsigned)((a.M + rows - 1) / rows)), block(T < 256 ? 256 : T);
+    if (a.s) k_rms_norm<T, U, true><<<grid, block, 0, st>>>(a);
+    else k_rms_norm<T, U, false><<<grid, block, 0, st>>>(a);
     return hipGetLastError();
 }
 
@@ -265,7 +281,8 @@ hipError_t launch_rms_norm(const uint16_t* X, const uint16_t* residual, const ui
     if (octs <= 1024) return few ? norm<1024, 1>(a, st) : norm<512, 2>(a, st);
     if (octs <= 2048) return few ? norm<1024, 2>(a, st) : norm<512, 4>(a, st);
     if (octs <= 4096) return norm<1024, 4>(a, st);
-    k_rms_norm_long<<<(unsigned)M, 1024, 0, st>>>(a);
+    if (a.s) k_rms_norm_long<true><<<(unsigned)M, 1024, 0, st>>>(a);
+    else k_rms_norm_long<false><<<(unsigned)M, 1024, 0, st>>>(a);
     return hipGetLastError();
 }
 
