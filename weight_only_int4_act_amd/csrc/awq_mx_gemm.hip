@@ -226,27 +226,19 @@ __device__ __forceinline__ i32x4 byte_rsrc(const void* base, uint32_t bytes) {
                  (int)(__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)) & 0xffff),
                  (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000};
 }
-// 16 bytes per lane from byte voff + soff of the resource to LDS address lds + 16 * lane; a lane whose
-// voff is at or past the resource's end brings zeros.  M0 holds the LDS address; nothing else in
-// these kernels uses it, and a wait state lies between its write and its use.
-__device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+// 16 bytes per lane from byte voff + soff of the resource to LDS address lds + off + 16 * lane (off a constant); a lane
+// whose voff is at or past the resource's end brings zeros.  M0 holds the LDS address: every transfer writes it
+// itself, with a wait state before its use, and leaves nothing there for another statement.
+__device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds, int off) {
+#ifdef __HIP_DEVICE_COMPILE__                   // the host pass does not know the registers
     asm volatile(
-        "s_mov_b32 m0, %3\n\t"
+        "s_add_u32 m0, %3, %4\n\t"
         "s_nop 0\n\t"
         "buffer_load_dwordx4 %0, %1, %2 offen lds"
         :
-        : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(soff)), "s"(__builtin_amdgcn_readfirstlane(lds))
-        : "memory");
-}
-// The same to the next 1 KB after the last dma16.
-__device__ __forceinline__ void dma16_next(i32x4 rsrc, uint32_t voff, uint32_t soff) {
-    asm volatile(
-        "s_add_u32 m0, m0, 0x400\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %0, %1, %2 offen lds"
-        :
-        : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(soff))
+        : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(soff)), "s"(__builtin_amdgcn_readfirstlane(lds)), "i"(off)
         : "memory", "scc");
+#endif
 }
 
 // The results of four 16-column fragments for 16 rows (lane (i, g): row i, columns 16j + 4g .. + 3 of
@@ -392,8 +384,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
             lds[x / 16 + lane] = lds_nan16();
             lds_write_fence();
         }
-        dma16(fr, foff + q * 1024, 0, base + f);
-        dma16(sr, soff + q * 16, 0, base + x);
+        dma16(fr, foff + q * 1024, 0, base + f, 0);
+        dma16(sr, soff + q * 16, 0, base + x, 0);
     };
     // transfer k of chunk c's batch; for a chunk past the slice the resources are empty, which brings zeros
     // (no traffic), so that the counted waits stay the same
@@ -407,9 +399,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
         const i32x4 xc = {xr[0], xr[1], in ? xr[2] : 0, xr[3]}, wc = {wr[0], wr[1], in ? wr[2] : 0, wr[3]};
         const uint32_t past = ALIGNED || xk[k & 1] < Kc - c * kMxChunk ? 0 : kOutside;   // a piece past K
         const uint32_t sx = c * (BITS == 8 ? 128 : 64);
-        if (k == 0) dma16(xc, xoff[0] | past, sx, base + st);
-        else if (k < S::kXu) dma16_next(xc, xoff[k] | past, sx);
-        else dma16_next(wc, woff[k - S::kXu], c * 4096);
+        const uint32_t to = base + (ST == 4 ? wave * kOwn : st);
+        const int off = (ST == 4 ? stage * S::kStage : 0) + k * 1024;
+        if (k < S::kXu) dma16(xc, xoff[k] | past, sx, to, off);
+        else dma16(wc, woff[k - S::kXu], c * 4096, to, off);
     };
 
     // LDS byte offsets of this lane's operands within a stage; of its weight scales and of its scale byte of
