@@ -297,6 +297,10 @@ __device__ __forceinline__ void mx_pin(floatx4& acc) {
 template <int BITS>
 __device__ __forceinline__ void mx_settle() { asm volatile("s_nop %0" ::"n"(BITS == 8 ? 13 : 9)); }
 
+// What the debug build fills LDS with before a transfer: scale bytes of 255 and e4m3 elements of 0xff are NaN, e2m1 elements
+// of 0xf are -6, far from any data's sums.
+__device__ __forceinline__ u32x4 mx_poison() { return u32x4{~0u, ~0u, ~0u, ~0u}; }
+
 template <int BITS, int WM, int WN, int RF, int CF, int ST>
 struct TileShape {
     static constexpr int kWaves = WM * WN, kRows = 16 * RF * WM, kCols = 16 * CF * WN;
@@ -336,8 +340,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     const int chunks = (int)(kb_all / 4), per = ((chunks + nz - 1) / nz + 1) / 2 * 2;
     const int cb = min(z * per, chunks), ce = min(cb + per, chunks);
     const int64_t row0 = (int64_t)rt * S::kRows, t0 = (int64_t)ct * 4, nt = (N + 63) / 64;
-    const int rows = (int)min<int64_t>(S::kRows, M - row0);       // rows past the last repeat it
-    const int cts = (int)min<int64_t>(4, nt - t0);                // column tiles past the last repeat it
+    const int rows = (int)min<int64_t>(S::kRows, M - row0);       // past the last row and
+    const int cts = (int)min<int64_t>(4, nt - t0);                // column tile: zeros
     const uint32_t xrow = (uint32_t)(BITS == 8 ? K : K / 2), srow = (uint32_t)(K / kMxBlock);
     const uint32_t wtile = (uint32_t)kb_all * 1024, ftile = (uint32_t)kb_all * 64;
     const int Kc = (int)K;
@@ -379,9 +383,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     auto issue_scales = [&](int q) __attribute__((always_inline)) {
         const uint32_t f = S::kScales + (q & 1) * S::kFs + (wave & 3) * 1024;
         const uint32_t x = S::kScales + 2 * S::kFs + (q & 1) * S::kXs + part64 * 1024;
-        if constexpr (kLdsPoison) {              // debug build: scales of about 2^120 where these will land
-            lds[f / 16 + lane] = lds_nan16();
-            lds[x / 16 + lane] = lds_nan16();
+        if constexpr (kLdsPoison) {              // debug build: where these will land, scales that make every value NaN
+            lds[f / 16 + lane] = mx_poison();
+            lds[x / 16 + lane] = mx_poison();
             lds_write_fence();
         }
         dma16(fr, foff + q * 1024, 0, base + f, 0);
@@ -392,8 +396,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm_tile(
     auto issue_op = [&](int c, int stage, int k) __attribute__((always_inline)) {
         const bool in = c < ce;
         const uint32_t st = stage * S::kStage + wave * kOwn;
-        if constexpr (kLdsPoison) {              // debug build: NaN where this transfer will land
-            lds[st / 16 + k * 64 + lane] = lds_nan16();
+        if constexpr (kLdsPoison) {              // debug build: e4m3 NaN, or e2m1's -6 in every element (it has no NaN)
+            lds[st / 16 + k * 64 + lane] = mx_poison();
             lds_write_fence();
         }
         const i32x4 xc = {xr[0], xr[1], in ? xr[2] : 0, xr[3]}, wc = {wr[0], wr[1], in ? wr[2] : 0, wr[3]};
