@@ -683,6 +683,8 @@ def rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual:
 def mx_gemm(a: MxActs, q: MxWeights, stream=None) -> torch.Tensor:
     """The product of MX activations (divided by q.s when they were quantized) and MX weights."""
     M = a.codes.shape[0]
+    if a.scales.shape[-1] * 32 != q.K:              # the weights' buffers are padded and would not tell
+        raise ValueError(f"mx_gemm: activations of {a.scales.shape[-1] * 32} channels, weights of {q.K}")
     bits = _MX_BITS.get(a.codes.dtype, 0)
     with _allocating_on(stream):
         Y = torch.empty((M, q.N), dtype=torch.bfloat16, device=a.codes.device)
