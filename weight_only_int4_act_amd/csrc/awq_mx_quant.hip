@@ -12,8 +12,8 @@ __device__ __forceinline__ u32x4 pack_bf16x8(const float (&v)[8]) {
 
 // ---------------------------------------------------------------- quantizer
 // p = x, or x g / (1 + e^-g), divided by s per channel.  Bound by HBM: 2 (4 with a gate) bytes read and
-// 1.03 or 0.53 written per element; 8192 x 11008 with a gate, 8 bits, takes 84 us (5.4 TB/s), and
-// 16 x 28672 2.7 us, of which a launch is 2.  A workgroup takes 64 octets of channels (512) and 4 R rows; a
+// 1.03 or 0.53 written per element; 8192 x 11008 with a gate, 8 bits, takes 83 us (5.4 TB/s), and
+// 16 x 28672 2.4 us, of which a launch is 2.  A workgroup takes 64 octets of channels (512) and 4 R rows; a
 // wavefront walks its R rows with the reciprocals of s in registers, two rows' loads in flight.
 // Four consecutive lanes hold a block.
 constexpr int kRowsInFlight = 2;
@@ -245,11 +245,12 @@ hipError_t norm(const NormArgs& a, hipStream_t st) {
 
 hipError_t launch_mx_quantize(const uint16_t* X, const uint16_t* gate, int64_t M, int64_t K, const float* s, int bits,
                               uint8_t* codes, uint8_t* scales, hipStream_t st) {
-    // Rows per wavefront: one while that gives no more than two workgroups per CU (64 x 8192: 2.36 us, with
-    // two rows 2.62), else two (257 x 5120, 4 bits: 2.65 us, with one row 2.90; 8192 x 11008 with a gate: 83 us,
-    // 88 with four rows, 92 with eight).
+    // Rows per wavefront (on inputs that no cache holds).  Two where a wavefront has reciprocals of s to share and one
+    // row gives more than two workgroups per CU (4096 x 8192, 8 bits: 23.4 us, with one row 29.1; 8192 x 11008 with a gate: 93 and
+    // 109; but 64 x 8192: 2.58 and 2.32), or lanes to spare (100000 x 96: 18.1 and 24.1); else one (4096 x 8192,
+    // 8 bits, without s: 20.6 us, with two rows 21.9; 257 x 5120, 4 bits: 2.54 and 2.70; 8192 x 11008 with a gate: 83.1 and 85.6).
     const int64_t cols = (K / 8 + 63) / 64, quads = (M + 3) / 4;
-    int R = cols * quads > 2 * kNumXcd * kCusPerXcd ? 2 : 1;
+    int R = (s || K < 512) && cols * quads > 2 * kNumXcd * kCusPerXcd ? 2 : 1;
     while ((quads + R - 1) / R > 65535) R *= 2;
     const dim3 grid((unsigned)cols, (unsigned)((quads + R - 1) / R));
     auto go = [&](auto kernel) {
