@@ -214,11 +214,13 @@ __global__ __launch_bounds__(64 * NW) void k_mx_gemm_rows(
 // which leave no register for the four-turn loop, took 643 instead of 640 us for 4096 x 8192 x 28672 with 8 bits,
 // 438 instead of 424 for 4096 x 28672 x 8192 with 4).
 //
-// What bounds it.  256 rows: the power that the matrix cores take; 4096 x 8192 x 28672 runs at 2.8 to 3.0
-// PFLOP/s with 8 bits (640 to 700 us, with the clock that a card holds) and 4096 x 28672 x 8192 at 4.2 to 4.5
-// with 4 (424 to 459 us), the 8-bit products without any transfer or read at 3.0.  64 and 128 rows: one wavefront per SIMD issues everything, and products,
-// transfers and LDS reads overlap in part (257 x 5120 x 13824, 4 bits, 23 us: products alone 10, transfers
-// alone 10, LDS reads 4, prologue and epilogue 6).
+// What bounds it.  256 rows: the clock, which falls from 2.4 to 1.6-1.95 GHz under this load, and, within the cycles left,
+// how far LDS reads, transfers and barriers hide behind products.  4096 x 8192 x 28672, 8 bits: 640 to 700 us (2.8 to 3.0
+// PFLOP/s), the matrix cores busy in 0.72 of the cycles; the products alone, on operands that stay in registers, 490 to 512.
+// 4096 x 28672 x 8192, 4 bits: 424 to 459 us (4.2 to 4.5 PFLOP/s), busy in 0.57 (a product takes half the cycles,
+// its LDS reads do not); products alone 302 to 316.  64 and 128 rows: one wavefront per SIMD issues everything, and
+// products, transfers and LDS reads overlap in part (257 x 5120 x 13824, 4 bits, 23 us where a cache holds the
+// weights, 25.8 where none does: products alone 10, transfers alone 10, LDS reads 4, prologue and epilogue 6).
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ i32x4 byte_rsrc(const void* base, uint32_t bytes) {
     const uint64_t a = (uint64_t)(uintptr_t)base;

@@ -9,11 +9,12 @@ namespace {
 // A thread owns four adjacent columns of one block (32 rows), so that a wavefront reads 512
 // contiguous bytes of each row; a workgroup's four wavefronts take the four blocks of one 128-row
 // chunk.  Bound by HBM: 2 bytes read and 0.53 written per weight; 8192 x 28672 with scales takes
-// 119 us (5.0 TB/s; a copy of 2 GiB reaches 4.9), 4096 x 4096 9.8 us.  The rows stay packed in
+// 119 us (5.0 TB/s; a copy of 2 GiB reaches 4.9; right behind an unpack, whose output is still being written
+// back, 147), 4096 x 4096 11.7 us.  The rows stay packed in
 // registers (64 of them, all loads in flight at once): without scales the maximum is taken on packed
 // bf16 bits and pairs go straight into the conversion; with scales the products are formed twice,
 // for the maximum and for the conversion, which is cheaper than holding them.  Both directions with
-// scales took 466 us when each row was converted by itself, 241 us now.
+// scales, one after the other, took 466 us when each row was converted by itself, 241 us now.
 //
 // Tile t holds columns 64t .. 64t+63: codes[(t * kb_all + kb) * 64 + c] is the 16-byte block of column
 // 64t + c, and scale byte 4i + j of (t, kb) belongs to column 64t + 16j + i, so that one 4-byte load
@@ -163,7 +164,7 @@ __global__ __launch_bounds__(256) void k_mx_pack(const uint16_t* __restrict__ W,
 }
 
 // The reverse: a thread reads four adjacent 16-byte blocks and writes four columns of 32 rows.  Bound by
-// HBM, too: 8192 x 28672 with scales 122 us (4.9 TB/s), 4096 x 4096 8.2 us.
+// HBM, too: 8192 x 28672 with scales 124 us (4.8 TB/s), without 118; 4096 x 4096 12.3 and 9.6 us.
 template <bool SCALED>
 __global__ __launch_bounds__(256) void k_mx_unpack(const uint8_t* __restrict__ codes,
                                                    const uint8_t* __restrict__ scales, int64_t K, int64_t N,

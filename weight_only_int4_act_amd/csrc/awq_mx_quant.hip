@@ -271,16 +271,16 @@ hipError_t launch_rms_norm(const uint16_t* X, const uint16_t* residual, const ui
     const NormArgs a{X, residual, weight, M, K, (double)eps, 1. / (double)K, residual_out, Y, s, bits, codes, scales};
     const int64_t octs = K / 8;
     // As many threads as the row has octets, because the sum's chain of float64 additions grows with the
-    // octets of a thread; but two or four octets for the longer rows once every CU has a row, so that several
-    // rows share a CU.  256 x 8192: 4.44 us with one octet, 4.62 with two; 4096 x 8192: 53.2 and 45.0, 50.3 with
-    // four; 200 x 16384: 7.2 us with two, 7.9 with four; 4096 x 16384: 97 and 92; 2000 x 4096: 10.8 us with one,
-    // 11.5 with two.
+    // octets of a thread (2000 x 4096: 13.7 us with one octet, 13.9 with two); but two octets for 1024 once every CU has a
+    // row, so that several rows share a CU (4096 x 8192: 43.5 us, with one octet 47.0, with four 44.4; 256 x 8192:
+    // 5.65 us with one, 5.69 with two).  Longer rows take 1024 threads (4096 x 16384: 85.7 us with two octets, 87.1 with 512
+    // threads and four).
     const bool few = M <= kNumXcd * kCusPerXcd;
     if (octs <= 64) return norm<64, 1>(a, st);
     if (octs <= 256) return norm<256, 1>(a, st);
     if (octs <= 512) return norm<512, 1>(a, st);
     if (octs <= 1024) return few ? norm<1024, 1>(a, st) : norm<512, 2>(a, st);
-    if (octs <= 2048) return few ? norm<1024, 2>(a, st) : norm<512, 4>(a, st);
+    if (octs <= 2048) return norm<1024, 2>(a, st);
     if (octs <= 4096) return norm<1024, 4>(a, st);
     if (a.s) k_rms_norm_long<true><<<(unsigned)M, 1024, 0, st>>>(a);
     else k_rms_norm_long<false><<<(unsigned)M, 1024, 0, st>>>(a);
