@@ -313,8 +313,9 @@ int awq_w4a16_gemm_noalloc(const void* X_bf16, int64_t M, const float* s, const 
  *                Blocks past K and columns past N hold zeros (codes and scales), written by
  *                awq_mx_pack and relied on by awq_mx_gemm.
  * K must be a multiple of 32 (of 8 for a norm without codes).  bits is 8 or 4 (AWQ_ERR_UNSUPPORTED
- * otherwise).  s, where it may be NULL, is float32 [K] with values in [2^-120, 2^120]: the input scales of an
- * AWQ search; weights are multiplied by it and activations divided.  Outputs must not overlap
+ * otherwise).  s, where it may be NULL, is float32 [K] with values in [2^-120, 2^120]: input scales;
+ * weights are multiplied by it and activations divided.  (An alpha search scores the integer quantizer; its s*
+ * seldom lowers the error of these formats, which need no scales.)  Outputs must not overlap
  * inputs or each other (AWQ_ERR_INVALID_ARG) unless a paragraph below says so.  Codes, weights'
  * scales, s and bf16 activations are 16-byte aligned; W needs only its own type's alignment.
  */

@@ -634,7 +634,7 @@ class MxActs:
 
 
 def mx_pack(W: torch.Tensor, s: Optional[torch.Tensor] = None, stream=None) -> MxWeights:
-    """Allocate and pack one layer's weights (s: the s* of a search over the layer, or None)."""
+    """Allocate and pack one layer's weights (s: input scales by which the activations will be divided, or None)."""
     K, N = W.shape
     kb, nt = -(-K // 128) * 4, -(-N // 64)
     with _allocating_on(stream):
