@@ -14,7 +14,10 @@
  *      the power-of-two per-group greedy of [P4];
  *   5. the microscaled (MX) operators: 4-bit floating-point weights with a power-of-two scale
  *      per 32 channels, activations quantized to 8 or 4 bits in the same way (on their own,
- *      behind a gate, or as the output of a root-mean-square norm), and their product.
+ *      behind a gate, or as the output of a root-mean-square norm), and their product;
+ *   6. the attention half of a block in 8 bits ([P4] LayerQuantPolicy: attention in 8 bits, MLP in 4):
+ *      the product in 8-bit floating point with float32 scales for blocks of 128, q|k|v normed, rotated
+ *      and appended to an 8-bit cache, and the attention that reads that cache.
  *
  * Sources (page title -- section), for the definitions cited below:
  *   [P1] "AWQ (Activation-aware Weight Quantization)" (compassingai.com)
@@ -51,7 +54,8 @@ extern "C" {
 #define AWQ_OK 0
 #define AWQ_ERR_INVALID_ARG (-1) /* null/misaligned pointer, non-positive size, K % group_size != 0, ... */
 #define AWQ_ERR_UNSUPPORTED (-2) /* w_bit != 4, group_size not in {32, 64, 128}, n_grid outside [2, 64],
-                                    clip_ratio outside [0, 1], MX bits not 8 or 4 */
+                                    clip_ratio outside [0, 1], MX bits not 8 or 4, a cache's head size or
+                                    block of tokens that is not one of those listed there */
 #define AWQ_ERR_WORKSPACE (-3)   /* workspace smaller than the matching *_workspace_size() */
 #define AWQ_ERR_HIP (-4)         /* a HIP call failed; awq_last_hip_error() holds its code */
 #define AWQ_ERR_SCRATCH (-5)     /* awq_w4a16_gemm_noalloc: the call needs more than its fixed scratch */
@@ -376,6 +380,114 @@ size_t awq_mx_gemm_workspace_size(int64_t M, int64_t K, int64_t N, int32_t bits)
 int awq_mx_gemm(const uint8_t* xcodes, const uint8_t* xscales, int32_t bits, int64_t M, const uint8_t* codes,
                 const uint8_t* scales, int64_t K, int64_t N, void* Y_bf16, void* workspace, size_t ws_bytes,
                 void* stream);
+
+/* ---------------------------------------------------------------- 8-bit products with scales per 128
+ * Elements are e4m3 (largest 448).  A group holds one float32 scale s: 128 consecutive channels of one
+ * row of activations, or 128 channels x 128 output columns of weights.  Quantizing a group of float32
+ * numbers p:
+ *   s = max(max|p|, 448 * 2^-120) / 448;  element = p / s rounded to nearest even, where the float32
+ *   quotient is off by at most 2 units in its last place.
+ * A group that holds an infinity or a NaN has s = NaN and zero elements: every value it stands for is
+ * NaN, and so is every product with it.  The value of an element is element * s.
+ *
+ * Layouts (Kc = ceil(K/128), Nt = ceil(N/64), Nb = ceil(N/128)):
+ *   activations  codes uint8 [M, K], scales float32 [M, Kc].
+ *   weights      codes uint8 [Nt, Kc, 8, 64, 16]: byte b of (t, c, 2f + h, 16g + i), f < 4, h < 2, g < 4, i < 16, is
+ *                channel 128c + 64h + 16g + b of output column 64t + 16f + i (the order in which the matrix
+ *                core's lanes take them); zero past K and past N, written by awq_fp8_pack and relied on by
+ *                awq_fp8_gemm.  scales float32 [Nb, Kc].
+ *                Codes [N, K] of a checkpoint, padded with zeros to [64 Nt, 128 Kc], come into this order as
+ *                view(Nt, 4, 16, Kc, 2, 4, 16) permuted to (0, 3, 1, 4, 5, 2, 6); their scales [Nb, Kc] stay.
+ * K must be a multiple of 16.  Codes and bf16 arrays are 16-byte aligned, scales 4-byte; W of awq_fp8_pack
+ * needs only its own type's alignment.  Outputs must not overlap inputs or each other (AWQ_ERR_INVALID_ARG).
+ */
+/* Bytes of packed weights and number of their scales (0 for bad sizes): K a multiple of 16, at most
+ * 65535 * 128; K * N at most 2^36. */
+size_t awq_fp8_codes_bytes(int64_t K, int64_t N);
+size_t awq_fp8_scales_count(int64_t K, int64_t N);
+
+/* Weights into groups of 128 x 128.  W bf16 [K, N], any N. */
+int awq_fp8_pack(const void* W_bf16, int64_t K, int64_t N, uint8_t* codes, float* scales, void* stream);
+
+/* Activations into groups of 128 channels: p = x, or with a gate p = x * g / (1 + e^-g), in float32 (1 / (1 + e^-g) below
+ * 2^-126 counts as zero).  X, gate  bf16 [M, K] (gate may be NULL). */
+int awq_fp8_quantize(const void* X_bf16, const void* gate_bf16, int64_t M, int64_t K, uint8_t* codes, float* scales,
+                     void* stream);
+
+/* Y[m, n] = sum_c sx[m, c] sw[n/128, c] sum_{k in group c} xcode_mk wcode_kn: a group's sum on the matrix cores,
+ * the groups' sums times their two scales added in float32, bf16 out.  Within a group the matrix core adds
+ * the products of eight consecutive channels with 13 binary places below the largest (about 1e-4 of a typical
+ * sum, under bf16's rounding).  The product of two scales must be a float32 number (within 2^-126 .. 2^128) where a
+ * result is to be more than that underflow or overflow.
+ *   Y  bf16 [M, N], N % 8 == 0, N at most 4194304, M at most 65535 * 16.
+ *   workspace >= awq_fp8_gemm_workspace_size(M, K, N) bytes (the size may be 0), 256-byte aligned, with
+ *   arrival counters in its first 64 KiB under the rules of awq_w4a16_gemm's: one workspace serves any sequence of
+ *   calls of the products and of awq_attention, ordered by the caller, replays of captured graphs included.
+ */
+size_t awq_fp8_gemm_workspace_size(int64_t M, int64_t K, int64_t N);
+int awq_fp8_gemm(const uint8_t* xcodes, const float* xscales, int64_t M, const uint8_t* codes, const float* scales,
+                 int64_t K, int64_t N, void* Y_bf16, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- 8-bit cache and its attention
+ * The cache holds K and V of `blocks` blocks of T tokens for Hk heads of D numbers, in e4m3, with one
+ * power-of-two scale each for K and V per block and head: a byte E stands for 2^(E - 127), the least E >= 0 under which
+ * the block's largest number is at most 448.  E = 255 marks a block (of one head) that an infinity or a NaN has
+ * been appended to, as K or as V: attention gives NaN to every query that sees one of its tokens.
+ *   k_codes  uint8 [blocks, Hk, T, D]
+ *   v_codes  uint8 [blocks, Hk, T/16, D, 16]: the 16 tokens of a group side by side (the order of the
+ *            second product's operand)
+ *   scales   uint8 [blocks, Hk, 2]: K's and V's E
+ * T is 16, 32, 64 or 128, D 64 or 128 (AWQ_ERR_UNSUPPORTED otherwise); codes 16-byte aligned, scales 2-byte.
+ *
+ * Sequences (device arrays; n_seq of them):
+ *   cu      int32 [n_seq + 1]: the new tokens of sequence b are rows cu[b] .. cu[b+1] - 1 of q|k|v, of q and of the
+ *           attention's output; not decreasing.  Rows that no sequence has are left as they were.
+ *   length  int32 [n_seq]: the sequence's tokens, the new ones included: the i-th of n new ones has position
+ *           length - n + i.
+ *   table   int32 [n_seq, width]: tokens T j .. T j + T - 1 of sequence b are in block table[b, j].
+ *   max_q   at least the largest number of new tokens of one sequence (a host number; it sizes the launch).
+ * The arrays are read on the device and may change between replays of a captured graph.  Values that fit
+ * nothing are taken as follows, without a fault: a cu below the one before it or past the rows: as that bound; a
+ * block outside [0, blocks) or past the table's width: its tokens are neither stored nor seen; a token at a
+ * negative position (length below the new tokens): not stored, its q and its output are zero; rows past
+ * max_q: left out.
+ */
+
+/* q|k|v of new tokens: q and k normed per head and rotated, q out in bf16, k and v into the cache.
+ *   qkv       bf16 [M, (Hq + 2 Hk) D]: Hq heads of q, Hk of k, Hk of v.  Hq a multiple of Hk, at most 1024.
+ *   q_weight, k_weight  bf16 [D] or NULL (no norm of that one): h * weight / sqrt(mean_d h^2 + eps), the squares summed
+ *             in float64; eps in (0, 1] (read only with a weight).
+ *   rope      float32 [P, R] or NULL (no rotation): cosines, then sines, of position p's R/2 angles.  Pair i of a head
+ *             is numbers i and i + R/2, or 2i and 2i + 1 (interleaved = 1); (a, c) becomes (a cos - c sin,
+ *             c cos + a sin); numbers past R stay.  R a multiple of 16, at most D.  A position past P counts as a
+ *             negative one does.
+ *   q         bf16 [M, Hq, D] out.
+ * All in float32, rounded once.  A block that a sequence begins takes its scale from its new tokens alone; one
+ * that already holds tokens of the sequence keeps the larger of its scale and theirs, and where that grows its
+ * older codes are rounded again to the new scale (only numbers in e4m3's subnormal range change).  Slots of a block
+ * that no token has reached are left as they were.  A block that tokens are appended to must belong to one sequence only.
+ * M at most 2^31 / ((Hq + 2 Hk) D).
+ */
+int awq_qkv_append(const void* qkv_bf16, int64_t M, int32_t Hq, int32_t Hk, int32_t D, const void* q_weight_bf16,
+                   const void* k_weight_bf16, float eps, const float* rope, int64_t P, int32_t R, int32_t interleaved,
+                   const int32_t* cu, const int32_t* length, const int32_t* table, int32_t n_seq, int32_t width,
+                   int32_t max_q, void* q_bf16, uint8_t* k_codes, uint8_t* v_codes, uint8_t* scales, int64_t blocks,
+                   int32_t T, void* stream);
+
+/* Attention over the cache: with head j of q reading head j / (Hq/Hk) of the cache, for every new token
+ *   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q . k_t),
+ * over the tokens of its sequence up to its own position (causal = 1) or all of them (causal = 0); zero where it sees
+ * none.  Sums and exponents in float32; p_t is rounded to bf16 for the second product (its error, 2^-9 at most, is
+ * of the output's own rounding's size), K and V are exact in it.
+ *   q, out  bf16 [M, Hq, D];  scale  finite (often 1/sqrt(D)).
+ *   workspace >= awq_attention_workspace_size(M, n_seq, max_q, Hq, Hk, D) bytes, under the rules of
+ *   awq_fp8_gemm's.
+ */
+size_t awq_attention_workspace_size(int64_t M, int32_t n_seq, int32_t max_q, int32_t Hq, int32_t Hk, int32_t D);
+int awq_attention(const void* q_bf16, int64_t M, int32_t Hq, int32_t Hk, int32_t D, const int32_t* cu,
+                  const int32_t* length, const int32_t* table, int32_t n_seq, int32_t width, int32_t max_q,
+                  const uint8_t* k_codes, const uint8_t* v_codes, const uint8_t* scales, int64_t blocks, int32_t T,
+                  float scale, int32_t causal, void* out_bf16, void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- status helpers */
 const char* awq_status_string(int status);

@@ -81,6 +81,17 @@ _SIGNATURES = {
     "awq_rms_norm": (ctypes.c_int, [_P, _P, _P, _I64, _I64, ctypes.c_float, _P, _P, _P, _I32, _P, _P, _P]),
     "awq_mx_gemm_workspace_size": (_SZ, [_I64, _I64, _I64, _I32]),
     "awq_mx_gemm": (ctypes.c_int, [_P, _P, _I32, _I64, _P, _P, _I64, _I64, _P, _P, _SZ, _P]),
+    "awq_fp8_codes_bytes": (_SZ, [_I64, _I64]),
+    "awq_fp8_scales_count": (_SZ, [_I64, _I64]),
+    "awq_fp8_pack": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P]),
+    "awq_fp8_quantize": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _P]),
+    "awq_fp8_gemm_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "awq_fp8_gemm": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _SZ, _P]),
+    "awq_qkv_append": (ctypes.c_int, [_P, _I64, _I32, _I32, _I32, _P, _P, ctypes.c_float, _P, _I64, _I32, _I32, _P, _P,
+                                      _P, _I32, _I32, _I32, _P, _P, _P, _P, _I64, _I32, _P]),
+    "awq_attention_workspace_size": (_SZ, [_I64, _I32, _I32, _I32, _I32, _I32]),
+    "awq_attention": (ctypes.c_int, [_P, _I64, _I32, _I32, _I32, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _I64, _I32,
+                                     ctypes.c_float, _I32, _P, _P, _SZ, _P]),
     "awq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "awq_last_hip_error": (ctypes.c_int, []),
     "awq_version": (ctypes.c_char_p, []),
@@ -691,3 +702,228 @@ def mx_gemm(a: MxActs, q: MxWeights, stream=None) -> torch.Tensor:
         ws = workspace(awq_mx_gemm_workspace_size(M, q.K, q.N, bits), a.codes.device)
     awq_mx_gemm(a.codes, a.scales, q.codes, q.scales, Y, ws, stream)
     return Y
+
+
+# ------------------------------------------------------------------ 8-bit products with scales per 128
+_F8_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _f8_codes(fn: str, name: str, t: torch.Tensor, shape) -> int:
+    if t.shape != shape or t.dtype not in _F8_DTYPES:
+        _expect(fn, name, t, _F8_DTYPES, shape)
+    return t.data_ptr()
+
+
+def _fp8_weights(fn: str, codes: torch.Tensor, scales: torch.Tensor, K: int, N: int):
+    kc = -(-K // 128)
+    return (_f8_codes(fn, "codes", codes, (-(-N // 64), kc, 8, 64, 16)),
+            _mx_arg(fn, "scales", scales, torch.float32, (-(-N // 128), kc)))
+
+
+def _fp8_acts(fn: str, codes: torch.Tensor, scales: torch.Tensor, M: int, K: int):
+    return (_f8_codes(fn, "codes", codes, (M, K)), _mx_arg(fn, "scales", scales, torch.float32, (M, -(-K // 128))))
+
+
+def awq_fp8_codes_bytes(K: int, N: int) -> int:
+    return int(_lib.awq_fp8_codes_bytes(K, N))
+
+
+def awq_fp8_scales_count(K: int, N: int) -> int:
+    return int(_lib.awq_fp8_scales_count(K, N))
+
+
+def awq_fp8_pack(W: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    fn = "awq_fp8_pack"
+    K, N = _matrix(fn, "W", W)
+    _mx_rows(fn, K, 16)
+    pc, ps = _fp8_weights(fn, codes, scales, K, N)
+    st = _lib.awq_fp8_pack(W.data_ptr(), K, N, pc, ps, _mx_stream(fn, stream, W, codes, scales))
+    if st:
+        _check(fn, st)
+
+
+def awq_fp8_quantize(X: torch.Tensor, gate: Optional[torch.Tensor], codes: torch.Tensor, scales: torch.Tensor,
+                     stream=None) -> None:
+    fn = "awq_fp8_quantize"
+    M, K = MK = _matrix(fn, "X", X)
+    _mx_rows(fn, K, 16)
+    pg = None if gate is None else _mx_arg(fn, "gate", gate, torch.bfloat16, MK)
+    pc, ps = _fp8_acts(fn, codes, scales, M, K)
+    st = _lib.awq_fp8_quantize(X.data_ptr(), pg, M, K, pc, ps, _mx_stream(fn, stream, X, gate, codes, scales))
+    if st:
+        _check(fn, st)
+
+
+def awq_fp8_gemm_workspace_size(M: int, K: int, N: int) -> int:
+    return int(_lib.awq_fp8_gemm_workspace_size(M, K, N))
+
+
+def awq_fp8_gemm(xcodes: torch.Tensor, xscales: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                 Y: torch.Tensor, ws: Optional[torch.Tensor], stream=None) -> None:
+    fn = "awq_fp8_gemm"
+    M, N = _matrix(fn, "Y", Y)
+    K = _matrix(fn, "xcodes", xcodes, xcodes.dtype if xcodes.dtype in _F8_DTYPES else torch.float8_e4m3fn)[1]
+    _mx_rows(fn, K, 16)
+    px, pxs = _fp8_acts(fn, xcodes, xscales, M, K)
+    pc, ps = _fp8_weights(fn, codes, scales, K, N)
+    st = _lib.awq_fp8_gemm(px, pxs, M, pc, ps, K, N, Y.data_ptr(), None if ws is None else ws.data_ptr(), _nbytes(ws),
+                           _mx_stream(fn, stream, Y, xcodes, xscales, codes, scales, ws))
+    if st:
+        _check(fn, st)
+
+
+class Fp8Weights:
+    """Device buffers of one layer's 8-bit weights: codes float8_e4m3fn [ceil(N/64), ceil(K/128), 8, 64, 16], scales
+    float32 [ceil(N/128), ceil(K/128)] and the layer's K and N."""
+
+    def __init__(self, codes, scales, K, N):
+        self.codes, self.scales, self.K, self.N = codes, scales, K, N
+
+
+class Fp8Acts:
+    """Device buffers of 8-bit activations: codes float8_e4m3fn [M, K], scales float32 [M, ceil(K/128)]."""
+
+    def __init__(self, codes, scales):
+        self.codes, self.scales = codes, scales
+
+
+def fp8_pack(W: torch.Tensor, stream=None) -> Fp8Weights:
+    """Allocate and pack one layer's weights."""
+    K, N = W.shape
+    kc = -(-K // 128)
+    with _allocating_on(stream):
+        codes = torch.empty((-(-N // 64), kc, 8, 64, 16), dtype=torch.float8_e4m3fn, device=W.device)
+        scales = torch.empty((-(-N // 128), kc), dtype=torch.float32, device=W.device)
+    awq_fp8_pack(W, codes, scales, stream)
+    return Fp8Weights(codes, scales, K, N)
+
+
+def fp8_quantize(X: torch.Tensor, gate: Optional[torch.Tensor] = None, stream=None) -> Fp8Acts:
+    """X (or silu(gate) * X) in 8-bit groups of 128 channels."""
+    M, K = X.shape
+    with _allocating_on(stream):
+        a = Fp8Acts(torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device),
+                    torch.empty((M, -(-K // 128)), dtype=torch.float32, device=X.device))
+    awq_fp8_quantize(X, gate, a.codes, a.scales, stream)
+    return a
+
+
+def fp8_gemm(a: Fp8Acts, q: Fp8Weights, stream=None) -> torch.Tensor:
+    """The product of 8-bit activations and 8-bit weights."""
+    M, K = a.codes.shape
+    if K != q.K:                                    # the weights' buffers are padded and would not tell
+        raise ValueError(f"fp8_gemm: activations of {K} channels, weights of {q.K}")
+    with _allocating_on(stream):
+        Y = torch.empty((M, q.N), dtype=torch.bfloat16, device=a.codes.device)
+        ws = workspace(awq_fp8_gemm_workspace_size(M, K, q.N), a.codes.device)
+    awq_fp8_gemm(a.codes, a.scales, q.codes, q.scales, Y, ws, stream)
+    return Y
+
+
+# ------------------------------------------------------------------ 8-bit cache and its attention
+def _sequences(fn: str, cu: torch.Tensor, length: torch.Tensor, table: torch.Tensor):
+    n, width = _matrix(fn, "table", table, torch.int32)
+    return (_mx_arg(fn, "cu", cu, torch.int32, (n + 1,)), _mx_arg(fn, "length", length, torch.int32, (n,)),
+            table.data_ptr(), n, width)
+
+
+def _cache(fn: str, k_codes: torch.Tensor, v_codes: torch.Tensor, scales: torch.Tensor):
+    if k_codes.dim() != 4:
+        raise ValueError(f"{fn}: k_codes must be [blocks, heads, T, D], got shape {tuple(k_codes.shape)}")
+    blocks, Hk, T, D = shape = k_codes.shape
+    if scales.shape != (blocks, Hk, 2) or scales.dtype not in _SCALE_DTYPES:
+        _expect(fn, "scales", scales, _SCALE_DTYPES, (blocks, Hk, 2))
+    return (_f8_codes(fn, "k_codes", k_codes, shape), _f8_codes(fn, "v_codes", v_codes, (blocks, Hk, T // 16, D, 16)),
+            scales.data_ptr(), blocks, Hk, T, D)
+
+
+def _query(fn: str, name: str, t: torch.Tensor, D: int):
+    if t.dim() != 3 or t.dtype is not torch.bfloat16 or t.shape[2] != D:
+        raise ValueError(f"{fn}: {name} must be {torch.bfloat16} [M, heads, {D}], got {t.dtype} {tuple(t.shape)}")
+    return t.shape[0], t.shape[1]
+
+
+def awq_qkv_append(qkv: torch.Tensor, q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor], eps: float,
+                   rope: Optional[torch.Tensor], interleaved: bool, cu: torch.Tensor, length: torch.Tensor,
+                   table: torch.Tensor, max_q: int, q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor,
+                   scales: torch.Tensor, stream=None) -> None:
+    fn = "awq_qkv_append"
+    pk, pv, pe, blocks, Hk, T, D = _cache(fn, k_codes, v_codes, scales)
+    M, Hq = _query(fn, "q", q, D)
+    pc, pl, pt, n, width = _sequences(fn, cu, length, table)
+    px = _mx_arg(fn, "qkv", qkv, torch.bfloat16, (M, (Hq + 2 * Hk) * D))
+    pqw = None if q_weight is None else _mx_arg(fn, "q_weight", q_weight, torch.bfloat16, (D,))
+    pkw = None if k_weight is None else _mx_arg(fn, "k_weight", k_weight, torch.bfloat16, (D,))
+    P, R = (0, 0) if rope is None else _matrix(fn, "rope", rope, torch.float32)
+    st = _lib.awq_qkv_append(px, M, Hq, Hk, D, pqw, pkw, eps, None if rope is None else rope.data_ptr(), P, R,
+                             1 if interleaved else 0, pc, pl, pt, n, width, max_q, q.data_ptr(), pk, pv, pe, blocks, T,
+                             _mx_stream(fn, stream, qkv, q_weight, k_weight, rope, cu, length, table, q, k_codes, v_codes,
+                                        scales))
+    if st:
+        _check(fn, st)
+
+
+def awq_attention_workspace_size(M: int, n_seq: int, max_q: int, Hq: int, Hk: int, D: int) -> int:
+    return int(_lib.awq_attention_workspace_size(M, n_seq, max_q, Hq, Hk, D))
+
+
+def awq_attention(q: torch.Tensor, cu: torch.Tensor, length: torch.Tensor, table: torch.Tensor, max_q: int,
+                  k_codes: torch.Tensor, v_codes: torch.Tensor, scales: torch.Tensor, scale: float, causal: bool,
+                  out: torch.Tensor, ws: Optional[torch.Tensor], stream=None) -> None:
+    fn = "awq_attention"
+    pk, pv, pe, blocks, Hk, T, D = _cache(fn, k_codes, v_codes, scales)
+    M, Hq = _query(fn, "q", q, D)
+    po = _mx_arg(fn, "out", out, torch.bfloat16, q.shape)
+    pc, pl, pt, n, width = _sequences(fn, cu, length, table)
+    st = _lib.awq_attention(q.data_ptr(), M, Hq, Hk, D, pc, pl, pt, n, width, max_q, pk, pv, pe, blocks, T, scale,
+                            1 if causal else 0, po, None if ws is None else ws.data_ptr(), _nbytes(ws),
+                            _mx_stream(fn, stream, q, cu, length, table, k_codes, v_codes, scales, out, ws))
+    if st:
+        _check(fn, st)
+
+
+class KVCache:
+    """Device buffers of an 8-bit cache: K codes float8_e4m3fn [blocks, heads, T, D], V codes [blocks, heads, T/16, D, 16]
+    and the scale bytes [blocks, heads, 2].  A block needs no clearing before its first token."""
+
+    def __init__(self, blocks: int, heads: int, D: int, T: int = 64, device="cuda"):
+        self.k = torch.zeros((blocks, heads, T, D), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+        self.v = torch.zeros((blocks, heads, T // 16, D, 16), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+        self.scales = torch.zeros((blocks, heads, 2), dtype=torch.uint8, device=device).view(torch.float8_e8m0fnu)
+
+
+class Sequences:
+    """The sequences of one step: cu [n + 1] (rows of their new tokens), length [n] (tokens with the new ones) and table
+    [n, width] (blocks of the cache), int32 on the device, and the largest number of new tokens."""
+
+    def __init__(self, cu: torch.Tensor, length: torch.Tensor, table: torch.Tensor, max_q: int):
+        self.cu, self.length, self.table, self.max_q = cu, length, table, max_q
+
+
+def qkv_append(qkv: torch.Tensor, seqs: Sequences, cache: KVCache, rope: Optional[torch.Tensor] = None,
+               q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+               interleaved: bool = False, stream=None) -> torch.Tensor:
+    """q [M, heads, D] of q|k|v, normed and rotated; k and v go into the cache.  Rows that no sequence has are zero."""
+    _, Hk, _, D = cache.k.shape
+    M, Hq = qkv.shape[0], qkv.shape[1] // D - 2 * Hk
+    if Hq <= 0:
+        raise ValueError(f"qkv_append: q|k|v of {qkv.shape[1]} columns leaves no head of q beside {Hk} of k and v")
+    with _allocating_on(stream):
+        q = torch.zeros((M, Hq, D), dtype=torch.bfloat16, device=qkv.device)
+    awq_qkv_append(qkv, q_weight, k_weight, eps, rope, interleaved, seqs.cu, seqs.length, seqs.table, seqs.max_q, q,
+                   cache.k, cache.v, cache.scales, stream)
+    return q
+
+
+def attention(q: torch.Tensor, seqs: Sequences, cache: KVCache, scale: Optional[float] = None, causal: bool = True,
+              stream=None) -> torch.Tensor:
+    """Attention of q [M, heads, D] over the cache, [M, heads, D]; scale 1/sqrt(D) unless given.  Rows that no sequence
+    has are zero."""
+    M, Hq, D = q.shape
+    with _allocating_on(stream):
+        out = torch.zeros_like(q)
+        ws = workspace(awq_attention_workspace_size(M, seqs.length.shape[0], seqs.max_q, Hq, cache.k.shape[1], D),
+                       q.device)
+    awq_attention(q, seqs.cu, seqs.length, seqs.table, seqs.max_q, cache.k, cache.v, cache.scales,
+                  D ** -0.5 if scale is None else scale, causal, out, ws, stream)
+    return out

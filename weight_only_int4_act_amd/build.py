@@ -30,7 +30,9 @@ FLAGS = [
     "-Wno-unused-command-line-argument",
 ]
 SOURCES = ["awq_api.hip", "awq_stats.hip", "awq_search.hip", "awq_pack.hip", "awq_gemm.hip", "awq_greedy.hip",
-           "awq_mx_api.hip", "awq_mx_pack.hip", "awq_mx_quant.hip", "awq_mx_gemm.hip"]
+           "awq_mx_api.hip", "awq_mx_pack.hip", "awq_mx_quant.hip", "awq_mx_gemm.hip",
+           "awq_fp8_api.hip", "awq_fp8_quant.hip", "awq_fp8_gemm.hip", "awq_cache_api.hip", "awq_append.hip",
+           "awq_attention.hip"]
 
 
 def hipcc() -> str:

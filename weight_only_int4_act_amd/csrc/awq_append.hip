@@ -1,0 +1,238 @@
+// q|k|v of new tokens: norms of queries and keys per head, rotation, and the append of keys and values to the 8-bit
+// cache.
+#include "awq_cache.h"
+
+namespace awq {
+namespace {
+
+__device__ __forceinline__ uint32_t cache_scale_byte(uint32_t top) {
+    const int e = (int)(top >> 23);
+    return e == 255 ? 255u : (uint32_t)max(e - 8 + ((top & 0x7fffffu) > 0x600000u), 0);
+}
+// The conversions' scale operand: they read the exponent field alone (0 is 2^-127).
+__device__ __forceinline__ float cache_scale(uint32_t E) { return __uint_as_float(E << 23); }
+
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+
+// Eight numbers over their block's scale; none is beyond 448 times it.
+__device__ __forceinline__ uint2 cache_codes8(const float (&p)[8], uint32_t E) {
+    const float scale = cache_scale(E);
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        s16x2 r = {0, 0};
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, p[4 * h], p[4 * h + 1], scale, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, p[4 * h + 2], p[4 * h + 3], scale, true);
+        w[h] = E == 255 ? 0u : __builtin_bit_cast(uint32_t, r);
+    }
+    return uint2{w[0], w[1]};
+}
+// Four codes over 2^d: what an older scale wrote, to a larger one.  Past 2^-30 every code becomes zero.
+__device__ __forceinline__ uint32_t cache_rescale4(uint32_t w, uint32_t d) {
+    const float scale = cache_scale(127u + min(d, 40u));
+    const floatx2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    s16x2 r = {0, 0};
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a[0], a[1], scale, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, b[0], b[1], scale, true);
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+__device__ __forceinline__ void widen8(const u32x4& v, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(v[i]);
+        x[2 * i + 1] = bf16_hi(v[i]);
+    }
+}
+
+// One head of D numbers is held by D / 8 consecutive lanes, eight numbers each.
+template <int D>
+struct Head {
+    static constexpr int L = D / 8;              // lanes
+    // the sum of squares over the head's lanes
+    static __device__ __forceinline__ double sum(double v) {
+#pragma unroll
+        for (int off = 1; off < L; off *= 2) v += __shfl_xor(v, off, kWave);
+        return v;
+    }
+    static __device__ __forceinline__ void norm(float (&x)[8], const uint16_t* weight, int l, double eps) {
+        double s = 0.;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += (double)x[i] * (double)x[i];
+        const double m = sum(s) * (1. / D) + eps, y = __builtin_amdgcn_rsq(m);
+        const float r = (float)(m < __builtin_inf() ? y * (1.5 - 0.5 * m * y * y) : y);   // infinity: 0; NaN: NaN
+        float w[8];
+        widen8(*(const u32x4*)(weight + l * 8), w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
+    }
+    // pairs (i, i + R/2) or (2i, 2i + 1); turn: the row of the rotation's table
+    static __device__ __forceinline__ void rotate(float (&x)[8], const float* turn, int R, int interleaved, int l) {
+        const int half = R / 16;                 // lanes of the cosines
+        const bool in = l < 2 * half;
+        if (interleaved) {
+            const int at = in ? 4 * l : 0;
+            const floatx4 c = *(const floatx4*)(turn + at), s = *(const floatx4*)(turn + R / 2 + at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = x[2 * i], b = x[2 * i + 1];
+                if (in) x[2 * i] = a * c[i] - b * s[i], x[2 * i + 1] = b * c[i] + a * s[i];
+            }
+            return;
+        }
+        const bool low = l < half;
+        const int at = in ? 8 * (low ? l : l - half) : 0, lane = threadIdx.x & 63;
+        const int other = in ? (low ? lane + half : lane - half) : lane;
+        const floatx4 c[2] = {*(const floatx4*)(turn + at), *(const floatx4*)(turn + at + 4)};
+        const floatx4 s[2] = {*(const floatx4*)(turn + R / 2 + at), *(const floatx4*)(turn + R / 2 + at + 4)};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float o = __shfl(x[i], other, kWave), t = o * s[i / 4][i % 4];
+            if (in) x[i] = x[i] * c[i / 4][i % 4] + (low ? -t : t);
+        }
+    }
+};
+
+// A workgroup takes the new tokens of one block of the cache for one head of K and V and the heads of q that read it.
+// The numbers of K (float32, normed and rotated) and V (bf16) stay in registers until the block's largest are
+// known; then come the codes.
+template <int D, int T>
+__global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, Cache c, int per_seq) {
+    using H = Head<D>;
+    constexpr int L = H::L, W = 256 / L, U = (T + W - 1) / W;   // lanes of a head, heads at a time, rounds of a block
+    __shared__ uint32_t tops[4][2];
+    lds_poison_start(&tops[0][0], 8);
+    const int h = blockIdx.x % c.Hk, j = blockIdx.x / c.Hk % per_seq, b = blockIdx.x / c.Hk / per_seq;
+    const NewTokens t = new_tokens(s, b, (int)a.M);
+    const int l = threadIdx.x % L, w = threadIdx.x / L;
+    const int G = a.Hq / c.Hk;
+    const int64_t row_size = (int64_t)(a.Hq + 2 * c.Hk) * D;
+
+    // positions below zero: no block; the first workgroup of a head writes zeros
+    if (j == 0 && t.start < 0) {
+        const int none = min(min(t.count, -t.start), s.max_q);
+        for (int i = w; i < none * G; i += W)
+            *(u32x4*)(a.q + (((int64_t)t.row0 + i / G) * a.Hq + h * G + i % G) * D + l * 8) = u32x4{0, 0, 0, 0};
+    }
+    const int64_t first_block = max(t.start, 0) / T, index = first_block + j;   // of the sequence
+    const int64_t p0 = max((int64_t)t.start, index * T);
+    const int64_t p1 = min(min((int64_t)t.length, (index + 1) * T), (int64_t)t.start + s.max_q);
+    if (t.count <= 0 || p0 >= p1) return;        // the whole workgroup
+    const int n = (int)(p1 - p0), slot0 = (int)(p0 - index * T);
+    const int row0 = t.row0 + (int)(p0 - t.start);
+    const int turned = a.rope ? (int)min(max((int64_t)a.P - p0, (int64_t)0), (int64_t)n) : n;   // tokens that the rotation covers
+    const int64_t block = index < s.width ? s.table[(int64_t)b * s.width + index] : -1;
+    const bool stored = block >= 0 && block < c.blocks && turned > 0;
+
+    if (stored) {
+        const int64_t at = block * c.Hk + h;
+        const uint32_t before = *(const uint16_t*)(c.scales + at * 2);
+        float k[U][8];
+        u32x4 v[U];
+        uint32_t kt = 0, vt = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = u * W + w;
+            const bool in = i < turned;
+            const uint16_t* row = a.qkv + (int64_t)(row0 + min(i, n - 1)) * row_size + (int64_t)(a.Hq + h) * D + l * 8;
+            widen8(*(const u32x4*)row, k[u]);
+            v[u] = *(const u32x4*)(row + (int64_t)c.Hk * D);
+            if (a.k_weight) H::norm(k[u], a.k_weight, l, a.eps);
+            if (a.rope) H::rotate(k[u], a.rope + min(p0 + i, (int64_t)a.P - 1) * a.R, a.R, a.interleaved, l);
+            if (!in) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kt = max(kt, __float_as_uint(k[u][e]) & 0x7fffffffu);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) vt = max(vt, max(v[u][e] << 16 & 0x7fffffffu, v[u][e] & 0x7fff0000u));
+        }
+#pragma unroll
+        for (int off = 1; off < 64; off *= 2) {
+            kt = max(kt, (uint32_t)__shfl_xor((int)kt, off, kWave));
+            vt = max(vt, (uint32_t)__shfl_xor((int)vt, off, kWave));
+        }
+        if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6][0] = kt, tops[threadIdx.x >> 6][1] = vt;
+        __syncthreads();                         // `stored` is the workgroup's
+        kt = max(max(tops[0][0], tops[1][0]), max(tops[2][0], tops[3][0]));
+        vt = max(max(tops[0][1], tops[1][1]), max(tops[2][1], tops[3][1]));
+        // a block that holds older tokens keeps the larger scale
+        const uint32_t ke0 = slot0 ? before & 255 : 0, ve0 = slot0 ? before >> 8 : 0;
+        const uint32_t ke = max(cache_scale_byte(kt), ke0), ve = max(cache_scale_byte(vt), ve0);
+        uint8_t* const kc = c.k + at * T * D;
+        uint8_t* const vc = c.v + at * T * D;
+        if (slot0 && ((ke > ke0 && ke != 255) || (ve > ve0 && ve != 255))) {   // the whole workgroup
+            if (ke > ke0 && ke != 255)
+                for (int i = threadIdx.x; i < slot0 * D / 4; i += 256) {
+                    uint32_t* p = (uint32_t*)kc + i;
+                    *p = cache_rescale4(*p, ke - ke0);
+                }
+            if (ve > ve0 && ve != 255)
+                for (int i = threadIdx.x; i < (slot0 + 15) / 16 * D * 4; i += 256) {   // four tokens of a group
+                    const int first = i / (4 * D) * 16 + i % 4 * 4, older = min(max(slot0 - first, 0), 4);
+                    const uint32_t mask = older == 4 ? ~0u : (1u << 8 * older) - 1;
+                    uint32_t* p = (uint32_t*)vc + i;
+                    if (older) *p = (cache_rescale4(*p, ve - ve0) & mask) | (*p & ~mask);
+                }
+            __syncthreads();                     // before new tokens' bytes of the same words
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = u * W + w, slot = slot0 + i;
+            if (i >= turned) continue;
+            *(uint2*)(kc + (int64_t)slot * D + l * 8) = cache_codes8(k[u], ke);
+            float x[8];
+            widen8(v[u], x);
+            const uint2 codes = cache_codes8(x, ve);
+            uint8_t* const to = vc + ((slot >> 4) * D + l * 8) * 16 + (slot & 15);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) to[e * 16] = (uint8_t)((e < 4 ? codes.x : codes.y) >> 8 * (e % 4));
+        }
+        if (threadIdx.x == 0) *(uint16_t*)(c.scales + at * 2) = (uint16_t)(ke | ve << 8);
+    }
+    // q: the tokens' G heads
+    for (int i = w; i < (n * G + W - 1) / W * W; i += W) {   // every lane of a wavefront, for the exchanges
+        const bool in = i < n * G;
+        const int tok = in ? i / G : n - 1, head = h * G + (in ? i % G : 0);
+        float x[8];
+        widen8(*(const u32x4*)(a.qkv + (int64_t)(row0 + tok) * row_size + (int64_t)head * D + l * 8), x);
+        if (a.q_weight) H::norm(x, a.q_weight, l, a.eps);
+        if (a.rope) {
+            H::rotate(x, a.rope + min(p0 + tok, (int64_t)a.P - 1) * a.R, a.R, a.interleaved, l);
+            if (tok >= turned) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            }
+        }
+        if (in)
+            *(u32x4*)(a.q + ((int64_t)(row0 + tok) * a.Hq + head) * D + l * 8) =
+                u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+    }
+}
+
+}  // namespace
+
+hipError_t launch_qkv_append(const AppendArgs& a, const Sequences& s, const Cache& c, hipStream_t st) {
+    // the blocks that max_q tokens touch at most, wherever the first lies
+    const int per_seq = (int)(((int64_t)s.max_q + c.T - 2) / c.T + 1);
+    const unsigned grid = (unsigned)((int64_t)s.n * per_seq * c.Hk);
+    const auto go = [&](auto kernel) {
+        kernel<<<grid, 256, 0, st>>>(a, s, c, per_seq);
+        return hipGetLastError();
+    };
+    if (c.D == 128) {
+        switch (c.T) {
+            case 16: return go(k_qkv_append<128, 16>);
+            case 32: return go(k_qkv_append<128, 32>);
+            case 64: return go(k_qkv_append<128, 64>);
+            default: return go(k_qkv_append<128, 128>);
+        }
+    }
+    switch (c.T) {
+        case 16: return go(k_qkv_append<64, 16>);
+        case 32: return go(k_qkv_append<64, 32>);
+        case 64: return go(k_qkv_append<64, 64>);
+        default: return go(k_qkv_append<64, 128>);
+    }
+}
+
+}  // namespace awq
