@@ -163,6 +163,278 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_rows(
     if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// ---------------------------------------------------------------- rows by the hundred: tiles in LDS
+// 64 WM rows x 256 columns per workgroup, WM x WN wavefronts of 64 rows x 32 CF columns, by 32x32x64 products (half the
+// operand reads of 16x16x128 ones for the same work).  Lane (i, h) = (lane % 32, lane / 32).  First operand: column i
+// of 32 weights; second: row i of 32; both take pieces (16 bytes) 4y + 2h and 4y + 2h + 1 of the group's eight for half y of
+// the channels (any order that both share will do).  Results: row i, column 8 (r / 4) + 4h + r % 4: one factor
+// sx sw per lane and row fragment.
+//
+// Both operands of a group are copied once per workgroup straight into LDS, ST groups deep:
+//   activations  1 KB units of 8 rows; piece q of row r lies at slot q ^ (r / 2 % 8), so that the lanes that a
+//                16-byte read serves together (0-3, 12-15, 20-27 and 4-11, 16-19, 28-31 of either half) hit different banks;
+//   weights      the packed order, read 256 contiguous bytes at a time;
+//   scales       of four groups at a time, two such sets deep: 16 bytes per row, and 16 per 128 columns.
+// Transfers are issued from inline asm and waited for with counted vmcnt waits (those of a wavefront complete in
+// order).  A turn multiplies one group in steps of one result fragment: two products, beside them the float32
+// additions of the fragment before, the LDS reads of the next weights, a share of the transfers.  Before the last column
+// fragment a barrier says that the group is in every wavefront's registers and the next one has landed; its place
+// is then filled with group c + ST.
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ u32x4 fp8_poison() { return u32x4{~0u, ~0u, ~0u, ~0u}; }   // NaN in e4m3 and in float32
+
+template <int WM, int WN, int CF, int ST>
+struct Fp8Tile {
+    static constexpr int kWaves = WM * WN, kRows = 64 * WM, kCols = 32 * CF * WN;
+    static_assert(kCols == 256 && CF % 2 == 0, "tile shape");
+    static constexpr int kXu = kRows / 8 / kWaves, kWu = 32 / kWaves, kData = kXu + kWu;   // 1 KB units per wavefront
+    static_assert(kXu % 2 == 0 && kXu * kWaves * 8 == kRows && kWu * kWaves == 32, "even shares");
+    static constexpr int kX = kRows * 128, kStage = kX + 32768;
+    static constexpr int kScaleSet = kRows * 16 + 1024;           // rows, then columns (32 bytes of a transfer's 1 KB)
+    static constexpr int kScales = ST * kStage, kLds = kScales + 2 * kScaleSet;
+    static_assert(kLds <= 160 * 1024, "LDS of a CU");
+};
+
+template <int WM, int WN, int CF, int ST, bool EDGE>
+__global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_tile(
+    const uint8_t* __restrict__ xcodes, const float* __restrict__ xscales, int64_t M, const uint8_t* __restrict__ codes,
+    const float* __restrict__ scales, int64_t K, int64_t N, int chunks, uint16_t* __restrict__ Y,
+    float* __restrict__ part, int row_tiles, int col_tiles, int nz, int total, int per_xcd) {
+    using S = Fp8Tile<WM, WN, CF, ST>;
+    extern __shared__ u32x4 lds[];
+    const int logical = xcd_tile(blockIdx.x, per_xcd);
+    if (logical >= total) return;
+    const int tiles = row_tiles * col_tiles;
+    const int z = logical / tiles, tile = logical % tiles;
+    // eight row tiles by four column tiles at a time share an XCD's L2
+    const int panel = tile / (8 * col_tiles), in = tile % (8 * col_tiles);
+    const int prow = min(8, row_tiles - 8 * panel);
+    const int rt = 8 * panel + in % prow, ct = in / prow;
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int i = lane & 31, h = lane >> 5;
+    const int wm = wave / WN, wn = wave % WN;
+    const int per = (chunks + nz - 1) / nz;
+    const int cb = min(z * per, chunks), ce = min(cb + per, chunks);
+    const int64_t row0 = (int64_t)rt * S::kRows, t0 = (int64_t)ct * 4, nt = (N + 63) / 64, nb = (N + 127) / 128;
+    const int rows = (int)min<int64_t>(S::kRows, M - row0);       // past the last row and
+    const int cts = (int)min<int64_t>(4, nt - t0);                // column tile: zeros
+    const uint32_t xrow = (uint32_t)K, srow = (uint32_t)chunks * 4, wtile = (uint32_t)chunks * 8192;
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+    const i32x4 xr = byte_rsrc(xcodes + row0 * xrow, (uint32_t)rows * xrow);
+    const i32x4 wr = byte_rsrc(codes + t0 * wtile, (uint32_t)cts * wtile);
+    const i32x4 sr = byte_rsrc(xscales + row0 * chunks, (uint32_t)rows * srow);
+    const i32x4 fr = byte_rsrc(scales + t0 / 2 * chunks, (uint32_t)min<int64_t>(2, nb - t0 / 2) * srow);
+
+    // this lane's places in its wavefront's transfers
+    const int ur = wave * S::kXu * 8 + lane / 8, us = lane & 7;
+    uint32_t xoff[S::kXu];
+    int xk[2];                                   // first channel of the piece, units of either parity
+#pragma unroll
+    for (int k = 0; k < 2; ++k) xk[k] = 16 * (us ^ ((4 * k + lane / 16) & 7));
+#pragma unroll
+    for (int k = 0; k < S::kXu; ++k) xoff[k] = (uint32_t)(ur + 8 * k) * xrow + xk[k & 1];
+    static_assert(8 % S::kWu == 0, "a wavefront's units lie in one column tile");
+    const uint32_t woff = (uint32_t)(wave * S::kWu / 8) * wtile + wave * S::kWu % 8 * 1024 + lane * 16;
+    // the scales of the slice's groups 4q .. 4q + 3: 64 rows per wavefront (the same ones by several where there are
+    // fewer), and the columns' by every wavefront alike
+    const int part64 = wave % WM;
+    const uint32_t soff = (uint32_t)(part64 * 64 + lane) * srow + cb * 4;
+    const uint32_t foff = lane < 2 ? (uint32_t)lane * srow + cb * 4 : kOutside;
+    auto issue_scales = [&](int q) __attribute__((always_inline)) {
+        const uint32_t at = S::kScales + (q & 1) * S::kScaleSet;
+        if constexpr (kLdsPoison) {
+            lds[at / 16 + part64 * 64 + lane] = fp8_poison();
+            lds[at / 16 + S::kRows + lane] = fp8_poison();
+            lds_write_fence();
+        }
+        dma16(sr, soff + q * 16, 0, base + at + part64 * 1024, 0);
+        dma16(fr, foff + q * 16, 0, base + at + S::kRows * 16, 0);
+    };
+    // transfer k of group c's batch; for a group past the slice the resources are empty, which brings zeros
+    // (no traffic), so that the counted waits stay the same
+    auto issue_op = [&](int c, int stage, int k) __attribute__((always_inline)) {
+        const bool on = c < ce;
+        const uint32_t st = stage * S::kStage;
+        const uint32_t to = k < S::kXu ? st + (wave * S::kXu + k) * 1024 : st + S::kX + (wave * S::kWu + k - S::kXu) * 1024;
+        if constexpr (kLdsPoison) {
+            lds[to / 16 + lane] = fp8_poison();
+            lds_write_fence();
+        }
+        if (k < S::kXu) {
+            const i32x4 r = {xr[0], xr[1], on ? xr[2] : 0, xr[3]};
+            const uint32_t past = !EDGE || xk[k & 1] < (int)xrow - c * 128 ? 0 : kOutside;   // a piece past K
+            dma16(r, xoff[k] | past, (uint32_t)c * 128, base + to, 0);
+        } else {
+            const i32x4 r = {wr[0], wr[1], on ? wr[2] : 0, wr[3]};
+            dma16(r, woff, (uint32_t)c * 8192 + (k - S::kXu) * 1024, base + to, 0);
+        }
+    };
+
+    const uint8_t* const lb = (const uint8_t*)lds;
+    uint32_t xl[2][2];                           // by half of the channels and piece
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) xl[y][p] = (wm * 64 + i) * 128 + ((4 * y + 2 * h + p) ^ (i / 2 & 7)) * 16;
+    const uint32_t wl = S::kX + wn * CF * 4096 + (i / 16) * 2048 + h * 512 + (i & 15) * 16;
+    const uint32_t sl = S::kScales + (wm * 64 + i) * 16, fl = S::kScales + S::kRows * 16 + wn * CF * 32 / 128 * 16;
+
+    floatx16 acc[2][CF];
+#pragma unroll
+    for (int rf = 0; rf < 2; ++rf)
+#pragma unroll
+        for (int j = 0; j < CF; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[rf][j][r] = 0.f;
+
+    auto pair = [&](uint32_t a, uint32_t b) __attribute__((always_inline)) {
+        return join8(*(const u32x4*)(lb + a), *(const u32x4*)(lb + b));
+    };
+    i32x8 x[2][2], w[2][2];                      // [row fragment][half], [buffer][half]
+    float f[2];
+    auto fetch_x = [&](int c, int stage) __attribute__((always_inline)) {
+        const uint32_t st = stage * S::kStage, set = ((c - cb) / 4 & 1) * S::kScaleSet + ((c - cb) & 3) * 4;
+        const float sw = *(const float*)(lb + fl + set);
+#pragma unroll
+        for (int rf = 0; rf < 2; ++rf) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) x[rf][y] = pair(st + xl[y][0] + rf * 4096, st + xl[y][1] + rf * 4096);
+            f[rf] = *(const float*)(lb + sl + set + rf * 512) * sw;
+        }
+    };
+    auto fetch_w = [&](int stage, int j, int y, i32x8& to) __attribute__((always_inline)) {
+        const uint32_t at = stage * S::kStage + wl + j * 4096 + y * 1024;
+        to = pair(at, at + 256);
+    };
+
+    issue_scales(0);
+#pragma unroll
+    for (int s = 0; s < ST; ++s)
+#pragma unroll
+        for (int k = 0; k < S::kData; ++k) issue_op(cb + s, s, k);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((ST - 1) * S::kData) : "memory");
+    fetch_x(cb, 0);
+    fetch_w(0, 0, 0, w[0][0]);
+    fetch_w(0, 0, 1, w[0][1]);
+    floatx16 p[2];                               // the fragment before, not yet added, and its factor
+    float late = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) p[1][r] = 0.f;
+    const floatx16 zero = p[1];
+    int stage = 0;
+    for (int c = cb; c < ce; ++c) {
+        const int ahead = stage == ST - 1 ? 0 : stage + 1;
+        const float f1 = f[1];
+#pragma unroll
+        for (int n = 0; n < 2 * CF; ++n) {
+            const int j = n / 2, rf = n % 2, b = j & 1;
+            if (n == 2 * CF - 2) {               // every read of this group has been issued
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((ST - 2) * S::kData) : "memory");
+                if (((c - cb) & 3) == 0) issue_scales((c - cb) / 4 + 1);
+            }
+            floatx16& now = p[n & 1];
+            floatx16& old = p[(n & 1) ^ 1];
+            now = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[b][0], x[rf][0], zero, 0, 0, 0, 0, 0, 0);
+            now = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[b][1], x[rf][1], now, 0, 0, 0, 0, 0, 0);
+            if (j + 1 < CF) fetch_w(stage, j + 1, rf, w[b ^ 1][rf]);
+            const float g = n == 0 ? late : f[(n & 1) ^ 1];
+            const int oj = n == 0 ? CF - 1 : (n - 1) / 2, orf = n == 0 ? 1 : (n - 1) % 2;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[orf][oj][r] = fmaf(old[r], g, acc[orf][oj][r]);
+            asm volatile("" : "+v"(acc[orf][oj]));   // here, not behind the next barrier
+            if (n >= 2 * CF - 2) {
+#pragma unroll
+                for (int k = 0; k < S::kData; ++k)
+                    if (k * 2 / S::kData == n - (2 * CF - 2)) issue_op(c + ST, stage, k);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        late = f1;
+        fetch_x(c + 1, ahead);
+        fetch_w(ahead, 0, 0, w[0][0]);
+        fetch_w(ahead, 0, 1, w[0][1]);
+        stage = ahead;
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[1][CF - 1][r] = fmaf(p[1][r], late, acc[1][CF - 1][r]);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+    // Results leave through a buffer resource, where a row past M or a column past N lies outside: a branch around the
+    // stores would let the compiler move products into it, and those need every lane's operands.
+    if (nz == 1) {
+        const __amdgpu_buffer_rsrc_t yr = rsrc(Y + row0 * N, (int64_t)rows * N * 2);
+#pragma unroll
+        for (int rf = 0; rf < 2; ++rf) {
+            const int r = wm * 64 + rf * 32 + i;
+#pragma unroll
+            for (int j = 0; j < CF; ++j)
+#pragma unroll
+                for (int a = 0; a < 4; a += 2) {
+                    // columns 8a .. + 7 to the lanes of h = 0, the next eight to those of h = 1
+                    const floatx16& v = acc[rf][j];
+                    u32x4 out;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const auto s = __builtin_amdgcn_permlane32_swap(pack_bf16x2(v[4 * a + 2 * e], v[4 * a + 2 * e + 1]),
+                                                                        pack_bf16x2(v[4 * a + 4 + 2 * e], v[4 * a + 5 + 2 * e]),
+                                                                        false, false);
+                        out[e] = s[0];
+                        out[2 + e] = s[1];
+                    }
+                    const int64_t n = t0 * 64 + (wn * CF + j) * 32 + 8 * a + 8 * h;
+                    __builtin_amdgcn_raw_buffer_store_b128(out, yr, r < rows && n < N ? (uint32_t)(r * N + n) * 2 : kOutside,
+                                                           0, 0);
+                }
+        }
+        return;
+    }
+    // Split over K: float32 partials in fragment order, one per (tile, K slice), that k_fp8_join adds.
+    constexpr uint32_t kPart = S::kRows * 256 * 4;
+    const __amdgpu_buffer_rsrc_t pr = rsrc(part + (int64_t)tile * nz * (kPart / 4), (int64_t)nz * kPart);
+#pragma unroll
+    for (int rf = 0; rf < 2; ++rf)
+#pragma unroll
+        for (int j = 0; j < CF; ++j)
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const floatx16& v = acc[rf][j];
+                const floatx4 q = {v[4 * a], v[4 * a + 1], v[4 * a + 2], v[4 * a + 3]};
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, q), pr,
+                                                       z * kPart + (((wave * 2 + rf) * CF + j) * 4 + a) * 1024 + lane * 16, 0, 0);
+            }
+}
+
+// Adds the slices of the tiles above: a wavefront takes a quarter of one fragment of every slice, in slice order, eight
+// loads in flight.
+template <int WM, int WN, int CF>
+__global__ __launch_bounds__(256) void k_fp8_join(const float* __restrict__ part, int64_t M, int64_t N, int row_tiles,
+                                                  int col_tiles, int nz, uint16_t* __restrict__ Y) {
+    constexpr int kFrags = WM * WN * 2 * CF * 4, kRows = 64 * WM;
+    constexpr uint32_t kPart = kFrags * 1024;
+    const int lane = threadIdx.x & 63, i = lane & 31, h = lane >> 5;
+    const int f = (blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) % kFrags;
+    const int tile = blockIdx.x * 4 / kFrags;
+    const int panel = tile / (8 * col_tiles), in = tile % (8 * col_tiles), prow = min(8, row_tiles - 8 * panel);
+    const int rt = 8 * panel + in % prow, ct = in / prow;
+    const int a = f % 4, j = f / 4 % CF, rf = f / (4 * CF) % 2, wave = f / (8 * CF);
+    const float* p = part + (int64_t)tile * nz * (kPart / 4) + f * 256 + lane * 4;
+    floatx4 sum = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < nz; s += 8) {
+        floatx4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = *(const floatx4*)(p + (int64_t)min(s + u, nz - 1) * (kPart / 4));
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (s + u < nz) sum += v[u];
+    }
+    const int64_t m = (int64_t)rt * kRows + wave / WN * 64 + rf * 32 + i;
+    const int64_t n = (int64_t)ct * 256 + (wave % WN * CF + j) * 32 + 8 * a + 4 * h;
+    if (m < M && n < N)                          // N % 8 == 0: n < N implies n + 3 < N
+        *(uint2*)(Y + m * N + n) = uint2{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
+}
+
 }  // namespace
 
 constexpr size_t kCounterBytes = 65536;
@@ -172,15 +444,39 @@ constexpr int kMaxSlices = 16;
 Fp8GemmPlan plan_fp8_gemm(int64_t M, int64_t K, int64_t N) {
     Fp8GemmPlan p{};
     const int64_t chunks = fp8_kc(K);
-    p.col_tiles = fp8_nt(N);
-    const int rf = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-    p.row_tiles = (M + 16 * rf - 1) / (16 * rf);
-    const int64_t groups = p.col_tiles * p.row_tiles;
-    p.nz = 1;
-    if (groups <= (int64_t)(kCounterBytes / 4))
-        while (p.nz < kMaxSlices && groups * p.nz * 2 <= kCus && chunks / (p.nz * 2) >= 4) p.nz *= 2;
-    p.cstride = (int)std::max<int64_t>(1, std::min<int64_t>(32, kCounterBytes / 4 / groups));
-    p.ws_bytes = p.nz > 1 ? kCounterBytes + (size_t)groups * p.nz * rf * 4096 : 0;
+    if (M <= 64) {
+        p.col_tiles = fp8_nt(N);
+        const int rf = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+        p.row_tiles = (M + 16 * rf - 1) / (16 * rf);
+        const int64_t groups = p.col_tiles * p.row_tiles;
+        p.nz = 1;
+        if (groups <= (int64_t)(kCounterBytes / 4))
+            while (p.nz < kMaxSlices && groups * p.nz * 2 <= kCus && chunks / (p.nz * 2) >= 4) p.nz *= 2;
+        p.cstride = (int)std::max<int64_t>(1, std::min<int64_t>(32, kCounterBytes / 4 / groups));
+        p.ws_bytes = p.nz > 1 ? kCounterBytes + (size_t)groups * p.nz * rf * 4096 : 0;
+        return p;
+    }
+    static const double start_us[3] = {4, 6, 8.5}, turn_us[3] = {.39, .63, 1.10};
+    const double stream = 2 + (double)fp8_codes_bytes(K, N) / 4e6;
+    double best = 1e30;
+    for (int k = 0; k < 3; ++k) {
+        const int wm = 1 << k;
+        const int64_t rt = (M + 64 * wm - 1) / (64 * wm), ct = (N + 255) / 256, tiles = rt * ct;
+        for (int nz = 1; nz <= kMaxSlices; ++nz) {
+            const int64_t turns = (chunks + nz - 1) / nz, groups = tiles * nz;
+            if (nz > 1 && (turns < 4 || groups > kCus)) break;
+            const double rounds = (double)((groups + kCus - 1) / kCus);
+            const double us = std::max(stream, 1.5 + rounds * (start_us[k] + turns * turn_us[k])) +
+                              (nz == 1 ? 0 : 2 + .35e-6 * (double)(groups * 64 * wm * 256 * 4));
+            if (us >= best) continue;
+            best = us;
+            p.wm = wm;
+            p.row_tiles = rt;
+            p.col_tiles = ct;
+            p.nz = nz;
+            p.ws_bytes = nz > 1 ? kCounterBytes + (size_t)groups * 64 * wm * 256 * 4 : 0;
+        }
+    }
     return p;
 }
 
@@ -194,13 +490,39 @@ static hipError_t launch_rows(const uint8_t* xcodes, const float* xscales, int64
     return hipGetLastError();
 }
 
+template <int WM, int WN, int CF, int ST>
+static hipError_t launch_tile(const uint8_t* xcodes, const float* xscales, int64_t M, const uint8_t* codes,
+                              const float* scales, int64_t K, int64_t N, uint16_t* Y, void* ws, const Fp8GemmPlan& p,
+                              hipStream_t st) {
+    using S = Fp8Tile<WM, WN, CF, ST>;
+    const int64_t total = p.row_tiles * p.col_tiles * p.nz, per_xcd = (total + kNumXcd - 1) / kNumXcd;
+    const auto kernel = K % kFp8Group ? k_fp8_gemm_tile<WM, WN, CF, ST, true> : k_fp8_gemm_tile<WM, WN, CF, ST, false>;
+    // the limit is a property of the function on the current device; setting it again is harmless
+    const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
+    if (e != hipSuccess) return e;
+    float* const part = (float*)((char*)ws + kCounterBytes);
+    kernel<<<(unsigned)(per_xcd * kNumXcd), 64 * S::kWaves, S::kLds, st>>>(
+        xcodes, xscales, M, codes, scales, K, N, (int)fp8_kc(K), Y, part, (int)p.row_tiles, (int)p.col_tiles, p.nz,
+        (int)total, (int)per_xcd);
+    const hipError_t launched = hipGetLastError();
+    if (launched != hipSuccess || p.nz == 1) return launched;
+    k_fp8_join<WM, WN, CF><<<(unsigned)(p.row_tiles * p.col_tiles * (S::kWaves * 2 * CF)), 256, 0, st>>>(
+        part, M, N, (int)p.row_tiles, (int)p.col_tiles, p.nz, Y);
+    return hipGetLastError();
+}
+
 hipError_t launch_fp8_gemm(const uint8_t* xcodes, const float* xscales, int64_t M, const uint8_t* codes,
                            const float* scales, int64_t K, int64_t N, uint16_t* Y, void* ws, const Fp8GemmPlan& p,
                            hipStream_t st) {
     const auto run = [&](auto f) { return f(xcodes, xscales, M, codes, scales, K, N, Y, ws, p, st); };
-    if (M <= 16) return run(launch_rows<1, 8>);
-    if (M <= 32) return run(launch_rows<2, 4>);
-    return run(launch_rows<4, 4>);
+    if (p.wm == 0) {
+        if (M <= 16) return run(launch_rows<1, 8>);
+        if (M <= 32) return run(launch_rows<2, 4>);
+        return run(launch_rows<4, 4>);
+    }
+    if (p.wm == 4) return run(launch_tile<4, 2, 4, 2>);
+    if (p.wm == 2) return run(launch_tile<2, 2, 4, 3>);
+    return run(launch_tile<1, 4, 2, 3>);
 }
 
 }  // namespace awq
