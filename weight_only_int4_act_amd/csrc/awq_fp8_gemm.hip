@@ -294,15 +294,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_tile(
     };
     i32x8 x[2][2], w[2][2];                      // [row fragment][half], [buffer][half]
     float f[2];
-    auto fetch_x = [&](int c, int stage) __attribute__((always_inline)) {
+    auto fetch_x = [&](int c, int stage, int rf) __attribute__((always_inline)) {
         const uint32_t st = stage * S::kStage, set = ((c - cb) / 4 & 1) * S::kScaleSet + ((c - cb) & 3) * 4;
-        const float sw = *(const float*)(lb + fl + set);
 #pragma unroll
-        for (int rf = 0; rf < 2; ++rf) {
-#pragma unroll
-            for (int y = 0; y < 2; ++y) x[rf][y] = pair(st + xl[y][0] + rf * 4096, st + xl[y][1] + rf * 4096);
-            f[rf] = *(const float*)(lb + sl + set + rf * 512) * sw;
-        }
+        for (int y = 0; y < 2; ++y) x[rf][y] = pair(st + xl[y][0] + rf * 4096, st + xl[y][1] + rf * 4096);
+        f[rf] = *(const float*)(lb + sl + set + rf * 512) * *(const float*)(lb + fl + set);
     };
     auto fetch_w = [&](int stage, int j, int y, i32x8& to) __attribute__((always_inline)) {
         const uint32_t at = stage * S::kStage + wl + j * 4096 + y * 1024;
@@ -315,7 +311,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_tile(
 #pragma unroll
         for (int k = 0; k < S::kData; ++k) issue_op(cb + s, s, k);
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((ST - 1) * S::kData) : "memory");
-    fetch_x(cb, 0);
+    fetch_x(cb, 0, 0);
+    fetch_x(cb, 0, 1);
     fetch_w(0, 0, 0, w[0][0]);
     fetch_w(0, 0, 1, w[0][1]);
     floatx16 p[2];                               // the fragment before, not yet added, and its factor
@@ -326,7 +323,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_tile(
     int stage = 0;
     for (int c = cb; c < ce; ++c) {
         const int ahead = stage == ST - 1 ? 0 : stage + 1;
-        const float f1 = f[1];
+        const float factor[2] = {f[0], f[1]};    // of this group: f becomes the next one's on the way
 #pragma unroll
         for (int n = 0; n < 2 * CF; ++n) {
             const int j = n / 2, rf = n % 2, b = j & 1;
@@ -338,23 +335,24 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_tile(
             floatx16& old = p[(n & 1) ^ 1];
             now = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[b][0], x[rf][0], zero, 0, 0, 0, 0, 0, 0);
             now = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[b][1], x[rf][1], now, 0, 0, 0, 0, 0, 0);
+            const float g = n == 0 ? late : factor[(n & 1) ^ 1];
+            __builtin_amdgcn_sched_barrier(0);
+            // the next weights; at the end the next group's rows, each where its last product has been issued
             if (j + 1 < CF) fetch_w(stage, j + 1, rf, w[b ^ 1][rf]);
-            const float g = n == 0 ? late : f[(n & 1) ^ 1];
+            else fetch_w(ahead, 0, rf, w[b ^ 1][rf]);
             const int oj = n == 0 ? CF - 1 : (n - 1) / 2, orf = n == 0 ? 1 : (n - 1) % 2;
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[orf][oj][r] = fmaf(old[r], g, acc[orf][oj][r]);
             asm volatile("" : "+v"(acc[orf][oj]));   // here, not behind the next barrier
             if (n >= 2 * CF - 2) {
+                fetch_x(c + 1, ahead, rf);
 #pragma unroll
                 for (int k = 0; k < S::kData; ++k)
                     if (k * 2 / S::kData == n - (2 * CF - 2)) issue_op(c + ST, stage, k);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        late = f1;
-        fetch_x(c + 1, ahead);
-        fetch_w(ahead, 0, 0, w[0][0]);
-        fetch_w(ahead, 0, 1, w[0][1]);
+        late = factor[1];
         stage = ahead;
     }
 #pragma unroll
@@ -521,7 +519,7 @@ hipError_t launch_fp8_gemm(const uint8_t* xcodes, const float* xscales, int64_t 
         return run(launch_rows<4, 4>);
     }
     if (p.wm == 4) return run(launch_tile<4, 2, 4, 2>);
-    if (p.wm == 2) return run(launch_tile<2, 2, 4, 3>);
+    if (p.wm == 2) return run(launch_tile<2, 4, 2, 3>);
     return run(launch_tile<1, 4, 2, 3>);
 }
 
