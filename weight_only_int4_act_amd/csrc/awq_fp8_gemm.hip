@@ -189,7 +189,7 @@ struct Fp8Tile {
     static constexpr int kWaves = WM * WN, kRows = 64 * WM, kCols = 32 * CF * WN;
     static_assert(kCols == 256 && CF % 2 == 0, "tile shape");
     static constexpr int kXu = kRows / 8 / kWaves, kWu = 32 / kWaves, kData = kXu + kWu;   // 1 KB units per wavefront
-    static_assert(kXu % 2 == 0 && kXu * kWaves * 8 == kRows && kWu * kWaves == 32, "even shares");
+    static_assert(kData % 2 == 0 && kXu % 2 == 0 && kXu * kWaves * 8 == kRows && kWu * kWaves == 32, "even shares");
     static constexpr int kX = kRows * 128, kStage = kX + 32768;
     static constexpr int kScaleSet = kRows * 16 + 1024;           // rows, then columns (32 bytes of a transfer's 1 KB)
     static constexpr int kScales = ST * kStage, kLds = kScales + 2 * kScaleSet;
@@ -222,19 +222,24 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_tile(
     const int cts = (int)min<int64_t>(4, nt - t0);                // column tile: zeros
     const uint32_t xrow = (uint32_t)K, srow = (uint32_t)chunks * 4, wtile = (uint32_t)chunks * 8192;
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
-    const i32x4 xr = byte_rsrc(xcodes + row0 * xrow, (uint32_t)rows * xrow);
+    i32x4 xr[S::kXu / 2];                        // one for 16 rows of the wavefront's each
     const i32x4 wr = byte_rsrc(codes + t0 * wtile, (uint32_t)cts * wtile);
     const i32x4 sr = byte_rsrc(xscales + row0 * chunks, (uint32_t)rows * srow);
     const i32x4 fr = byte_rsrc(scales + t0 / 2 * chunks, (uint32_t)min<int64_t>(2, nb - t0 / 2) * srow);
 
     // this lane's places in its wavefront's transfers
-    const int ur = wave * S::kXu * 8 + lane / 8, us = lane & 7;
-    uint32_t xoff[S::kXu];
+#pragma unroll
+    for (int k = 0; k < S::kXu / 2; ++k) {
+        const int first = wave * S::kXu * 8 + 16 * k;
+        xr[k] = byte_rsrc(xcodes + (row0 + min(first, rows)) * xrow, (uint32_t)max(rows - first, 0) * xrow);
+    }
+    const int us = lane & 7;
+    uint32_t xoff[2];
     int xk[2];                                   // first channel of the piece, units of either parity
 #pragma unroll
     for (int k = 0; k < 2; ++k) xk[k] = 16 * (us ^ ((4 * k + lane / 16) & 7));
 #pragma unroll
-    for (int k = 0; k < S::kXu; ++k) xoff[k] = (uint32_t)(ur + 8 * k) * xrow + xk[k & 1];
+    for (int k = 0; k < 2; ++k) xoff[k] = (uint32_t)(lane / 8 + 8 * k) * xrow + xk[k];
     static_assert(8 % S::kWu == 0, "a wavefront's units lie in one column tile");
     const uint32_t woff = (uint32_t)(wave * S::kWu / 8) * wtile + wave * S::kWu % 8 * 1024 + lane * 16;
     // the scales of the slice's groups 4q .. 4q + 3: 64 rows per wavefront (the same ones by several where there are
@@ -263,9 +268,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_tile(
             lds_write_fence();
         }
         if (k < S::kXu) {
-            const i32x4 r = {xr[0], xr[1], on ? xr[2] : 0, xr[3]};
+            const i32x4 r = {xr[k / 2][0], xr[k / 2][1], on ? xr[k / 2][2] : 0, xr[k / 2][3]};
             const uint32_t past = !EDGE || xk[k & 1] < (int)xrow - c * 128 ? 0 : kOutside;   // a piece past K
-            dma16(r, xoff[k] | past, (uint32_t)c * 128, base + to, 0);
+            dma16(r, xoff[k & 1] | past, (uint32_t)c * 128, base + to, 0);
         } else {
             const i32x4 r = {wr[0], wr[1], on ? wr[2] : 0, wr[3]};
             dma16(r, woff, (uint32_t)c * 8192 + (k - S::kXu) * 1024, base + to, 0);
@@ -273,11 +278,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_tile(
     };
 
     const uint8_t* const lb = (const uint8_t*)lds;
-    uint32_t xl[2][2];                           // by half of the channels and piece
-#pragma unroll
-    for (int y = 0; y < 2; ++y)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) xl[y][p] = (wm * 64 + i) * 128 + ((4 * y + 2 * h + p) ^ (i / 2 & 7)) * 16;
+    uint32_t xl = (wm * 64 + i) * 128 + ((2 * h) ^ (i / 2 & 7)) * 16;   // piece p of half y: ^ (4 y + p) * 16
     const uint32_t wl = S::kX + wn * CF * 4096 + (i / 16) * 2048 + h * 512 + (i & 15) * 16;
     const uint32_t sl = S::kScales + (wm * 64 + i) * 16, fl = S::kScales + S::kRows * 16 + wn * CF * 32 / 128 * 16;
 
@@ -293,12 +294,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_tile(
         return join8(*(const u32x4*)(lb + a), *(const u32x4*)(lb + b));
     };
     i32x8 x[2][2], w[2][2];                      // [row fragment][half], [buffer][half]
-    float f[2];
-    auto fetch_x = [&](int c, int stage, int rf) __attribute__((always_inline)) {
-        const uint32_t st = stage * S::kStage, set = ((c - cb) / 4 & 1) * S::kScaleSet + ((c - cb) & 3) * 4;
+    auto fetch_x = [&](int stage, int rf) __attribute__((always_inline)) {
+        const uint32_t st = stage * S::kStage + rf * 4096;
+        asm volatile("" : "+v"(xl));             // four exclusive ors a turn instead of four registers
 #pragma unroll
-        for (int y = 0; y < 2; ++y) x[rf][y] = pair(st + xl[y][0] + rf * 4096, st + xl[y][1] + rf * 4096);
-        f[rf] = *(const float*)(lb + sl + set + rf * 512) * *(const float*)(lb + fl + set);
+        for (int y = 0; y < 2; ++y) x[rf][y] = pair(st + (xl ^ (64 * y)), st + (xl ^ (64 * y + 16)));
     };
     auto fetch_w = [&](int stage, int j, int y, i32x8& to) __attribute__((always_inline)) {
         const uint32_t at = stage * S::kStage + wl + j * 4096 + y * 1024;
@@ -309,21 +309,22 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_tile(
 #pragma unroll
     for (int s = 0; s < ST; ++s)
 #pragma unroll
-        for (int k = 0; k < S::kData; ++k) issue_op(cb + s, s, k);
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((ST - 1) * S::kData) : "memory");
-    fetch_x(cb, 0, 0);
-    fetch_x(cb, 0, 1);
+        for (int k = 0; k < S::kData; ++k)
+            if (s < ST - 1 || k * 4 / S::kData < 2) issue_op(cb + s, s, k);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((ST - 2) * S::kData + S::kData / 2) : "memory");
+    fetch_x(0, 0);
+    fetch_x(0, 1);
     fetch_w(0, 0, 0, w[0][0]);
     fetch_w(0, 0, 1, w[0][1]);
     floatx16 p[2];                               // the fragment before, not yet added, and its factor
-    float late = 0.f;
+    float late = 0.f, sw = 0.f;
 #pragma unroll
     for (int r = 0; r < 16; ++r) p[1][r] = 0.f;
     const floatx16 zero = p[1];
     int stage = 0;
     for (int c = cb; c < ce; ++c) {
         const int ahead = stage == ST - 1 ? 0 : stage + 1;
-        const float factor[2] = {f[0], f[1]};    // of this group: f becomes the next one's on the way
+        float factor[2];
 #pragma unroll
         for (int n = 0; n < 2 * CF; ++n) {
             const int j = n / 2, rf = n % 2, b = j & 1;
@@ -335,8 +336,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_tile(
             floatx16& old = p[(n & 1) ^ 1];
             now = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[b][0], x[rf][0], zero, 0, 0, 0, 0, 0, 0);
             now = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[b][1], x[rf][1], now, 0, 0, 0, 0, 0, 0);
-            const float g = n == 0 ? late : factor[(n & 1) ^ 1];
             __builtin_amdgcn_sched_barrier(0);
+            if (n == 0) {
+                const uint32_t set = ((c - cb) / 4 & 1) * S::kScaleSet + ((c - cb) & 3) * 4;
+                factor[0] = *(const float*)(lb + sl + set);
+                factor[1] = *(const float*)(lb + sl + set + 512);
+                sw = *(const float*)(lb + fl + set);
+            }
+            if (n == 1) factor[0] *= sw, factor[1] *= sw;
+            const float g = n == 0 ? late : factor[(n & 1) ^ 1];
             // the next weights; at the end the next group's rows, each where its last product has been issued
             if (j + 1 < CF) fetch_w(stage, j + 1, rf, w[b ^ 1][rf]);
             else fetch_w(ahead, 0, rf, w[b ^ 1][rf]);
@@ -344,11 +352,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_gemm_tile(
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[orf][oj][r] = fmaf(old[r], g, acc[orf][oj][r]);
             asm volatile("" : "+v"(acc[orf][oj]));   // here, not behind the next barrier
-            if (n >= 2 * CF - 2) {
-                fetch_x(c + 1, ahead, rf);
+            if (n >= 2 * CF - 2) fetch_x(ahead, rf);
+            // the transfers of a batch over four steps: two behind the barrier, two of the next turn
 #pragma unroll
-                for (int k = 0; k < S::kData; ++k)
-                    if (k * 2 / S::kData == n - (2 * CF - 2)) issue_op(c + ST, stage, k);
+            for (int k = 0; k < S::kData; ++k) {
+                if (k * 4 / S::kData == n - (2 * CF - 2)) issue_op(c + ST, stage, k);
+                if (k * 4 / S::kData == n + 2) issue_op(c + ST - 1, stage == 0 ? ST - 1 : stage - 1, k);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
