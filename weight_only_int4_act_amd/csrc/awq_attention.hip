@@ -261,18 +261,285 @@ __global__ __launch_bounds__(256) void k_attention_rows(Args a, Sequences s, Cac
     if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// ---------------------------------------------------------------- many rows: tiles in LDS
+// Bound by the matrix cores and, beside them, the exponentials.  A workgroup takes 128 rows, 32 for each of four
+// wavefronts, and a slice of the tokens, 64 at a time.  K and V of a tile are loaded once for all rows, a tile ahead, widened
+// to bf16 with their scales on the way into LDS (exact), two tiles deep, one barrier a tile.
+//   first product   S^T = K Q^T by 32x32x16 products: lane (i, h) = (lane % 32, lane / 32) gives row i of K and of Q, and takes,
+//                   of query row i, token 8 (r / 4) + 4h + r % 4 of 32;
+//   second product  O^T = V^T P^T: the lane's own results are its operand, if V's tokens 16s .. 16s + 15 lie in the order
+//                   0-3, 8-11 (h = 0), 4-7, 12-15 (h = 1): the order in which they go into LDS.
+// So a row's maximum and sum cross two lanes only.  The running maximum is taken over when a tile passes it by more
+// than 2^8 (any reference gives the same quotient, and p up to 2^8 loses nothing), so that the sums are seldom rescaled.
+// LDS rows (K: a token, V: a number of the head) keep 16-byte piece q at slot q ^ (row % 16) where a row is 256 bytes, at
+// q ^ (row / 2 % 8) where it is 128: lanes that a read serves together hit different banks.
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ floatx16 mfma32x32x16(const bf16x8& a, const bf16x8& b, const floatx16& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+constexpr int kTileRows = 128;
+
+template <int D>
+__global__ __launch_bounds__(256, 2) void k_attention_tile(Args a, Sequences s, Cache c) {
+    constexpr int NP = D / 64, NB = D / 32;      // 16-byte pieces of K and of V per thread; blocks of 32 numbers
+    constexpr int kK = kTile * D * 2, kStage = 2 * kK;
+    __shared__ u32x4 lds[2 * kStage / 16];
+    __shared__ uint32_t arrival;
+    lds_poison_start(&lds[0], 2 * kStage / 16);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int i = lane & 31, h = lane >> 5;
+    const int head = blockIdx.x % c.Hk, rest = blockIdx.x / c.Hk;
+    const int z = rest % a.split, rt = a.tiles - 1 - rest / a.split % a.tiles, b = rest / a.split / a.tiles;
+    const NewTokens t = new_tokens(s, b, a.M);
+    const int rows = min(t.count, s.max_q) * a.G;
+    if (kTileRows * rt >= rows) return;          // the whole workgroup
+    const int row = kTileRows * rt + 32 * wave + i, mine = min(row, rows - 1), tok = mine / a.G;
+    const int64_t qat = ((int64_t)(t.row0 + tok) * a.Hq + head * a.G + mine % a.G) * D;
+    // tokens that this lane's row sees, that every row of the wavefront sees, and that any row of the workgroup does
+    const int cap = s.width << c.logT;
+    auto reach = [&](int r) { return min(a.causal ? max(t.start + min(r, rows - 1) / a.G + 1, 0) : t.length, cap); };
+    const int base_row = kTileRows * rt + 32 * wave;
+    const int seen = reach(row), all = reach(base_row), wave_most = base_row < rows ? reach(base_row + 31) : 0;
+    const int most = reach(kTileRows * rt + kTileRows - 1);
+    const int tiles = (most + kTile - 1) / kTile;
+    const int used = max(min(a.split, (tiles + 3) / 4), 1);      // slices of this sequence: four tiles each or more
+    if (z >= used) return;
+    const int per = (tiles + used - 1) / used, tb = min(z * per, tiles), te = min(tb + per, tiles);
+
+    // scores are f times the products with f > 0: a negative scale's sign goes into q, a zero scale makes q zero
+    const float f = a.scale == 0.f ? 1.f : fabsf(a.scale);
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u, keep_q = a.scale == 0.f ? 0u : ~0u;
+    bf16x8 q[D / 16];
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) {
+        u32x4 v = *(const u32x4*)(a.q + qat + 16 * n + 8 * h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (v[e] ^ flip) & keep_q;
+        q[n] = __builtin_bit_cast(bf16x8, v);
+    }
+
+    const int32_t* const table = s.table + (int64_t)b * s.width;
+    // of the tile at `tile`, by lane % 4: the block of 16 tokens, or -1
+    auto blocks_of = [&](int tile) __attribute__((always_inline)) {
+        const int first = tile * kTile + 16 * (lane & 3), j = first >> c.logT;
+        const int v = first < most && j < s.width ? table[j] : -1;
+        return v >= 0 && v < c.blocks ? v : -1;
+    };
+    auto scales_of = [&](int blk) __attribute__((always_inline)) {
+        return (uint32_t)*(const uint16_t*)(c.scales + ((int64_t)max(blk, 0) * c.Hk + head) * 2);
+    };
+    // piece n of this thread: K of token 32 n + thread / 8 (D = 128) or thread / 4, V of 16 tokens and one number;
+    // both belong to 16 tokens that are the wavefront's
+    auto group_of = [&](int n) { return D == 128 ? 2 * n + (wave >> 1) : wave; };
+    constexpr int kPieces = D / 16;              // of a K row
+    const int token = threadIdx.x / kPieces, piece = threadIdx.x % kPieces, number = threadIdx.x % D;
+    u32x4 kn[NP], vn[NP];
+    auto load = [&](int tile, int blk) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const int g = group_of(n), first = tile * kTile + 16 * g;
+            const int64_t base = ((int64_t)max(__builtin_amdgcn_readlane(blk, g), 0) * c.Hk + head) * c.T + (first & (c.T - 1));
+            kn[n] = *(const u32x4*)(c.k + (base + (token & 15)) * D + 16 * piece);
+            vn[n] = *(const u32x4*)(c.v + base * D + 16 * number);
+        }
+    };
+    uint8_t* const lb = (uint8_t*)lds;
+    auto k_slot = [](int r, int p) { return D == 128 ? p ^ (r & 15) : p ^ (r / 2 & 7); };
+    auto store = [&](int tile, int stage, int blk, uint32_t sc) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const int g = group_of(n), r = 16 * g + (token & 15);
+            const uint32_t e = __builtin_amdgcn_readlane(sc, g);
+            const bool marked = (e & 255) == 255 || e >> 8 == 255;   // K becomes NaN, V finite
+            const float ks = __uint_as_float(marked ? 0x7f800000u : (e & 255) << 23);
+            const float vs = __uint_as_float(marked ? 127u << 23 : (e >> 8) << 23);
+            uint8_t* const kr = lb + stage * kStage + r * D * 2;
+            *(bf16x8*)(kr + 16 * k_slot(r, 2 * piece)) = widen_codes(kn[n][0], kn[n][1], ks);
+            *(bf16x8*)(kr + 16 * k_slot(r, 2 * piece + 1)) = widen_codes(kn[n][2], kn[n][3], ks);
+            // what lies behind the sequence's last token, or in no block, may be anything, NaN among it: zeros
+            const int live = __builtin_amdgcn_readlane(blk, g) < 0 ? 0 : t.length - tile * kTile - 16 * g;
+            u32x4 x = vn[n];
+            if (live < 16) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int left = min(max(live - 4 * y, 0), 4);
+                    x[y] = left == 4 ? x[y] : x[y] & ((1u << 8 * left) - 1);
+                }
+            }
+            uint8_t* const vr = lb + stage * kStage + kK + number * 128;
+            *(bf16x8*)(vr + 16 * ((2 * g) ^ (number / 2 & 7))) = widen_codes(x[0], x[2], vs);
+            *(bf16x8*)(vr + 16 * ((2 * g + 1) ^ (number / 2 & 7))) = widen_codes(x[1], x[3], vs);
+        }
+    };
+
+    floatx16 o[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[n][r] = 0.f;
+    float m = -INFINITY, sum = 0.f;
+
+    int blk = blocks_of(tb), next = blocks_of(tb + 1);
+    uint32_t sc = scales_of(blk);
+    uint32_t holes = (uint32_t)__ballot(blk >= 0) & 15;          // 16-token groups that are there
+    load(tb, blk);
+    store(tb, 0, blk, sc);
+    __syncthreads();
+    for (int tile = tb; tile < te; ++tile) {
+        const int stage = (tile - tb) & 1, first = tile * kTile;
+        const uint32_t there = holes;
+        blk = next;
+        next = blocks_of(tile + 2);
+        if (tile + 1 < te) {
+            sc = scales_of(blk);
+            holes = (uint32_t)__ballot(blk >= 0) & 15;
+            load(tile + 1, blk);
+        }
+        if (first < wave_most) {
+            const uint8_t* const kb = lb + stage * kStage;
+            floatx16 p[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) p[u][r] = 0.f;
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n)
+                    p[u] = mfma32x32x16(*(const bf16x8*)(kb + (32 * u + i) * D * 2 + 16 * k_slot(i, 2 * n + h)), q[n], p[u]);
+            }
+            if (first + kTile > all || there != 15) {            // a token that some row does not see
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int at = 32 * u + 8 * (r / 4) + 4 * h + r % 4;
+                        if (!(first + at < seen && there >> (2 * u + r / 8) & 1)) p[u][r] = -INFINITY;
+                    }
+            }
+            float top = fmaxf(p[0][0], p[1][0]);
+#pragma unroll
+            for (int r = 1; r < 16; ++r) top = fmaxf(top, fmaxf(p[0][r], p[1][r]));
+            const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+            top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * f;
+            if (__any(top > m + 8.f)) {          // the first numbers are, beside minus infinity
+                const float now = fmaxf(m, top), base = now == -INFINITY ? 0.f : now;
+                const float keep = __builtin_amdgcn_exp2f(m - base);
+                m = now;
+                sum *= keep;
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[n][r] *= keep;
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            bf16x8 w[4];                         // 16 tokens each
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    p[u][r] = __builtin_amdgcn_exp2f(fmaf(p[u][r], f, -base));
+                    sum += p[u][r];
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    w[2 * u + y] = __builtin_bit_cast(
+                        bf16x8, u32x4{pack_bf16x2(p[u][8 * y], p[u][8 * y + 1]), pack_bf16x2(p[u][8 * y + 2], p[u][8 * y + 3]),
+                                      pack_bf16x2(p[u][8 * y + 4], p[u][8 * y + 5]), pack_bf16x2(p[u][8 * y + 6], p[u][8 * y + 7])});
+            }
+            const uint8_t* const vb = kb + kK;
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+                    o[n] = mfma32x32x16(*(const bf16x8*)(vb + (32 * n + i) * 128 + 16 * ((2 * y + h) ^ (i / 2 & 7))), w[y], o[n]);
+        }
+        if (tile + 1 < te) store(tile + 1, stage ^ 1, blk, sc);
+        __syncthreads();
+    }
+    const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
+    sum = __uint_as_float(halves[0]) + __uint_as_float(halves[1]);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) asm volatile("" : "+v"(o[n]));  // the products stay before the branches
+    auto write = [&](float total) __attribute__((always_inline)) {
+        const float inv = total == 0.f ? 0.f : 1.f / total;      // nothing seen: zeros
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int y = 0; y < 4; y += 2) {     // numbers 8y .. + 7 to the lanes of h = 0, the next eight to those of h = 1
+                u32x4 out;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const auto w = __builtin_amdgcn_permlane32_swap(
+                        pack_bf16x2(o[n][4 * y + 2 * e] * inv, o[n][4 * y + 2 * e + 1] * inv),
+                        pack_bf16x2(o[n][4 * y + 4 + 2 * e] * inv, o[n][4 * y + 5 + 2 * e] * inv), false, false);
+                    out[e] = w[0];
+                    out[2 + e] = w[1];
+                }
+                if (row < rows) *(u32x4*)(a.out + qat + 32 * n + 8 * y + 8 * h) = out;
+            }
+    };
+    if (used == 1) {
+        write(sum);
+        return;
+    }
+    // several slices: maximum and sum of the rows, then the numbers, per slice; the last workgroup to arrive joins them in
+    // slice order
+    constexpr uint32_t kPart = kTileRows * 8 + kTileRows * D * 4;
+    const int slot = (b * a.tiles + rt) * c.Hk + head;
+    const __amdgpu_buffer_rsrc_t pr = rsrc((const char*)a.part + (int64_t)slot * a.split * kPart, (int64_t)a.split * kPart);
+    auto at = [&](int z, int n, int y) { return z * kPart + kTileRows * 8 + (uint32_t)(((wave * NB + n) * 4 + y) * 64 + lane) * 16; };
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            store4_agent(pr, at(z, n, y), floatx4{o[n][4 * y], o[n][4 * y + 1], o[n][4 * y + 2], o[n][4 * y + 3]});
+    const uint32_t st = (32 * wave + i) * 8;
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(h ? sum : m), pr, z * kPart + st + 4 * h, 0, kCpolAgent);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wavefront's part has landed
+    __syncthreads();
+    uint32_t* const counter = a.cnt + (int64_t)slot * a.cstride;
+    if (threadIdx.x == 0) arrival = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (arrival != (uint32_t)(used - 1)) return;
+    float ms = -INFINITY, ts = 0.f;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[n][r] = 0.f;
+    for (int y = 0; y < used; ++y) {
+        const float mz = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(pr, y * kPart + st, 0, kCpolAgent));
+        const float tz = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(pr, y * kPart + st + 4, 0, kCpolAgent));
+        floatx4 v[NB][4];
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[n][e] = load4_agent(pr, at(y, n, e));
+        const float now = fmaxf(ms, mz), base = now == -INFINITY ? 0.f : now;
+        const float keep = __builtin_amdgcn_exp2f(ms - base), g = __builtin_amdgcn_exp2f(mz - base);
+        ms = now;
+        ts = ts * keep + tz * g;
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[n][r] = o[n][r] * keep + v[n][r / 4][r % 4] * g;
+    }
+    write(ts);
+    if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 }  // namespace
 
 AttentionPlan plan_attention(int64_t M, int n_seq, int max_q, int Hq, int Hk, int D) {
     AttentionPlan p{};
     const int64_t rows = std::min<int64_t>(max_q, M) * (Hq / Hk);
-    p.tiles = (int)((rows + 15) / 16);
-    const int64_t slots = (int64_t)n_seq * p.tiles * Hk;
+    p.rows = rows <= 32 ? 16 : kTileRows;
+    p.tiles = (int)((rows + p.rows - 1) / p.rows);
+    const int64_t slots = (int64_t)n_seq * p.tiles * Hk, enough = p.rows == 16 ? 1024 : 512;
     p.split = 1;
     if (slots <= (int64_t)(kCounterBytes / 4))
-        while (p.split < 64 && slots * p.split < 1024) p.split *= 2;
+        while (p.split < 64 && slots * p.split < enough) p.split *= 2;
     p.cstride = (int)std::max<int64_t>(1, std::min<int64_t>(32, kCounterBytes / 4 / slots));
-    p.ws_bytes = p.split > 1 ? kCounterBytes + (size_t)slots * p.split * (128 + 64 * (size_t)D) : 0;
+    p.ws_bytes = p.split > 1 ? kCounterBytes + (size_t)slots * p.split * p.rows * (8 + 4 * (size_t)D) : 0;
     return p;
 }
 
@@ -281,9 +548,12 @@ hipError_t launch_attention(const uint16_t* q, int64_t M, int Hq, const Sequence
     const Args a{q, out, (float*)((char*)ws + kCounterBytes), (uint32_t*)ws, (int)M, Hq, Hq / c.Hk, causal, p.tiles,
                  p.split, p.cstride, scale * kLog2e};
     const unsigned grid = (unsigned)((int64_t)s.n * p.tiles * p.split * c.Hk);
-    if (c.D == 128) k_attention_rows<128><<<grid, 256, 0, st>>>(a, s, c);
-    else k_attention_rows<64><<<grid, 256, 0, st>>>(a, s, c);
-    return hipGetLastError();
+    const auto go = [&](auto kernel) {
+        kernel<<<grid, 256, 0, st>>>(a, s, c);
+        return hipGetLastError();
+    };
+    if (p.rows == 16) return c.D == 128 ? go(k_attention_rows<128>) : go(k_attention_rows<64>);
+    return c.D == 128 ? go(k_attention_tile<128>) : go(k_attention_tile<64>);
 }
 
 }  // namespace awq
