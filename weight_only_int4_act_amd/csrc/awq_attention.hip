@@ -278,6 +278,14 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ floatx16 mfma32x32x16(const bf16x8& a, const bf16x8& b, const floatx16& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
+// c + the eight numbers
+__device__ __forceinline__ float add_pairs(const bf16x8& v, float c) {
+    const u32x4 w = __builtin_bit_cast(u32x4, v);
+    const bf16x2 one = {(__bf16)1.f, (__bf16)1.f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w[e]), one, c, false);
+    return c;
+}
 constexpr int kTileRows = 128;
 
 template <int D>
@@ -361,11 +369,9 @@ __global__ __launch_bounds__(256, 2) void k_attention_tile(Args a, Sequences s, 
             const int live = __builtin_amdgcn_readlane(blk, g) < 0 ? 0 : t.length - tile * kTile - 16 * g;
             u32x4 x = vn[n];
             if (live < 16) {
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int left = min(max(live - 4 * y, 0), 4);
-                    x[y] = left == 4 ? x[y] : x[y] & ((1u << 8 * left) - 1);
-                }
+                const uint64_t bytes = live >= 8 ? ~0ull : (1ull << 8 * max(live, 0)) - 1;
+                const uint64_t more = live <= 8 ? 0ull : (1ull << 8 * (live - 8)) - 1;
+                x &= u32x4{(uint32_t)bytes, (uint32_t)(bytes >> 32), (uint32_t)more, (uint32_t)(more >> 32)};
             }
             uint8_t* const vr = lb + stage * kStage + kK + number * 128;
             *(bf16x8*)(vr + 16 * ((2 * g) ^ (number / 2 & 7))) = widen_codes(x[0], x[2], vs);
@@ -416,11 +422,13 @@ __global__ __launch_bounds__(256, 2) void k_attention_tile(Args a, Sequences s, 
                         if (!(first + at < seen && there >> (2 * u + r / 8) & 1)) p[u][r] = -INFINITY;
                     }
             }
-            float top = fmaxf(p[0][0], p[1][0]);
+            // (a maximum that hands on NaN, which makes the row NaN anyway: one instruction for two numbers)
+            float top = __builtin_elementwise_maximum(p[0][0], p[1][0]);
 #pragma unroll
-            for (int r = 1; r < 16; ++r) top = fmaxf(top, fmaxf(p[0][r], p[1][r]));
+            for (int r = 1; r < 16; ++r)
+                top = __builtin_elementwise_maximum(top, __builtin_elementwise_maximum(p[0][r], p[1][r]));
             const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
-            top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * f;
+            top = __builtin_elementwise_maximum(__uint_as_float(both[0]), __uint_as_float(both[1])) * f;
             if (__any(top > m + 8.f)) {          // the first numbers are, beside minus infinity
                 const float now = fmaxf(m, top), base = now == -INFINITY ? 0.f : now;
                 const float keep = __builtin_amdgcn_exp2f(m - base);
@@ -436,16 +444,16 @@ __global__ __launch_bounds__(256, 2) void k_attention_tile(Args a, Sequences s, 
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    p[u][r] = __builtin_amdgcn_exp2f(fmaf(p[u][r], f, -base));
-                    sum += p[u][r];
-                }
+                for (int r = 0; r < 16; ++r) p[u][r] = __builtin_amdgcn_exp2f(fmaf(p[u][r], f, -base));
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
                     w[2 * u + y] = __builtin_bit_cast(
                         bf16x8, u32x4{pack_bf16x2(p[u][8 * y], p[u][8 * y + 1]), pack_bf16x2(p[u][8 * y + 2], p[u][8 * y + 3]),
                                       pack_bf16x2(p[u][8 * y + 4], p[u][8 * y + 5]), pack_bf16x2(p[u][8 * y + 6], p[u][8 * y + 7])});
             }
+            // the sum of the rounded p, two in an instruction, in float32: what the second product weighs V with
+#pragma unroll
+            for (int y = 0; y < 4; ++y) sum = add_pairs(w[y], sum);
             const uint8_t* const vb = kb + kK;
 #pragma unroll
             for (int y = 0; y < 4; ++y)
