@@ -283,15 +283,19 @@ __device__ __forceinline__ float add_pairs(const bf16x8& v, float c) {
     const u32x4 w = __builtin_bit_cast(u32x4, v);
     const bf16x2 one = {(__bf16)1.f, (__bf16)1.f};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w[e]), one, c, false);
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t two = w[e];               // (a vector's element itself would be cast from its first bytes)
+        c = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, two), one, c, false);
+    }
     return c;
 }
-constexpr int kTileRows = 128;
 
-template <int D>
-__global__ __launch_bounds__(256, 2) void k_attention_tile(Args a, Sequences s, Cache c) {
+// NW wavefronts; 16 NW tokens are staged at a time.
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences s, Cache c) {
     constexpr int NP = D / 64, NB = D / 32;      // 16-byte pieces of K and of V per thread; blocks of 32 numbers
-    constexpr int kK = kTile * D * 2, kStage = 2 * kK;
+    constexpr int kTileRows = 32 * NW, NG = NW, kTokens = 16 * NG;   // groups of 16 tokens of a stage
+    constexpr int kVRow = kTokens * 2, kK = kTokens * D * 2, kStage = 2 * kK;
     __shared__ u32x4 lds[2 * kStage / 16];
     __shared__ uint32_t arrival;
     lds_poison_start(&lds[0], 2 * kStage / 16);
@@ -310,8 +314,8 @@ __global__ __launch_bounds__(256, 2) void k_attention_tile(Args a, Sequences s, 
     const int base_row = kTileRows * rt + 32 * wave;
     const int seen = reach(row), all = reach(base_row), wave_most = base_row < rows ? reach(base_row + 31) : 0;
     const int most = reach(kTileRows * rt + kTileRows - 1);
-    const int tiles = (most + kTile - 1) / kTile;
-    const int used = max(min(a.split, (tiles + 3) / 4), 1);      // slices of this sequence: four tiles each or more
+    const int tiles = (most + kTokens - 1) / kTokens;
+    const int used = max(min(a.split, (tiles + 3) / 4), 1);      // slices of this sequence: four stages each or more
     if (z >= used) return;
     const int per = (tiles + used - 1) / used, tb = min(z * per, tiles), te = min(tb + per, tiles);
 
@@ -328,25 +332,25 @@ __global__ __launch_bounds__(256, 2) void k_attention_tile(Args a, Sequences s, 
     }
 
     const int32_t* const table = s.table + (int64_t)b * s.width;
-    // of the tile at `tile`, by lane % 4: the block of 16 tokens, or -1
+    // of stage `tile`, by lane % NG: the block of 16 tokens, or -1
     auto blocks_of = [&](int tile) __attribute__((always_inline)) {
-        const int first = tile * kTile + 16 * (lane & 3), j = first >> c.logT;
+        const int first = tile * kTokens + 16 * (lane & (NG - 1)), j = first >> c.logT;
         const int v = first < most && j < s.width ? table[j] : -1;
         return v >= 0 && v < c.blocks ? v : -1;
     };
     auto scales_of = [&](int blk) __attribute__((always_inline)) {
         return (uint32_t)*(const uint16_t*)(c.scales + ((int64_t)max(blk, 0) * c.Hk + head) * 2);
     };
-    // piece n of this thread: K of token 32 n + thread / 8 (D = 128) or thread / 4, V of 16 tokens and one number;
-    // both belong to 16 tokens that are the wavefront's
-    auto group_of = [&](int n) { return D == 128 ? 2 * n + (wave >> 1) : wave; };
+    // piece n of this thread: K of one token, V of 16 tokens and one number; both belong to 16 tokens that are the
+    // wavefront's
+    auto group_of = [&](int n) { return D == 128 ? NG / 2 * n + (wave >> 1) : wave; };
     constexpr int kPieces = D / 16;              // of a K row
     const int token = threadIdx.x / kPieces, piece = threadIdx.x % kPieces, number = threadIdx.x % D;
     u32x4 kn[NP], vn[NP];
     auto load = [&](int tile, int blk) __attribute__((always_inline)) {
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-            const int g = group_of(n), first = tile * kTile + 16 * g;
+            const int g = group_of(n), first = tile * kTokens + 16 * g;
             const int64_t base = ((int64_t)max(__builtin_amdgcn_readlane(blk, g), 0) * c.Hk + head) * c.T + (first & (c.T - 1));
             kn[n] = *(const u32x4*)(c.k + (base + (token & 15)) * D + 16 * piece);
             vn[n] = *(const u32x4*)(c.v + base * D + 16 * number);
@@ -354,6 +358,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_tile(Args a, Sequences s, 
     };
     uint8_t* const lb = (uint8_t*)lds;
     auto k_slot = [](int r, int p) { return D == 128 ? p ^ (r & 15) : p ^ (r / 2 & 7); };
+    auto v_slot = [](int r, int p) { return kVRow == 256 ? p ^ (r & 15) : p ^ (r / 2 & 7); };
     auto store = [&](int tile, int stage, int blk, uint32_t sc) __attribute__((always_inline)) {
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
@@ -366,16 +371,16 @@ __global__ __launch_bounds__(256, 2) void k_attention_tile(Args a, Sequences s, 
             *(bf16x8*)(kr + 16 * k_slot(r, 2 * piece)) = widen_codes(kn[n][0], kn[n][1], ks);
             *(bf16x8*)(kr + 16 * k_slot(r, 2 * piece + 1)) = widen_codes(kn[n][2], kn[n][3], ks);
             // what lies behind the sequence's last token, or in no block, may be anything, NaN among it: zeros
-            const int live = __builtin_amdgcn_readlane(blk, g) < 0 ? 0 : t.length - tile * kTile - 16 * g;
+            const int live = __builtin_amdgcn_readlane(blk, g) < 0 ? 0 : t.length - tile * kTokens - 16 * g;
             u32x4 x = vn[n];
             if (live < 16) {
                 const uint64_t bytes = live >= 8 ? ~0ull : (1ull << 8 * max(live, 0)) - 1;
                 const uint64_t more = live <= 8 ? 0ull : (1ull << 8 * (live - 8)) - 1;
                 x &= u32x4{(uint32_t)bytes, (uint32_t)(bytes >> 32), (uint32_t)more, (uint32_t)(more >> 32)};
             }
-            uint8_t* const vr = lb + stage * kStage + kK + number * 128;
-            *(bf16x8*)(vr + 16 * ((2 * g) ^ (number / 2 & 7))) = widen_codes(x[0], x[2], vs);
-            *(bf16x8*)(vr + 16 * ((2 * g + 1) ^ (number / 2 & 7))) = widen_codes(x[1], x[3], vs);
+            uint8_t* const vr = lb + stage * kStage + kK + number * kVRow;
+            *(bf16x8*)(vr + 16 * v_slot(number, 2 * g)) = widen_codes(x[0], x[2], vs);
+            *(bf16x8*)(vr + 16 * v_slot(number, 2 * g + 1)) = widen_codes(x[1], x[3], vs);
         }
     };
 
@@ -388,22 +393,27 @@ __global__ __launch_bounds__(256, 2) void k_attention_tile(Args a, Sequences s, 
 
     int blk = blocks_of(tb), next = blocks_of(tb + 1);
     uint32_t sc = scales_of(blk);
-    uint32_t holes = (uint32_t)__ballot(blk >= 0) & 15;          // 16-token groups that are there
+    constexpr uint32_t kAll = (1u << NG) - 1;
+    uint32_t holes = (uint32_t)__ballot(blk >= 0) & kAll;        // 16-token groups that are there
     load(tb, blk);
     store(tb, 0, blk, sc);
     __syncthreads();
     for (int tile = tb; tile < te; ++tile) {
-        const int stage = (tile - tb) & 1, first = tile * kTile;
+        const int stage = (tile - tb) & 1, base_token = tile * kTokens;
         const uint32_t there = holes;
         blk = next;
         next = blocks_of(tile + 2);
         if (tile + 1 < te) {
             sc = scales_of(blk);
-            holes = (uint32_t)__ballot(blk >= 0) & 15;
+            holes = (uint32_t)__ballot(blk >= 0) & kAll;
             load(tile + 1, blk);
         }
-        if (first < wave_most) {
-            const uint8_t* const kb = lb + stage * kStage;
+#pragma unroll
+        for (int part = 0; part < NG / 4; ++part) {              // 64 tokens at a time
+            const int first = base_token + 64 * part;
+            if (first >= wave_most) break;
+            const uint32_t groups = there >> 4 * part & 15;
+            const uint8_t* const kb = lb + stage * kStage + 64 * part * D * 2;
             floatx16 p[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -413,13 +423,13 @@ __global__ __launch_bounds__(256, 2) void k_attention_tile(Args a, Sequences s, 
                 for (int n = 0; n < D / 16; ++n)
                     p[u] = mfma32x32x16(*(const bf16x8*)(kb + (32 * u + i) * D * 2 + 16 * k_slot(i, 2 * n + h)), q[n], p[u]);
             }
-            if (first + kTile > all || there != 15) {            // a token that some row does not see
+            if (first + kTile > all || groups != 15) {            // a token that some row does not see
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
                         const int at = 32 * u + 8 * (r / 4) + 4 * h + r % 4;
-                        if (!(first + at < seen && there >> (2 * u + r / 8) & 1)) p[u][r] = -INFINITY;
+                        if (!(first + at < seen && groups >> (2 * u + r / 8) & 1)) p[u][r] = -INFINITY;
                     }
             }
             // (a maximum that hands on NaN, which makes the row NaN anyway: one instruction for two numbers)
@@ -454,12 +464,12 @@ __global__ __launch_bounds__(256, 2) void k_attention_tile(Args a, Sequences s, 
             // the sum of the rounded p, two in an instruction, in float32: what the second product weighs V with
 #pragma unroll
             for (int y = 0; y < 4; ++y) sum = add_pairs(w[y], sum);
-            const uint8_t* const vb = kb + kK;
+            const uint8_t* const vb = lb + stage * kStage + kK;
 #pragma unroll
             for (int y = 0; y < 4; ++y)
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
-                    o[n] = mfma32x32x16(*(const bf16x8*)(vb + (32 * n + i) * 128 + 16 * ((2 * y + h) ^ (i / 2 & 7))), w[y], o[n]);
+                    o[n] = mfma32x32x16(*(const bf16x8*)(vb + (32 * n + i) * kVRow + 16 * v_slot(i, 8 * part + 2 * y + h)), w[y], o[n]);
         }
         if (tile + 1 < te) store(tile + 1, stage ^ 1, blk, sc);
         __syncthreads();
@@ -540,7 +550,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_tile(Args a, Sequences s, 
 AttentionPlan plan_attention(int64_t M, int n_seq, int max_q, int Hq, int Hk, int D) {
     AttentionPlan p{};
     const int64_t rows = std::min<int64_t>(max_q, M) * (Hq / Hk);
-    p.rows = rows <= 32 ? 16 : kTileRows;
+    p.rows = rows <= 32 ? 16 : rows <= 512 ? 128 : 256;
     p.tiles = (int)((rows + p.rows - 1) / p.rows);
     const int64_t slots = (int64_t)n_seq * p.tiles * Hk, enough = p.rows == 16 ? 1024 : 512;
     p.split = 1;
@@ -557,11 +567,12 @@ hipError_t launch_attention(const uint16_t* q, int64_t M, int Hq, const Sequence
                  p.split, p.cstride, scale * kLog2e};
     const unsigned grid = (unsigned)((int64_t)s.n * p.tiles * p.split * c.Hk);
     const auto go = [&](auto kernel) {
-        kernel<<<grid, 256, 0, st>>>(a, s, c);
+        kernel<<<grid, p.rows == 256 ? 512 : 256, 0, st>>>(a, s, c);
         return hipGetLastError();
     };
     if (p.rows == 16) return c.D == 128 ? go(k_attention_rows<128>) : go(k_attention_rows<64>);
-    return c.D == 128 ? go(k_attention_tile<128>) : go(k_attention_tile<64>);
+    if (p.rows == 128) return c.D == 128 ? go(k_attention_tile<128, 4>) : go(k_attention_tile<64, 4>);
+    return c.D == 128 ? go(k_attention_tile<128, 8>) : go(k_attention_tile<64, 8>);
 }
 
 }  // namespace awq

@@ -46,7 +46,7 @@ hipError_t launch_qkv_append(const AppendArgs& a, const Sequences& s, const Cach
 
 struct AttentionPlan {
     int split;                   // most slices of a sequence's tokens
-    int rows;                    // rows per workgroup, which says which kernel: 16 or 128
+    int rows;                    // rows per workgroup, which says which kernel: 16, 128 or 256
     int tiles;                   // row tiles per sequence and head
     int cstride;                 // arrival counter i at word i * cstride of the counter region
     size_t ws_bytes;
