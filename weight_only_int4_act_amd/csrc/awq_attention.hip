@@ -290,6 +290,56 @@ __device__ __forceinline__ float add_pairs(const bf16x8& v, float c) {
     return c;
 }
 
+// What a tile of 32 NW rows is: its sequence, its rows, the tokens that they see and the slices that these make.
+template <int NW>
+struct TileRows {
+    int b, rt, rows, row0, start, length, G, cap, most, tiles, used;
+    __device__ __forceinline__ TileRows(const Args& a, const Sequences& s, const Cache& c, int b_, int rt_) : b(b_), rt(rt_) {
+        const NewTokens t = new_tokens(s, b, a.M);
+        rows = min(t.count, s.max_q) * a.G;
+        row0 = t.row0, start = t.start, length = t.length, G = a.G;
+        cap = s.width << c.logT;                 // what the table covers
+        most = reach(32 * NW * rt + 32 * NW - 1, a);
+        tiles = (most + 16 * NW - 1) / (16 * NW);
+        used = max(min(a.split, (tiles + 3) / 4), 1);            // four stages each or more
+    }
+    // tokens that a row sees (of one past the last: what the last sees), and where its numbers are
+    __device__ __forceinline__ int reach(int row, const Args& a) const {
+        return min(a.causal ? max(start + max(min(row, rows - 1), 0) / G + 1, 0) : length, cap);
+    }
+    __device__ __forceinline__ int64_t at(int row, int head, const Args& a, int D) const {
+        const int r = max(min(row, rows - 1), 0);
+        return ((int64_t)(row0 + r / G) * a.Hq + head * G + r % G) * D;
+    }
+};
+// A slice's part: maximum and sum of the rows, then the numbers as the lanes hold them.
+template <int D, int NW>
+struct Partial {
+    static constexpr int kRows = 32 * NW, kFloats = kRows * 2 + kRows * D;
+    float* base;
+    __device__ __forceinline__ Partial(const Args& a, int slot) : base(a.part + (int64_t)slot * a.split * kFloats) {}
+    __device__ __forceinline__ float* stats(int z, int row) const { return base + (int64_t)z * kFloats + row * 2; }
+    __device__ __forceinline__ floatx4* numbers(int z, int wave, int n, int y, int lane) const {
+        return (floatx4*)(base + (int64_t)z * kFloats + kRows * 2 + (((wave * (D / 32) + n) * 4 + y) * 64 + lane) * 4);
+    }
+};
+// 32 numbers of a row, of which lane (i, h) holds 8y + 4h .. + 3: as bf16, 16 bytes a lane.
+__device__ __forceinline__ void write_row32(uint16_t* to, const floatx16& o, float inv, int h, bool on) {
+#pragma unroll
+    for (int y = 0; y < 4; y += 2) {             // numbers 8y .. + 7 to the lanes of h = 0, the next eight to those of h = 1
+        u32x4 out;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const auto w = __builtin_amdgcn_permlane32_swap(pack_bf16x2(o[4 * y + 2 * e] * inv, o[4 * y + 2 * e + 1] * inv),
+                                                            pack_bf16x2(o[4 * y + 4 + 2 * e] * inv, o[4 * y + 5 + 2 * e] * inv),
+                                                            false, false);
+            out[e] = w[0];
+            out[2 + e] = w[1];
+        }
+        if (on) *(u32x4*)(to + 8 * y + 8 * h) = out;
+    }
+}
+
 // NW wavefronts; 16 NW tokens are staged at a time.
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences s, Cache c) {
@@ -297,27 +347,19 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
     constexpr int kTileRows = 32 * NW, NG = NW, kTokens = 16 * NG;   // groups of 16 tokens of a stage
     constexpr int kVRow = kTokens * 2, kK = kTokens * D * 2, kStage = 2 * kK;
     __shared__ u32x4 lds[2 * kStage / 16];
-    __shared__ uint32_t arrival;
     lds_poison_start(&lds[0], 2 * kStage / 16);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int i = lane & 31, h = lane >> 5;
     const int head = blockIdx.x % c.Hk, rest = blockIdx.x / c.Hk;
     const int z = rest % a.split, rt = a.tiles - 1 - rest / a.split % a.tiles, b = rest / a.split / a.tiles;
-    const NewTokens t = new_tokens(s, b, a.M);
-    const int rows = min(t.count, s.max_q) * a.G;
-    if (kTileRows * rt >= rows) return;          // the whole workgroup
-    const int row = kTileRows * rt + 32 * wave + i, mine = min(row, rows - 1), tok = mine / a.G;
-    const int64_t qat = ((int64_t)(t.row0 + tok) * a.Hq + head * a.G + mine % a.G) * D;
-    // tokens that this lane's row sees, that every row of the wavefront sees, and that any row of the workgroup does
-    const int cap = s.width << c.logT;
-    auto reach = [&](int r) { return min(a.causal ? max(t.start + min(r, rows - 1) / a.G + 1, 0) : t.length, cap); };
-    const int base_row = kTileRows * rt + 32 * wave;
-    const int seen = reach(row), all = reach(base_row), wave_most = base_row < rows ? reach(base_row + 31) : 0;
-    const int most = reach(kTileRows * rt + kTileRows - 1);
-    const int tiles = (most + kTokens - 1) / kTokens;
-    const int used = max(min(a.split, (tiles + 3) / 4), 1);      // slices of this sequence: four stages each or more
-    if (z >= used) return;
-    const int per = (tiles + used - 1) / used, tb = min(z * per, tiles), te = min(tb + per, tiles);
+    const TileRows<NW> g(a, s, c, b, rt);
+    const int rows = g.rows, most = g.most, used = g.used;
+    if (kTileRows * rt >= rows || z >= used) return;             // the whole workgroup
+    const int row = kTileRows * rt + 32 * wave + i, base_row = kTileRows * rt + 32 * wave;
+    const int64_t qat = g.at(row, head, a, D);
+    // tokens that this lane's row sees, that every row of the wavefront sees, and that any of its rows does
+    const int seen = g.reach(row, a), all = g.reach(base_row, a), wave_most = base_row < rows ? g.reach(base_row + 31, a) : 0;
+    const int per = (g.tiles + used - 1) / used, tb = min(z * per, g.tiles), te = min(tb + per, g.tiles);
 
     // scores are f times the products with f > 0: a negative scale's sign goes into q, a zero scale makes q zero
     const float f = a.scale == 0.f ? 1.f : fabsf(a.scale);
@@ -350,8 +392,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
     auto load = [&](int tile, int blk) __attribute__((always_inline)) {
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-            const int g = group_of(n), first = tile * kTokens + 16 * g;
-            const int64_t base = ((int64_t)max(__builtin_amdgcn_readlane(blk, g), 0) * c.Hk + head) * c.T + (first & (c.T - 1));
+            const int grp = group_of(n), first = tile * kTokens + 16 * grp;
+            const int64_t base = ((int64_t)max(__builtin_amdgcn_readlane(blk, grp), 0) * c.Hk + head) * c.T + (first & (c.T - 1));
             kn[n] = *(const u32x4*)(c.k + (base + (token & 15)) * D + 16 * piece);
             vn[n] = *(const u32x4*)(c.v + base * D + 16 * number);
         }
@@ -362,8 +404,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
     auto store = [&](int tile, int stage, int blk, uint32_t sc) __attribute__((always_inline)) {
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-            const int g = group_of(n), r = 16 * g + (token & 15);
-            const uint32_t e = __builtin_amdgcn_readlane(sc, g);
+            const int grp = group_of(n), r = 16 * grp + (token & 15);
+            const uint32_t e = __builtin_amdgcn_readlane(sc, grp);
             const bool marked = (e & 255) == 255 || e >> 8 == 255;   // K becomes NaN, V finite
             const float ks = __uint_as_float(marked ? 0x7f800000u : (e & 255) << 23);
             const float vs = __uint_as_float(marked ? 127u << 23 : (e >> 8) << 23);
@@ -371,7 +413,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
             *(bf16x8*)(kr + 16 * k_slot(r, 2 * piece)) = widen_codes(kn[n][0], kn[n][1], ks);
             *(bf16x8*)(kr + 16 * k_slot(r, 2 * piece + 1)) = widen_codes(kn[n][2], kn[n][3], ks);
             // what lies behind the sequence's last token, or in no block, may be anything, NaN among it: zeros
-            const int live = __builtin_amdgcn_readlane(blk, g) < 0 ? 0 : t.length - tile * kTokens - 16 * g;
+            const int live = __builtin_amdgcn_readlane(blk, grp) < 0 ? 0 : g.length - tile * kTokens - 16 * grp;
             u32x4 x = vn[n];
             if (live < 16) {
                 const uint64_t bytes = live >= 8 ? ~0ull : (1ull << 8 * max(live, 0)) - 1;
@@ -379,8 +421,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
                 x &= u32x4{(uint32_t)bytes, (uint32_t)(bytes >> 32), (uint32_t)more, (uint32_t)(more >> 32)};
             }
             uint8_t* const vr = lb + stage * kStage + kK + number * kVRow;
-            *(bf16x8*)(vr + 16 * v_slot(number, 2 * g)) = widen_codes(x[0], x[2], vs);
-            *(bf16x8*)(vr + 16 * v_slot(number, 2 * g + 1)) = widen_codes(x[1], x[3], vs);
+            *(bf16x8*)(vr + 16 * v_slot(number, 2 * grp)) = widen_codes(x[0], x[2], vs);
+            *(bf16x8*)(vr + 16 * v_slot(number, 2 * grp + 1)) = widen_codes(x[1], x[3], vs);
         }
     };
 
@@ -478,71 +520,58 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
     sum = __uint_as_float(halves[0]) + __uint_as_float(halves[1]);
 #pragma unroll
     for (int n = 0; n < NB; ++n) asm volatile("" : "+v"(o[n]));  // the products stay before the branches
-    auto write = [&](float total) __attribute__((always_inline)) {
-        const float inv = total == 0.f ? 0.f : 1.f / total;      // nothing seen: zeros
+    if (used > 1) {                              // several slices: k_attention_join adds them
+        const Partial<D, NW> to(a, (b * a.tiles + rt) * c.Hk + head);
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int y = 0; y < 4; y += 2) {     // numbers 8y .. + 7 to the lanes of h = 0, the next eight to those of h = 1
-                u32x4 out;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const auto w = __builtin_amdgcn_permlane32_swap(
-                        pack_bf16x2(o[n][4 * y + 2 * e] * inv, o[n][4 * y + 2 * e + 1] * inv),
-                        pack_bf16x2(o[n][4 * y + 4 + 2 * e] * inv, o[n][4 * y + 5 + 2 * e] * inv), false, false);
-                    out[e] = w[0];
-                    out[2 + e] = w[1];
-                }
-                if (row < rows) *(u32x4*)(a.out + qat + 32 * n + 8 * y + 8 * h) = out;
-            }
-    };
-    if (used == 1) {
-        write(sum);
+            for (int y = 0; y < 4; ++y)
+                *to.numbers(z, wave, n, y, lane) = floatx4{o[n][4 * y], o[n][4 * y + 1], o[n][4 * y + 2], o[n][4 * y + 3]};
+        to.stats(z, 32 * wave + i)[h] = h ? sum : m;
         return;
     }
-    // several slices: maximum and sum of the rows, then the numbers, per slice; the last workgroup to arrive joins them in
-    // slice order
-    constexpr uint32_t kPart = kTileRows * 8 + kTileRows * D * 4;
-    const int slot = (b * a.tiles + rt) * c.Hk + head;
-    const __amdgpu_buffer_rsrc_t pr = rsrc((const char*)a.part + (int64_t)slot * a.split * kPart, (int64_t)a.split * kPart);
-    auto at = [&](int z, int n, int y) { return z * kPart + kTileRows * 8 + (uint32_t)(((wave * NB + n) * 4 + y) * 64 + lane) * 16; };
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;              // nothing seen: zeros
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
+    for (int n = 0; n < NB; ++n) write_row32(a.out + qat + 32 * n, o[n], inv, h, row < rows);
+}
+
+// Adds the slices of the tiles above, in slice order: a workgroup takes 32 rows, a wavefront 32 numbers of each.
+// (By the last workgroup to arrive the join of 16 slices of 128 rows took longer than the slices.)
+template <int D, int NW>
+__global__ __launch_bounds__(2 * D) void k_attention_join(Args a, Sequences s, Cache c) {
+    const int n = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 31, h = lane >> 5;
+    const int wave = blockIdx.x % NW, head = blockIdx.x / NW % c.Hk, rest = blockIdx.x / NW / c.Hk;
+    const TileRows<NW> r(a, s, c, rest / a.tiles, rest % a.tiles);
+    const int row = 32 * NW * r.rt + 32 * wave + i;
+    if (32 * NW * r.rt + 32 * wave >= r.rows || r.used == 1) return;
+    const Partial<D, NW> from(a, (r.b * a.tiles + r.rt) * c.Hk + head);
+    float m = -INFINITY, sum = 0.f;
+    floatx16 o;
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
-            store4_agent(pr, at(z, n, y), floatx4{o[n][4 * y], o[n][4 * y + 1], o[n][4 * y + 2], o[n][4 * y + 3]});
-    const uint32_t st = (32 * wave + i) * 8;
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(h ? sum : m), pr, z * kPart + st + 4 * h, 0, kCpolAgent);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wavefront's part has landed
-    __syncthreads();
-    uint32_t* const counter = a.cnt + (int64_t)slot * a.cstride;
-    if (threadIdx.x == 0) arrival = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (arrival != (uint32_t)(used - 1)) return;
-    float ms = -INFINITY, ts = 0.f;
+    for (int e = 0; e < 16; ++e) o[e] = 0.f;
+    for (int z0 = 0; z0 < r.used; z0 += 4) {     // four slices' loads in flight
+        float2 st[4];
+        floatx4 v[4][4];
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
+        for (int u = 0; u < 4; ++u) {
+            const int z = min(z0 + u, r.used - 1);
+            st[u] = *(const float2*)from.stats(z, 32 * wave + i);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) o[n][r] = 0.f;
-    for (int y = 0; y < used; ++y) {
-        const float mz = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(pr, y * kPart + st, 0, kCpolAgent));
-        const float tz = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(pr, y * kPart + st + 4, 0, kCpolAgent));
-        floatx4 v[NB][4];
+            for (int y = 0; y < 4; ++y) v[u][y] = *from.numbers(z, wave, n, y, lane);
+        }
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+        for (int u = 0; u < 4; ++u) {
+            if (z0 + u >= r.used) break;
+            const float now = fmaxf(m, st[u].x), base = now == -INFINITY ? 0.f : now;
+            const float keep = __builtin_amdgcn_exp2f(m - base), g = __builtin_amdgcn_exp2f(st[u].x - base);
+            m = now;
+            sum = sum * keep + st[u].y * g;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[n][e] = load4_agent(pr, at(y, n, e));
-        const float now = fmaxf(ms, mz), base = now == -INFINITY ? 0.f : now;
-        const float keep = __builtin_amdgcn_exp2f(ms - base), g = __builtin_amdgcn_exp2f(mz - base);
-        ms = now;
-        ts = ts * keep + tz * g;
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) o[n][r] = o[n][r] * keep + v[n][r / 4][r % 4] * g;
+            for (int e = 0; e < 16; ++e) o[e] = o[e] * keep + v[u][e / 4][e % 4] * g;
+        }
     }
-    write(ts);
-    if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    write_row32(a.out + r.at(row, head, a, D) + 32 * n, o, inv, h, row < r.rows);
 }
 
 }  // namespace
@@ -550,7 +579,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
 AttentionPlan plan_attention(int64_t M, int n_seq, int max_q, int Hq, int Hk, int D) {
     AttentionPlan p{};
     const int64_t rows = std::min<int64_t>(max_q, M) * (Hq / Hk);
-    p.rows = rows <= 32 ? 16 : rows <= 512 ? 128 : 256;
+    p.rows = rows <= 32 ? 16 : rows <= 1024 ? 128 : 256;
     p.tiles = (int)((rows + p.rows - 1) / p.rows);
     const int64_t slots = (int64_t)n_seq * p.tiles * Hk, enough = p.rows == 16 ? 1024 : 512;
     p.split = 1;
@@ -570,9 +599,18 @@ hipError_t launch_attention(const uint16_t* q, int64_t M, int Hq, const Sequence
         kernel<<<grid, p.rows == 256 ? 512 : 256, 0, st>>>(a, s, c);
         return hipGetLastError();
     };
+    const auto tiles = [&](auto kernel, auto join) {
+        const hipError_t e = go(kernel);
+        if (e != hipSuccess || p.split == 1) return e;
+        join<<<(unsigned)((int64_t)s.n * p.tiles * c.Hk * (p.rows / 32)), 2 * c.D, 0, st>>>(a, s, c);
+        return hipGetLastError();
+    };
     if (p.rows == 16) return c.D == 128 ? go(k_attention_rows<128>) : go(k_attention_rows<64>);
-    if (p.rows == 128) return c.D == 128 ? go(k_attention_tile<128, 4>) : go(k_attention_tile<64, 4>);
-    return c.D == 128 ? go(k_attention_tile<128, 8>) : go(k_attention_tile<64, 8>);
+    if (p.rows == 128)
+        return c.D == 128 ? tiles(k_attention_tile<128, 4>, k_attention_join<128, 4>)
+                          : tiles(k_attention_tile<64, 4>, k_attention_join<64, 4>);
+    return c.D == 128 ? tiles(k_attention_tile<128, 8>, k_attention_join<128, 8>)
+                      : tiles(k_attention_tile<64, 8>, k_attention_join<64, 8>);
 }
 
 }  // namespace awq
