@@ -94,18 +94,33 @@ struct Head {
     }
 };
 
+// Codes of four tokens, eight numbers each in the two words of lanes l, l + 16, l + 32, l + 48 (token lane / 16): after it
+// lane l + 16 g holds numbers 2g and 2g + 1 of its eight, a word of the four tokens each.
+__device__ __forceinline__ uint2 four_tokens(const uint2& w) {
+    const auto a = __builtin_amdgcn_permlane32_swap(w.x, w.y, false, false);     // tokens 0, 1 and 2, 3 of one word
+    const uint32_t even = __builtin_amdgcn_perm(a[1], a[0], 0x05040100u), odd = __builtin_amdgcn_perm(a[1], a[0], 0x07060302u);
+    const auto b = __builtin_amdgcn_permlane16_swap(even, odd, false, false);    // two numbers of tokens 0, 2 and of 1, 3
+    return uint2{__builtin_amdgcn_perm(b[1], b[0], 0x06020400u), __builtin_amdgcn_perm(b[1], b[0], 0x07030501u)};
+}
+
 // A workgroup takes the new tokens of one block of the cache for one head of K and V and the heads of q that read it.
-// The numbers of K (float32, normed and rotated) and V (bf16) stay in registers until the block's largest are
-// known; then come the codes.
+// Bound by HBM for many tokens (per number of q 4 bytes, of K and V 3), by the chain of dependent reads for few
+// (lengths, blocks, rows).  K's and V's rows are requested first; while they come q's heads are done; the numbers of K
+// (float32, normed and rotated) and V (bf16) then stay in registers until the block's largest are known.  V's codes go
+// through LDS into their order: sixteen tokens of a number in one store where all of them are new, else bytes.
 template <int D, int T>
 __global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, Cache c, int per_seq) {
     using H = Head<D>;
     constexpr int L = H::L, W = 256 / L, U = (T + W - 1) / W;   // lanes of a head, heads at a time, rounds of a block
     __shared__ uint32_t tops[4][2];
+    __shared__ u32x4 vt[T / 16 * D];
     lds_poison_start(&tops[0][0], 8);
+    lds_poison_start(&vt[0], T / 16 * D);
     const int h = blockIdx.x % c.Hk, j = blockIdx.x / c.Hk % per_seq, b = blockIdx.x / c.Hk / per_seq;
     const NewTokens t = new_tokens(s, b, (int)a.M);
-    const int l = threadIdx.x % L, w = threadIdx.x / L;
+    const int lane = threadIdx.x & 63, l = threadIdx.x % L;
+    // which head of the W: those of lanes 16 apart are neighbours, for four_tokens
+    const int w = (threadIdx.x >> 6) * (64 / L) + (lane >> 4) + (L == 8 ? 4 * (lane >> 3 & 1) : 0);
     const int G = a.Hq / c.Hk;
     const int64_t row_size = (int64_t)(a.Hq + 2 * c.Hk) * D;
 
@@ -115,7 +130,7 @@ __global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, C
         for (int i = w; i < none * G; i += W)
             *(u32x4*)(a.q + (((int64_t)t.row0 + i / G) * a.Hq + h * G + i % G) * D + l * 8) = u32x4{0, 0, 0, 0};
     }
-    const int64_t first_block = max(t.start, 0) / T, index = first_block + j;   // of the sequence
+    const int64_t index = max(t.start, 0) / T + j;               // the block's, of the sequence
     const int64_t p0 = max((int64_t)t.start, index * T);
     const int64_t p1 = min(min((int64_t)t.length, (index + 1) * T), (int64_t)t.start + s.max_q);
     if (t.count <= 0 || p0 >= p1) return;        // the whole workgroup
@@ -124,73 +139,24 @@ __global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, C
     const int turned = a.rope ? (int)min(max((int64_t)a.P - p0, (int64_t)0), (int64_t)n) : n;   // tokens that the rotation covers
     const int64_t block = index < s.width ? s.table[(int64_t)b * s.width + index] : -1;
     const bool stored = block >= 0 && block < c.blocks && turned > 0;
+    const int64_t at = block * c.Hk + h;
+    const int slot1 = slot0 + turned;            // slots slot0 .. slot1 - 1 get tokens; head w of round u has slot u W + w
 
+    uint32_t before = 0;
+    u32x4 kr[U], v[U];
     if (stored) {
-        const int64_t at = block * c.Hk + h;
-        const uint32_t before = *(const uint16_t*)(c.scales + at * 2);
-        float k[U][8];
-        u32x4 v[U];
-        uint32_t kt = 0, vt = 0;
+        before = *(const uint16_t*)(c.scales + at * 2);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = u * W + w;
-            const bool in = i < turned;
-            const uint16_t* row = a.qkv + (int64_t)(row0 + min(i, n - 1)) * row_size + (int64_t)(a.Hq + h) * D + l * 8;
-            widen8(*(const u32x4*)row, k[u]);
+            const int i = min(max(u * W + w - slot0, 0), n - 1);
+            const uint16_t* const row = a.qkv + (int64_t)(row0 + i) * row_size + (int64_t)(a.Hq + h) * D + l * 8;
+            if (u * W + W <= slot0 || u * W >= slot1) continue;  // the whole workgroup
+            kr[u] = *(const u32x4*)row;
             v[u] = *(const u32x4*)(row + (int64_t)c.Hk * D);
-            if (a.k_weight) H::norm(k[u], a.k_weight, l, a.eps);
-            if (a.rope) H::rotate(k[u], a.rope + min(p0 + i, (int64_t)a.P - 1) * a.R, a.R, a.interleaved, l);
-            if (!in) continue;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) kt = max(kt, __float_as_uint(k[u][e]) & 0x7fffffffu);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) vt = max(vt, max(v[u][e] << 16 & 0x7fffffffu, v[u][e] & 0x7fff0000u));
         }
-#pragma unroll
-        for (int off = 1; off < 64; off *= 2) {
-            kt = max(kt, (uint32_t)__shfl_xor((int)kt, off, kWave));
-            vt = max(vt, (uint32_t)__shfl_xor((int)vt, off, kWave));
-        }
-        if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6][0] = kt, tops[threadIdx.x >> 6][1] = vt;
-        __syncthreads();                         // `stored` is the workgroup's
-        kt = max(max(tops[0][0], tops[1][0]), max(tops[2][0], tops[3][0]));
-        vt = max(max(tops[0][1], tops[1][1]), max(tops[2][1], tops[3][1]));
-        // a block that holds older tokens keeps the larger scale
-        const uint32_t ke0 = slot0 ? before & 255 : 0, ve0 = slot0 ? before >> 8 : 0;
-        const uint32_t ke = max(cache_scale_byte(kt), ke0), ve = max(cache_scale_byte(vt), ve0);
-        uint8_t* const kc = c.k + at * T * D;
-        uint8_t* const vc = c.v + at * T * D;
-        if (slot0 && ((ke > ke0 && ke != 255) || (ve > ve0 && ve != 255))) {   // the whole workgroup
-            if (ke > ke0 && ke != 255)
-                for (int i = threadIdx.x; i < slot0 * D / 4; i += 256) {
-                    uint32_t* p = (uint32_t*)kc + i;
-                    *p = cache_rescale4(*p, ke - ke0);
-                }
-            if (ve > ve0 && ve != 255)
-                for (int i = threadIdx.x; i < (slot0 + 15) / 16 * D * 4; i += 256) {   // four tokens of a group
-                    const int first = i / (4 * D) * 16 + i % 4 * 4, older = min(max(slot0 - first, 0), 4);
-                    const uint32_t mask = older == 4 ? ~0u : (1u << 8 * older) - 1;
-                    uint32_t* p = (uint32_t*)vc + i;
-                    if (older) *p = (cache_rescale4(*p, ve - ve0) & mask) | (*p & ~mask);
-                }
-            __syncthreads();                     // before new tokens' bytes of the same words
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = u * W + w, slot = slot0 + i;
-            if (i >= turned) continue;
-            *(uint2*)(kc + (int64_t)slot * D + l * 8) = cache_codes8(k[u], ke);
-            float x[8];
-            widen8(v[u], x);
-            const uint2 codes = cache_codes8(x, ve);
-            uint8_t* const to = vc + ((slot >> 4) * D + l * 8) * 16 + (slot & 15);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) to[e * 16] = (uint8_t)((e < 4 ? codes.x : codes.y) >> 8 * (e % 4));
-        }
-        if (threadIdx.x == 0) *(uint16_t*)(c.scales + at * 2) = (uint16_t)(ke | ve << 8);
     }
-    // q: the tokens' G heads
-    for (int i = w; i < (n * G + W - 1) / W * W; i += W) {   // every lane of a wavefront, for the exchanges
+    // q: the tokens' G heads; from the second wavefront on, so that one token's K and V are another's work
+    for (int i = (w + W - 64 / L) % W; i < (n * G + W - 1) / W * W; i += W) {   // every lane of a wavefront, for the exchanges
         const bool in = i < n * G;
         const int tok = in ? i / G : n - 1, head = h * G + (in ? i % G : 0);
         float x[8];
@@ -207,6 +173,73 @@ __global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, C
             *(u32x4*)(a.q + ((int64_t)(row0 + tok) * a.Hq + head) * D + l * 8) =
                 u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
     }
+    if (!stored) return;                         // the whole workgroup
+
+    float k[U][8];
+    uint32_t kt = 0, vmax = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (u * W + W <= slot0 || u * W >= slot1) continue;      // the whole workgroup
+        const int slot = u * W + w, i = min(max(slot - slot0, 0), n - 1);
+        widen8(kr[u], k[u]);
+        if (a.k_weight) H::norm(k[u], a.k_weight, l, a.eps);
+        if (a.rope) H::rotate(k[u], a.rope + min(p0 + i, (int64_t)a.P - 1) * a.R, a.R, a.interleaved, l);
+        if (slot < slot0 || slot >= slot1) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) kt = max(kt, __float_as_uint(k[u][e]) & 0x7fffffffu);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vmax = max(vmax, max(v[u][e] << 16 & 0x7fffffffu, v[u][e] & 0x7fff0000u));
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off *= 2) {
+        kt = max(kt, (uint32_t)__shfl_xor((int)kt, off, kWave));
+        vmax = max(vmax, (uint32_t)__shfl_xor((int)vmax, off, kWave));
+    }
+    if (lane == 0) tops[threadIdx.x >> 6][0] = kt, tops[threadIdx.x >> 6][1] = vmax;
+    __syncthreads();
+    kt = max(max(tops[0][0], tops[1][0]), max(tops[2][0], tops[3][0]));
+    vmax = max(max(tops[0][1], tops[1][1]), max(tops[2][1], tops[3][1]));
+    // a block that holds older tokens keeps the larger scale
+    const uint32_t ke0 = slot0 ? before & 255 : 0, ve0 = slot0 ? before >> 8 : 0;
+    const uint32_t ke = max(cache_scale_byte(kt), ke0), ve = max(cache_scale_byte(vmax), ve0);
+    uint8_t* const kc = c.k + at * T * D;
+    uint8_t* const vc = c.v + at * T * D;
+    if (slot0 && ke > ke0 && ke != 255)          // older codes to the new scale
+        for (int i = threadIdx.x; i < slot0 * D / 4; i += 256) {
+            uint32_t* p = (uint32_t*)kc + i;
+            *p = cache_rescale4(*p, ke - ke0);
+        }
+    if (slot0 && ve > ve0 && ve != 255)
+        for (int i = threadIdx.x; i < (slot0 + 15) / 16 * D * 4; i += 256) {   // four tokens of a group
+            const int first = i / (4 * D) * 16 + i % 4 * 4, older = min(max(slot0 - first, 0), 4);
+            const uint32_t mask = older == 4 ? ~0u : (1u << 8 * older) - 1;
+            uint32_t* p = (uint32_t*)vc + i;
+            if (older) *p = (cache_rescale4(*p, ve - ve0) & mask) | (*p & ~mask);
+        }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (u * W + W <= slot0 || u * W >= slot1) continue;      // the whole workgroup
+        const int slot = u * W + w;
+        if (slot >= slot0 && slot < slot1) *(uint2*)(kc + (int64_t)slot * D + l * 8) = cache_codes8(k[u], ke);
+        float x[8];
+        widen8(v[u], x);
+        const uint2 four = four_tokens(cache_codes8(x, ve));
+        if (U * W > T && slot >= T) continue;
+        uint32_t* const to = (uint32_t*)vt + ((slot >> 4) * D + l * 8 + 2 * (lane >> 4)) * 4 + (slot >> 2 & 3);
+        to[0] = four.x;
+        to[4] = four.y;
+    }
+    __syncthreads();                             // also: the older tokens' bytes before the new ones of the same words
+    for (int i = threadIdx.x; i < T / 16 * D; i += 256) {
+        const int lo = max(slot0 - (i / D) * 16, 0), hi = min(slot1 - (i / D) * 16, 16);   // new tokens of the sixteen
+        if (lo >= hi) continue;
+        if (hi - lo == 16) {
+            *(u32x4*)(vc + (int64_t)i * 16) = vt[i];
+        } else {
+            for (int e = lo; e < hi; ++e) vc[(int64_t)i * 16 + e] = ((const uint8_t*)vt)[i * 16 + e];
+        }
+    }
+    if (threadIdx.x == 0) *(uint16_t*)(c.scales + at * 2) = (uint16_t)(ke | ve << 8);
 }
 
 }  // namespace

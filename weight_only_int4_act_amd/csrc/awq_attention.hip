@@ -5,7 +5,6 @@
 // row r is token r / G, head r % G.  A key or value that one workgroup has loaded serves all of them.
 #include <algorithm>
 
-#include "awq_buffer.h"
 #include "awq_cache.h"
 
 namespace awq {
@@ -14,7 +13,7 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kTile = 64;                        // tokens that a wavefront takes at a time
-constexpr size_t kCounterBytes = 65536;
+constexpr size_t kCounterBytes = 65536;          // left alone: the products' arrival counters, in a workspace that they share
 
 // Eight e4m3 codes (two words) times 2^(E - 127), the scale's exponent field, in bf16: exact.
 __device__ __forceinline__ bf16x8 widen_codes(uint32_t a, uint32_t b, float scale) {
@@ -42,11 +41,33 @@ struct Args {
     const uint16_t* q;
     uint16_t* out;
     float* part;
-    uint32_t* cnt;
-    int M, Hq, G, causal, tiles, split, cstride;
+    int M, Hq, G, causal, tiles, split;
     float scale;                 // times log2 e
 };
 
+// What a tile of R rows is: its sequence, its rows, the tokens that they see, and the slices of four or more tiles of
+// TOKENS tokens that these make.
+template <int R, int TOKENS>
+struct TileRows {
+    int b, rt, rows, row0, start, length, G, cap, most, tiles, used;
+    __device__ __forceinline__ TileRows(const Args& a, const Sequences& s, const Cache& c, int b_, int rt_) : b(b_), rt(rt_) {
+        const NewTokens t = new_tokens(s, b, a.M);
+        rows = min(t.count, s.max_q) * a.G;
+        row0 = t.row0, start = t.start, length = t.length, G = a.G;
+        cap = s.width << c.logT;                 // what the table covers
+        most = reach(R * rt + R - 1, a);
+        tiles = (most + TOKENS - 1) / TOKENS;
+        used = max(min(a.split, (tiles + 3) / 4), 1);
+    }
+    // tokens that a row sees (of one past the last: what the last sees), and where its numbers are
+    __device__ __forceinline__ int reach(int row, const Args& a) const {
+        return min(a.causal ? max(start + max(min(row, rows - 1), 0) / G + 1, 0) : length, cap);
+    }
+    __device__ __forceinline__ int64_t at(int row, int head, const Args& a, int D) const {
+        const int r = max(min(row, rows - 1), 0);
+        return ((int64_t)(row0 + r / G) * a.Hq + head * G + r % G) * D;
+    }
+};
 // ---------------------------------------------------------------- few rows: the cache streamed once
 // Bound by the cache's bytes.  A workgroup takes 16 rows and a slice of the tokens; its four wavefronts take every
 // fourth tile of 64 tokens of it.  A lane (i, g) = (lane % 16, lane / 16) works for tokens 16g .. 16g + 15 of the tile in
@@ -56,33 +77,23 @@ struct Args {
 //   second product  O^T = V^T P^T: lane (i, g) gives the 16 bytes of number i of V's 16 tokens, and its own
 //                   results, in the order in which they are.
 // K and V become bf16 in registers (exact).  The running maximum and sum are per row; every wavefront has its own,
-// joined in LDS at the end, and those of several slices by the last workgroup to arrive, in slice order.
+// joined in LDS at the end, and those of several slices by k_attention_join_rows.
 template <int D>
 __global__ __launch_bounds__(256) void k_attention_rows(Args a, Sequences s, Cache c) {
     constexpr int ND = D / 16, NH = D / 64;
     __shared__ floatx4 red[4][ND][64];
     __shared__ float stat[4][2][16];
-    __shared__ uint32_t arrival;
     lds_poison_start(&red[0][0][0], 4 * ND * 64);
     lds_poison_start(&stat[0][0][0], 128);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int i = lane & 15, g = lane >> 4;
     const int h = blockIdx.x % c.Hk, rest = blockIdx.x / c.Hk;
     const int z = rest % a.split, rt = rest / a.split % a.tiles, b = rest / a.split / a.tiles;
-    const NewTokens t = new_tokens(s, b, a.M);
-    const int rows = min(t.count, s.max_q) * a.G;
-    if (16 * rt >= rows) return;                 // the whole workgroup
-    const int row = 16 * rt + i, tok = min(row, rows - 1) / a.G, head = h * a.G + min(row, rows - 1) % a.G;
-    const int64_t qat = ((int64_t)(t.row0 + tok) * a.Hq + head) * D;
-    // tokens that this lane's row sees, and that any row of the workgroup sees
-    const int last_tok = min(16 * rt + 15, rows - 1) / a.G;
-    const int cap = s.width << c.logT;           // what the table covers
-    const int seen = min(a.causal ? max(t.start + tok + 1, 0) : t.length, cap);
-    const int most = min(a.causal ? max(t.start + last_tok + 1, 0) : t.length, cap);
-    const int tiles = (most + kTile - 1) / kTile;
-    const int used = max(min(a.split, (tiles + 3) / 4), 1);      // slices of this sequence: four tiles each or more
-    if (z >= used) return;
-    const int per = (tiles + used - 1) / used, tb = min(z * per, tiles), te = min(tb + per, tiles);
+    const TileRows<16, kTile> t(a, s, c, b, rt);
+    if (16 * rt >= t.rows || z >= t.used) return;                // the whole workgroup
+    const int row = 16 * rt + i, seen = t.reach(row, a), most = t.most, used = t.used;
+    const int64_t qat = t.at(row, h, a, D);
+    const int per = (t.tiles + used - 1) / used, tb = min(z * per, t.tiles), te = min(tb + per, t.tiles);
 
     bf16x8 q[NH][2];
 #pragma unroll
@@ -97,25 +108,43 @@ __global__ __launch_bounds__(256) void k_attention_rows(Args a, Sequences s, Cac
 
     const int32_t* const table = s.table + (int64_t)b * s.width;
     // the block of tokens first .. first + 15 (a multiple of 16), or -1
-    auto block_of = [&](int first) {
+    auto block_of = [&](int first) __attribute__((always_inline)) {
         const int j = first >> c.logT;
         const int v = first < most && j < s.width ? table[j] : -1;
         return v >= 0 && v < c.blocks ? v : -1;
     };
-    for (int tile = tb + wave; tile < te; tile += 4) {
-        const int first = tile * kTile;
-        const int kg = i >> 2;                   // the 16 tokens whose K this lane gives
-        const int bk = block_of(first + 16 * kg), bv = block_of(first + 16 * g);
-        u32x4 k[4][NH], v[ND];
-        const uint8_t* const kp = c.k + (((int64_t)max(bk, 0) * c.Hk + h) * c.T + ((first + 16 * kg) & (c.T - 1)) + (i & 3)) * D + 16 * g;
+    u32x4 k[4][NH], v[ND];
+    uint32_t e;
+    const int kg = i >> 2;                       // the 16 tokens whose K this lane gives; V's are 16 g ..
+    auto load_k = [&](int first, int bk) __attribute__((always_inline)) {
+        const uint8_t* const p = c.k + (((int64_t)max(bk, 0) * c.Hk + h) * c.T + ((first + 16 * kg) & (c.T - 1)) + (i & 3)) * D + 16 * g;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int n = 0; n < NH; ++n) k[u][n] = *(const u32x4*)(kp + 4 * u * D + 64 * n);
-        const uint8_t* const vp = c.v + (((int64_t)max(bv, 0) * c.Hk + h) * c.T + ((first + 16 * g) & (c.T - 1))) * D + 16 * i;
+            for (int n = 0; n < NH; ++n) k[u][n] = *(const u32x4*)(p + 4 * u * D + 64 * n);
+    };
+    auto load_v = [&](int first, int bv) __attribute__((always_inline)) {
+        const uint8_t* const p = c.v + (((int64_t)max(bv, 0) * c.Hk + h) * c.T + ((first + 16 * g) & (c.T - 1))) * D + 16 * i;
 #pragma unroll
-        for (int n = 0; n < ND; ++n) v[n] = *(const u32x4*)(vp + 256 * n);
-        const uint32_t e = *(const uint16_t*)(c.scales + ((int64_t)max(bv, 0) * c.Hk + h) * 2);
+        for (int n = 0; n < ND; ++n) v[n] = *(const u32x4*)(p + 256 * n);
+    };
+    auto load_scales = [&](int bv) __attribute__((always_inline)) {
+        return (uint32_t)*(const uint16_t*)(c.scales + ((int64_t)max(bv, 0) * c.Hk + h) * 2);
+    };
+    // Blocks are looked up two tiles ahead; a tile's K is requested where the one before has left its registers, its V
+    // likewise, so that one tile is on its way all the time.
+    int first = (tb + wave) * kTile;
+    const int end = te * kTile;
+    int bk = block_of(first + 16 * kg), bv = block_of(first + 16 * g);
+    int bk1 = block_of(first + 4 * kTile + 16 * kg), bv1 = block_of(first + 4 * kTile + 16 * g);
+    if (first < end) {
+        e = load_scales(bv);
+        load_k(first, bk);
+        load_v(first, bv);
+    }
+    for (; first < end; first += 4 * kTile) {
+        const bool more = first + 4 * kTile < end;
+        const int bk2 = block_of(first + 8 * kTile + 16 * kg), bv2 = block_of(first + 8 * kTile + 16 * g);
         const bool poisoned = (e & 255) == 255 || e >> 8 == 255;
         // a marked block makes what is seen of it NaN; V's own scale then is any finite one
         const float f = poisoned ? NAN : __uint_as_float((e & 255) == 0 ? 0x00400000u : (e & 255) << 23) * a.scale;
@@ -130,6 +159,11 @@ __global__ __launch_bounds__(256) void k_attention_rows(Args a, Sequences s, Cac
                 p[u] = mfma16x16x32(widen_codes(k[u][n][0], k[u][n][1], 1.f), q[n][0], p[u]);
                 p[u] = mfma16x16x32(widen_codes(k[u][n][2], k[u][n][3], 1.f), q[n][1], p[u]);
             }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) {
+            e = load_scales(bv1);
+            load_k(first + 4 * kTile, bk1);
         }
         // token 16g + 4u + r of the tile is seen when it lies below `limit`
         const int limit = bv < 0 ? 0 : seen - first - 16 * g;
@@ -161,21 +195,22 @@ __global__ __launch_bounds__(256) void k_attention_rows(Args a, Sequences s, Cac
                                                     pack_bf16x2(p[2 * y + 1][2], p[2 * y + 1][3])});
         // what lies behind the sequence's last token may be anything, NaN among it: zeros
         const int live = bv < 0 ? 0 : t.length - first - 16 * g;
+        const uint64_t lo = live >= 8 ? ~0ull : (1ull << 8 * max(live, 0)) - 1;
+        const uint64_t hi = live >= 16 ? ~0ull : live <= 8 ? 0ull : (1ull << 8 * (live - 8)) - 1;
+        const u32x4 mask = {(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 #pragma unroll
         for (int n = 0; n < ND; ++n) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[n][r] *= keep;
-            u32x4 x = v[n];
-            if (live < 16) {
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int left = min(max(live - 4 * y, 0), 4);
-                    x[y] = left == 4 ? x[y] : x[y] & ((1u << 8 * left) - 1);
-                }
-            }
+            const u32x4 x = v[n] & mask;
             o[n] = mfma16x16x32(widen_codes(x[0], x[1], fv), w[0], o[n]);
             o[n] = mfma16x16x32(widen_codes(x[2], x[3], fv), w[1], o[n]);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) load_v(first + 4 * kTile, bv1);
+        bv = bv1;
+        bk1 = bk2;
+        bv1 = bv2;
     }
     // the wavefronts' parts: lane (i, g) holds numbers 16n + 4g .. + 3 of row i
     sum = sum_g(sum);
@@ -202,63 +237,58 @@ __global__ __launch_bounds__(256) void k_attention_rows(Args a, Sequences s, Cac
 #pragma unroll
         for (int n = 0; n < NP; ++n) x[n] += f * red[w][wave * NP + n][lane];
     }
-    auto write = [&]() __attribute__((always_inline)) {
-        const float inv = total == 0.f ? 0.f : 1.f / total;      // nothing seen: zeros
-        if (row >= rows) return;
+    if (row >= t.rows) return;
+    if (used > 1) {                              // several slices: k_attention_join_rows adds them
+        float* const to = a.part + ((int64_t)((b * a.tiles + rt) * c.Hk + h) * a.split + z) * (16 * (2 + D));
+        if (wave == 0 && g == 0) *(float2*)(to + 2 * i) = float2{top, total};
 #pragma unroll
-        for (int n = 0; n < NP; ++n)
-            *(uint2*)(a.out + qat + (wave * NP + n) * 16 + 4 * g) =
-                uint2{pack_bf16x2(x[n][0] * inv, x[n][1] * inv), pack_bf16x2(x[n][2] * inv, x[n][3] * inv)};
-    };
-    if (used == 1) {
-        write();
+        for (int n = 0; n < NP; ++n) *(floatx4*)(to + 32 + i * D + (wave * NP + n) * 16 + 4 * g) = x[n];
         return;
     }
-    // several slices: maximum and sum of the 16 rows, then the numbers, per slice
-    constexpr uint32_t kPart = 16 * 2 * 4 + 16 * D * 4;
-    const int slot = (b * a.tiles + rt) * c.Hk + h;
-    const __amdgpu_buffer_rsrc_t pr = rsrc((const char*)a.part + (int64_t)slot * a.split * kPart, (int64_t)a.split * kPart);
-    auto pat = [&](int z, int n) { return z * kPart + 128 + (uint32_t)((wave * NP + n) * 64 + lane) * 16; };
+    const float inv = total == 0.f ? 0.f : 1.f / total;          // nothing seen: zeros
 #pragma unroll
-    for (int n = 0; n < NP; ++n) store4_agent(pr, pat(z, n), x[n]);
-    if (wave == 0 && g == 0) {
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(top), pr, z * kPart + i * 4, 0, kCpolAgent);
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(total), pr, z * kPart + 64 + i * 4, 0, kCpolAgent);
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wavefront's part has landed
-    __syncthreads();
-    uint32_t* const counter = a.cnt + (int64_t)slot * a.cstride;
-    if (threadIdx.x == 0) arrival = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (arrival != (uint32_t)(used - 1)) return;
-    float ms = -INFINITY, ts = 0.f;
+    for (int n = 0; n < NP; ++n)
+        *(uint2*)(a.out + qat + (wave * NP + n) * 16 + 4 * g) =
+            uint2{pack_bf16x2(x[n][0] * inv, x[n][1] * inv), pack_bf16x2(x[n][2] * inv, x[n][3] * inv)};
+}
+
+// Adds the slices, in slice order: a wavefront takes 256 / D rows, eight slices' loads in flight.  A launch of its
+// own: the last workgroup of a row tile to arrive read 8 KB slices that other dies had written at .4 us each (one sequence of 4097
+// tokens 13.5 us, of 8192 20).
+template <int D>
+__global__ __launch_bounds__(64) void k_attention_join_rows(Args a, Sequences s, Cache c) {
+    constexpr int L = D / 4, R = 64 / L, kFlight = 8;            // lanes of a row, rows
+    const int part = blockIdx.x % (16 / R), h = blockIdx.x / (16 / R) % c.Hk, rest = blockIdx.x / (16 / R) / c.Hk;
+    const TileRows<16, kTile> t(a, s, c, rest / a.tiles, rest % a.tiles);
+    const int i = part * R + threadIdx.x / L, d = threadIdx.x % L * 4, row = 16 * t.rt + i;
+    if (row >= t.rows || t.used == 1) return;
+    const float* const from = a.part + (int64_t)((t.b * a.tiles + t.rt) * c.Hk + h) * a.split * (16 * (2 + D));
+    float m = -INFINITY, sum = 0.f;
+    floatx4 x = {0.f, 0.f, 0.f, 0.f};
+    for (int z0 = 0; z0 < t.used; z0 += kFlight) {
+        float2 st[kFlight];
+        floatx4 v[kFlight];
 #pragma unroll
-    for (int n = 0; n < NP; ++n) x[n] = floatx4{0.f, 0.f, 0.f, 0.f};
-    for (int z0 = 0; z0 < used; z0 += 4) {       // four slices' loads in flight
-        float mz[4], tz[4];
-        floatx4 v[4][NP];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int zz = min(z0 + u, used - 1);
-            mz[u] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(pr, zz * kPart + i * 4, 0, kCpolAgent));
-            tz[u] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(pr, zz * kPart + 64 + i * 4, 0, kCpolAgent));
-#pragma unroll
-            for (int n = 0; n < NP; ++n) v[u][n] = load4_agent(pr, pat(zz, n));
+        for (int u = 0; u < kFlight; ++u) {
+            const float* const p = from + (int64_t)min(z0 + u, t.used - 1) * (16 * (2 + D));
+            st[u] = *(const float2*)(p + 2 * i);
+            v[u] = *(const floatx4*)(p + 32 + i * D + d);
         }
+        // every load is on its way before the first is waited for (a branch around their use would take them along)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (z0 + u >= used) break;
-            const float next = fmaxf(ms, mz[u]), base = next == -INFINITY ? 0.f : next;
-            const float keep = __builtin_amdgcn_exp2f(ms - base), f = __builtin_amdgcn_exp2f(mz[u] - base);
-            ms = next;
-            ts = ts * keep + tz[u] * f;
+        for (int u = 0; u < kFlight; ++u) asm volatile("" : "+v"(st[u].x), "+v"(st[u].y), "+v"(v[u]));
 #pragma unroll
-            for (int n = 0; n < NP; ++n) x[n] = x[n] * keep + v[u][n] * f;
+        for (int u = 0; u < kFlight; ++u) {
+            if (z0 + u >= t.used) break;
+            const float now = fmaxf(m, st[u].x), base = now == -INFINITY ? 0.f : now;
+            const float keep = __builtin_amdgcn_exp2f(m - base), f = __builtin_amdgcn_exp2f(st[u].x - base);
+            m = now;
+            sum = sum * keep + st[u].y * f;
+            x = x * keep + v[u] * f;
         }
     }
-    total = ts;
-    write();
-    if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *(uint2*)(a.out + t.at(row, h, a, D) + d) = uint2{pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv)};
 }
 
 // ---------------------------------------------------------------- many rows: tiles in LDS
@@ -290,28 +320,6 @@ __device__ __forceinline__ float add_pairs(const bf16x8& v, float c) {
     return c;
 }
 
-// What a tile of 32 NW rows is: its sequence, its rows, the tokens that they see and the slices that these make.
-template <int NW>
-struct TileRows {
-    int b, rt, rows, row0, start, length, G, cap, most, tiles, used;
-    __device__ __forceinline__ TileRows(const Args& a, const Sequences& s, const Cache& c, int b_, int rt_) : b(b_), rt(rt_) {
-        const NewTokens t = new_tokens(s, b, a.M);
-        rows = min(t.count, s.max_q) * a.G;
-        row0 = t.row0, start = t.start, length = t.length, G = a.G;
-        cap = s.width << c.logT;                 // what the table covers
-        most = reach(32 * NW * rt + 32 * NW - 1, a);
-        tiles = (most + 16 * NW - 1) / (16 * NW);
-        used = max(min(a.split, (tiles + 3) / 4), 1);            // four stages each or more
-    }
-    // tokens that a row sees (of one past the last: what the last sees), and where its numbers are
-    __device__ __forceinline__ int reach(int row, const Args& a) const {
-        return min(a.causal ? max(start + max(min(row, rows - 1), 0) / G + 1, 0) : length, cap);
-    }
-    __device__ __forceinline__ int64_t at(int row, int head, const Args& a, int D) const {
-        const int r = max(min(row, rows - 1), 0);
-        return ((int64_t)(row0 + r / G) * a.Hq + head * G + r % G) * D;
-    }
-};
 // A slice's part: maximum and sum of the rows, then the numbers as the lanes hold them.
 template <int D, int NW>
 struct Partial {
@@ -352,7 +360,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
     const int i = lane & 31, h = lane >> 5;
     const int head = blockIdx.x % c.Hk, rest = blockIdx.x / c.Hk;
     const int z = rest % a.split, rt = a.tiles - 1 - rest / a.split % a.tiles, b = rest / a.split / a.tiles;
-    const TileRows<NW> g(a, s, c, b, rt);
+    const TileRows<32 * NW, 16 * NW> g(a, s, c, b, rt);
     const int rows = g.rows, most = g.most, used = g.used;
     if (kTileRows * rt >= rows || z >= used) return;             // the whole workgroup
     const int row = kTileRows * rt + 32 * wave + i, base_row = kTileRows * rt + 32 * wave;
@@ -541,7 +549,7 @@ template <int D, int NW>
 __global__ __launch_bounds__(2 * D) void k_attention_join(Args a, Sequences s, Cache c) {
     const int n = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 31, h = lane >> 5;
     const int wave = blockIdx.x % NW, head = blockIdx.x / NW % c.Hk, rest = blockIdx.x / NW / c.Hk;
-    const TileRows<NW> r(a, s, c, rest / a.tiles, rest % a.tiles);
+    const TileRows<32 * NW, 16 * NW> r(a, s, c, rest / a.tiles, rest % a.tiles);
     const int row = 32 * NW * r.rt + 32 * wave + i;
     if (32 * NW * r.rt + 32 * wave >= r.rows || r.used == 1) return;
     const Partial<D, NW> from(a, (r.b * a.tiles + r.rt) * c.Hk + head);
@@ -559,6 +567,9 @@ __global__ __launch_bounds__(2 * D) void k_attention_join(Args a, Sequences s, C
 #pragma unroll
             for (int y = 0; y < 4; ++y) v[u][y] = *from.numbers(z, wave, n, y, lane);
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)              // on their way together
+            asm volatile("" : "+v"(st[u].x), "+v"(st[u].y), "+v"(v[u][0]), "+v"(v[u][1]), "+v"(v[u][2]), "+v"(v[u][3]));
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             if (z0 + u >= r.used) break;
@@ -581,31 +592,32 @@ AttentionPlan plan_attention(int64_t M, int n_seq, int max_q, int Hq, int Hk, in
     const int64_t rows = std::min<int64_t>(max_q, M) * (Hq / Hk);
     p.rows = rows <= 32 ? 16 : rows <= 1024 ? 128 : 256;
     p.tiles = (int)((rows + p.rows - 1) / p.rows);
-    const int64_t slots = (int64_t)n_seq * p.tiles * Hk, enough = p.rows == 16 ? 1024 : 512;
+    const int64_t slots = (int64_t)n_seq * p.tiles * Hk, enough = 512;
     p.split = 1;
-    if (slots <= (int64_t)(kCounterBytes / 4))
-        while (p.split < 64 && slots * p.split < enough) p.split *= 2;
-    p.cstride = (int)std::max<int64_t>(1, std::min<int64_t>(32, kCounterBytes / 4 / slots));
+    while (p.split < 32 && slots * p.split < enough) p.split *= 2;
     p.ws_bytes = p.split > 1 ? kCounterBytes + (size_t)slots * p.split * p.rows * (8 + 4 * (size_t)D) : 0;
     return p;
 }
 
 hipError_t launch_attention(const uint16_t* q, int64_t M, int Hq, const Sequences& s, const Cache& c, float scale,
                             int causal, uint16_t* out, void* ws, const AttentionPlan& p, hipStream_t st) {
-    const Args a{q, out, (float*)((char*)ws + kCounterBytes), (uint32_t*)ws, (int)M, Hq, Hq / c.Hk, causal, p.tiles,
-                 p.split, p.cstride, scale * kLog2e};
+    const Args a{q, out, (float*)((char*)ws + kCounterBytes), (int)M, Hq, Hq / c.Hk, causal, p.tiles, p.split,
+                 scale * kLog2e};
     const unsigned grid = (unsigned)((int64_t)s.n * p.tiles * p.split * c.Hk);
     const auto go = [&](auto kernel) {
         kernel<<<grid, p.rows == 256 ? 512 : 256, 0, st>>>(a, s, c);
         return hipGetLastError();
     };
-    const auto tiles = [&](auto kernel, auto join) {
+    const auto both = [&](auto kernel, auto join, int per_slot, int threads) {
         const hipError_t e = go(kernel);
         if (e != hipSuccess || p.split == 1) return e;
-        join<<<(unsigned)((int64_t)s.n * p.tiles * c.Hk * (p.rows / 32)), 2 * c.D, 0, st>>>(a, s, c);
+        join<<<(unsigned)((int64_t)s.n * p.tiles * c.Hk * per_slot), threads, 0, st>>>(a, s, c);
         return hipGetLastError();
     };
-    if (p.rows == 16) return c.D == 128 ? go(k_attention_rows<128>) : go(k_attention_rows<64>);
+    const auto tiles = [&](auto kernel, auto join) { return both(kernel, join, p.rows / 32, 2 * c.D); };
+    if (p.rows == 16)
+        return c.D == 128 ? both(k_attention_rows<128>, k_attention_join_rows<128>, 8, 64)
+                          : both(k_attention_rows<64>, k_attention_join_rows<64>, 4, 64);
     if (p.rows == 128)
         return c.D == 128 ? tiles(k_attention_tile<128, 4>, k_attention_join<128, 4>)
                           : tiles(k_attention_tile<64, 4>, k_attention_join<64, 4>);

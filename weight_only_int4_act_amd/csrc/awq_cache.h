@@ -48,7 +48,6 @@ struct AttentionPlan {
     int split;                   // most slices of a sequence's tokens
     int rows;                    // rows per workgroup, which says which kernel: 16, 128 or 256
     int tiles;                   // row tiles per sequence and head
-    int cstride;                 // arrival counter i at word i * cstride of the counter region
     size_t ws_bytes;
 };
 AttentionPlan plan_attention(int64_t M, int n_seq, int max_q, int Hq, int Hk, int D);
