@@ -52,9 +52,27 @@ struct Head {
     static constexpr int L = D / 8;              // lanes
     // the sum of squares over the head's lanes
     static __device__ __forceinline__ double sum(double v) {
-#pragma unroll
-        for (int off = 1; off < L; off *= 2) v += __shfl_xor(v, off, kWave);
+        auto add = [&](auto move) {
+            const uint64_t b = __builtin_bit_cast(uint64_t, v);
+            const uint64_t o = (uint64_t)(uint32_t)move((int)(uint32_t)b) | ((uint64_t)(uint32_t)move((int)(uint32_t)(b >> 32)) << 32);
+            v += __builtin_bit_cast(double, o);
+        };
+        add([](int x) { return __builtin_amdgcn_mov_dpp(x, 0xB1, 0xf, 0xf, true); });    // lanes 1 0 3 2
+        add([](int x) { return __builtin_amdgcn_mov_dpp(x, 0x4E, 0xf, 0xf, true); });    // lanes 2 3 0 1
+        add([](int x) { return __builtin_amdgcn_mov_dpp(x, 0x141, 0xf, 0xf, true); });   // mirrored within 8
+        if constexpr (L == 16) add([](int x) { return __builtin_amdgcn_mov_dpp(x, 0x140, 0xf, 0xf, true); });   // within 16
         return v;
+    }
+    // lane l's number from lane l + L/2 modulo L
+    static __device__ __forceinline__ float across(float x) {
+        int v = __float_as_int(x);
+        if constexpr (L == 16) {
+            v = __builtin_amdgcn_mov_dpp(v, 0x128, 0xf, 0xf, true);                          // turned by 8 within 16
+        } else {
+            v = __builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true);                          // mirrored within 8 ..
+            v = __builtin_amdgcn_mov_dpp(v, 0x1B, 0xf, 0xf, true);                           // .. and within 4
+        }
+        return __int_as_float(v);
     }
     static __device__ __forceinline__ void norm(float (&x)[8], const uint16_t* weight, int l, double eps) {
         double s = 0.;
@@ -88,7 +106,7 @@ struct Head {
         const floatx4 s[2] = {*(const floatx4*)(turn + R / 2 + at), *(const floatx4*)(turn + R / 2 + at + 4)};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float o = __shfl(x[i], other, kWave), t = o * s[i / 4][i % 4];
+            const float o = R == D ? across(x[i]) : __shfl(x[i], other, kWave), t = o * s[i / 4][i % 4];
             if (in) x[i] = x[i] * c[i / 4][i % 4] + (low ? -t : t);
         }
     }
@@ -103,20 +121,21 @@ __device__ __forceinline__ uint2 four_tokens(const uint2& w) {
     return uint2{__builtin_amdgcn_perm(b[1], b[0], 0x06020400u), __builtin_amdgcn_perm(b[1], b[0], 0x07030501u)};
 }
 
-// A workgroup takes the new tokens of one block of the cache for one head of K and V and the heads of q that read it.
-// Bound by HBM for many tokens (per number of q 4 bytes, of K and V 3), by the chain of dependent reads for few
-// (lengths, blocks, rows).  K's and V's rows are requested first; while they come q's heads are done; the numbers of K
-// (float32, normed and rotated) and V (bf16) then stay in registers until the block's largest are known.  V's codes go
-// through LDS into their order: sixteen tokens of a number in one store where all of them are new, else bytes.
+// The new tokens of one block of the cache for one head of K and V are one workgroup's work, those of the heads of q that
+// read it another `parts` workgroups', or its own (parts = 0) where they are no more heads than a block has of K.  Bound by HBM for many tokens (per number of q 4 bytes, of K and V 3), by the
+// chain of dependent reads for few (lengths, blocks, rows).  The numbers of K (float32, normed and rotated) and V (bf16)
+// stay in registers until the block's largest are known.  V's codes go through LDS into their order: sixteen tokens of
+// a number in one store where all of them are new, else bytes.
 template <int D, int T>
-__global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, Cache c, int per_seq) {
+__global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, Cache c, int per_seq, int parts) {
     using H = Head<D>;
     constexpr int L = H::L, W = 256 / L, U = (T + W - 1) / W;   // lanes of a head, heads at a time, rounds of a block
     __shared__ uint32_t tops[4][2];
     __shared__ u32x4 vt[T / 16 * D];
     lds_poison_start(&tops[0][0], 8);
     lds_poison_start(&vt[0], T / 16 * D);
-    const int h = blockIdx.x % c.Hk, j = blockIdx.x / c.Hk % per_seq, b = blockIdx.x / c.Hk / per_seq;
+    const int h = blockIdx.x % c.Hk, part = blockIdx.x / c.Hk % (parts + 1), rest = blockIdx.x / c.Hk / (parts + 1);
+    const int j = rest % per_seq, b = rest / per_seq;
     const NewTokens t = new_tokens(s, b, (int)a.M);
     const int lane = threadIdx.x & 63, l = threadIdx.x % L;
     // which head of the W: those of lanes 16 apart are neighbours, for four_tokens
@@ -125,7 +144,7 @@ __global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, C
     const int64_t row_size = (int64_t)(a.Hq + 2 * c.Hk) * D;
 
     // positions below zero: no block; the first workgroup of a head writes zeros
-    if (j == 0 && t.start < 0) {
+    if (j == 0 && part == parts && t.start < 0) {
         const int none = min(min(t.count, -t.start), s.max_q);
         for (int i = w; i < none * G; i += W)
             *(u32x4*)(a.q + (((int64_t)t.row0 + i / G) * a.Hq + h * G + i % G) * D + l * 8) = u32x4{0, 0, 0, 0};
@@ -137,43 +156,67 @@ __global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, C
     const int n = (int)(p1 - p0), slot0 = (int)(p0 - index * T);
     const int row0 = t.row0 + (int)(p0 - t.start);
     const int turned = a.rope ? (int)min(max((int64_t)a.P - p0, (int64_t)0), (int64_t)n) : n;   // tokens that the rotation covers
+    // q: a head's eight numbers of this lane, of token tok
+    const int items = n * G;
+    struct Item {                                // a head of q: its token, where it is in q|k|v's row, whether it is one
+        int tok, col;
+        bool in;
+        u32x4 raw;
+    };
+    auto q_load = [&](int i, Item& q) __attribute__((always_inline)) {
+        q.in = i < items;                        // past the last: it again, not stored
+        q.tok = min(i, items - 1) / G;
+        q.col = (h * G + min(i, items - 1) - q.tok * G) * D + l * 8;
+        q.raw = *(const u32x4*)(a.qkv + (int64_t)(row0 + q.tok) * row_size + q.col);
+    };
+    auto q_do = [&](const Item& q) __attribute__((always_inline)) {
+        float x[8];
+        widen8(q.raw, x);
+        if (a.q_weight) H::norm(x, a.q_weight, l, a.eps);
+        if (a.rope) {
+            H::rotate(x, a.rope + min(p0 + q.tok, (int64_t)a.P - 1) * a.R, a.R, a.interleaved, l);
+            if (q.tok >= turned) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            }
+        }
+        if (q.in)
+            *(u32x4*)(a.q + (int64_t)(row0 + q.tok) * a.Hq * D + q.col) =
+                u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+    };
+    if (part < parts) {                          // the tokens' G heads, two at a time
+        for (int i0 = part * 2 * W; i0 < items; i0 += 2 * W * parts) {
+            Item x, y;
+            q_load(i0 + w, x);
+            q_load(i0 + W + w, y);
+            q_do(x);
+            q_do(y);
+        }
+        return;
+    }
     const int64_t block = index < s.width ? s.table[(int64_t)b * s.width + index] : -1;
     const bool stored = block >= 0 && block < c.blocks && turned > 0;
     const int64_t at = block * c.Hk + h;
     const int slot1 = slot0 + turned;            // slots slot0 .. slot1 - 1 get tokens; head w of round u has slot u W + w
 
-    uint32_t before = 0;
     u32x4 kr[U], v[U];
-    if (stored) {
-        before = *(const uint16_t*)(c.scales + at * 2);
+    Item qr[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = min(max(u * W + w - slot0, 0), n - 1);
-            const uint16_t* const row = a.qkv + (int64_t)(row0 + i) * row_size + (int64_t)(a.Hq + h) * D + l * 8;
-            if (u * W + W <= slot0 || u * W >= slot1) continue;  // the whole workgroup
-            kr[u] = *(const u32x4*)row;
-            v[u] = *(const u32x4*)(row + (int64_t)c.Hk * D);
-        }
-    }
-    // q: the tokens' G heads; from the second wavefront on, so that one token's K and V are another's work
-    for (int i = (w + W - 64 / L) % W; i < (n * G + W - 1) / W * W; i += W) {   // every lane of a wavefront, for the exchanges
-        const bool in = i < n * G;
-        const int tok = in ? i / G : n - 1, head = h * G + (in ? i % G : 0);
-        float x[8];
-        widen8(*(const u32x4*)(a.qkv + (int64_t)(row0 + tok) * row_size + (int64_t)head * D + l * 8), x);
-        if (a.q_weight) H::norm(x, a.q_weight, l, a.eps);
-        if (a.rope) {
-            H::rotate(x, a.rope + min(p0 + tok, (int64_t)a.P - 1) * a.R, a.R, a.interleaved, l);
-            if (tok >= turned) {
+    for (int u = 0; u < U; ++u)
+        if (parts == 0 && u * W < items) q_load(u * W + w, qr[u]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = 0.f;
-            }
-        }
-        if (in)
-            *(u32x4*)(a.q + ((int64_t)(row0 + tok) * a.Hq + head) * D + l * 8) =
-                u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+    for (int u = 0; u < U; ++u) {
+        const int i = min(max(u * W + w - slot0, 0), n - 1);
+        const uint16_t* const row = a.qkv + (int64_t)(row0 + i) * row_size + (int64_t)(a.Hq + h) * D + l * 8;
+        if (u * W + W <= slot0 || u * W >= slot1) continue;      // the whole workgroup
+        kr[u] = *(const u32x4*)row;
+        v[u] = *(const u32x4*)(row + (int64_t)c.Hk * D);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (parts == 0 && u * W < items) q_do(qr[u]);
     if (!stored) return;                         // the whole workgroup
+    const uint32_t before = *(const uint16_t*)(c.scales + at * 2);
 
     float k[U][8];
     uint32_t kt = 0, vmax = 0;
@@ -245,11 +288,11 @@ __global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, C
 }  // namespace
 
 hipError_t launch_qkv_append(const AppendArgs& a, const Sequences& s, const Cache& c, hipStream_t st) {
-    // the blocks that max_q tokens touch at most, wherever the first lies
-    const int per_seq = (int)(((int64_t)s.max_q + c.T - 2) / c.T + 1);
-    const unsigned grid = (unsigned)((int64_t)s.n * per_seq * c.Hk);
+    const int64_t per_seq = append_per_seq(s.max_q, c.T);
+    const int parts = append_parts(s.n, s.max_q, a.Hq / c.Hk, c.Hk, c.T, c.D);
+    const unsigned grid = (unsigned)(s.n * per_seq * c.Hk * (parts + 1));
     const auto go = [&](auto kernel) {
-        kernel<<<grid, 256, 0, st>>>(a, s, c, per_seq);
+        kernel<<<grid, 256, 0, st>>>(a, s, c, (int)per_seq, parts);
         return hipGetLastError();
     };
     if (c.D == 128) {

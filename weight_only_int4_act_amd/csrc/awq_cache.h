@@ -42,6 +42,17 @@ struct AppendArgs {
     int Hq, P, R, interleaved;
     double eps;
 };
+// The blocks that max_q tokens touch at most, wherever the first lies, and the workgroups that share the heads of q of one of
+// them and one head of K and V: up to four rounds of heads each.  None, where these are no more heads than a block
+// has of K and there are workgroups enough for several per CU: K's and V's take them along (6100 tokens of 40 heads,
+// each with its own K, T = 16: 97 us, with a workgroup of their own 120; one token of 64 such sequences 14.5 and 17.8; but
+// one token of one sequence of 64 and 8 heads 6.2 and 5.0, and 4096 of its tokens, T = 64: 76 and, by eight, 49).
+inline int64_t append_per_seq(int max_q, int T) { return ((int64_t)max_q + T - 2) / T + 1; }
+inline int append_parts(int n_seq, int max_q, int G, int Hk, int T, int D) {
+    const int64_t heads = (int64_t)(max_q < T ? max_q : T) * G, round = 256 / (D / 8);
+    if (heads <= T && n_seq * append_per_seq(max_q, T) >= 1024 / Hk) return 0;
+    return (int)((heads + 4 * round - 1) / (4 * round));
+}
 hipError_t launch_qkv_append(const AppendArgs& a, const Sequences& s, const Cache& c, hipStream_t st);
 
 struct AttentionPlan {

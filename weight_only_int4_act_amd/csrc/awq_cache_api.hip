@@ -66,8 +66,8 @@ int awq_qkv_append(const void* qkv_bf16, int64_t M, int32_t Hq, int32_t Hk, int3
     if (!aligned(qkv_bf16, 16) || !aligned(q_weight_bf16, 16) || !aligned(k_weight_bf16, 16) || !aligned(rope, 16) ||
         !aligned(q_bf16, 16))
         return AWQ_ERR_INVALID_ARG;
-    const int64_t per_seq = ((int64_t)max_q + T - 2) / T + 1;
-    if (n_seq * per_seq > kIntMax / Hk) return AWQ_ERR_INVALID_ARG;
+    const int64_t each = (int64_t)Hk * (awq::append_parts(n_seq, max_q, Hq / Hk, Hk, T, D) + 1);
+    if (n_seq * awq::append_per_seq(max_q, T) > kIntMax / each) return AWQ_ERR_INVALID_ARG;
     const size_t row = (size_t)M * D * 2, kv = block_bytes(blocks, Hk, T, D);
     const Range out[] = {{q_bf16, row * Hq}, {k_codes, kv}, {v_codes, kv}, {scales, (size_t)blocks * Hk * 2}};
     const Range in[] = {{qkv_bf16, row * (Hq + 2 * Hk)}, {q_weight_bf16, (size_t)D * 2}, {k_weight_bf16, (size_t)D * 2},
