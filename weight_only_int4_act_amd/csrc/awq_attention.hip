@@ -76,7 +76,8 @@ struct TileRows {
 //                   (i, g) gives K's row of token 16 (i / 4) + 4t + i % 4, and takes 16 results of query row i;
 //   second product  O^T = V^T P^T: lane (i, g) gives the 16 bytes of number i of V's 16 tokens, and its own
 //                   results, in the order in which they are.
-// K and V become bf16 in registers (exact).  The running maximum and sum are per row; every wavefront has its own,
+// K and V become bf16 in registers (exact); p goes into the second product as two bf16 numbers, whose cost the loads
+// hide.  The running maximum and sum are per row; every wavefront has its own,
 // joined in LDS at the end, and those of several slices by k_attention_join_rows.
 template <int D>
 __global__ __launch_bounds__(256) void k_attention_rows(Args a, Sequences s, Cache c) {
@@ -187,12 +188,19 @@ __global__ __launch_bounds__(256) void k_attention_rows(Args a, Sequences s, Cac
                 p[u][r] = __builtin_amdgcn_exp2f(p[u][r] - base);
                 sum += p[u][r];
             }
-        bf16x8 w[2];
+        bf16x8 w[2], rest[2];                    // p and what its rounding to bf16 leaves: 16 bits of it
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-            w[y] = __builtin_bit_cast(bf16x8, u32x4{pack_bf16x2(p[2 * y][0], p[2 * y][1]), pack_bf16x2(p[2 * y][2], p[2 * y][3]),
-                                                    pack_bf16x2(p[2 * y + 1][0], p[2 * y + 1][1]),
-                                                    pack_bf16x2(p[2 * y + 1][2], p[2 * y + 1][3])});
+        for (int y = 0; y < 2; ++y) {
+            u32x4 hi, lo;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float v0 = p[2 * y + e / 2][2 * (e & 1)], v1 = p[2 * y + e / 2][2 * (e & 1) + 1];
+                hi[e] = pack_bf16x2(v0, v1);
+                lo[e] = pack_bf16x2(v0 - bf16_lo(hi[e]), v1 - bf16_hi(hi[e]));
+            }
+            w[y] = __builtin_bit_cast(bf16x8, hi);
+            rest[y] = __builtin_bit_cast(bf16x8, lo);
+        }
         // what lies behind the sequence's last token may be anything, NaN among it: zeros
         const int live = bv < 0 ? 0 : t.length - first - 16 * g;
         const uint64_t lo = live >= 8 ? ~0ull : (1ull << 8 * max(live, 0)) - 1;
@@ -203,8 +211,11 @@ __global__ __launch_bounds__(256) void k_attention_rows(Args a, Sequences s, Cac
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[n][r] *= keep;
             const u32x4 x = v[n] & mask;
-            o[n] = mfma16x16x32(widen_codes(x[0], x[1], fv), w[0], o[n]);
-            o[n] = mfma16x16x32(widen_codes(x[2], x[3], fv), w[1], o[n]);
+            const bf16x8 x0 = widen_codes(x[0], x[1], fv), x1 = widen_codes(x[2], x[3], fv);
+            o[n] = mfma16x16x32(x0, rest[0], o[n]);
+            o[n] = mfma16x16x32(x1, rest[1], o[n]);
+            o[n] = mfma16x16x32(x0, w[0], o[n]);
+            o[n] = mfma16x16x32(x1, w[1], o[n]);
         }
         __builtin_amdgcn_sched_barrier(0);
         if (more) load_v(first + 4 * kTile, bv1);
