@@ -477,13 +477,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
             const uint8_t* const kb = lb + stage * kStage + 64 * part * D * 2;
             floatx16 p[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) p[u][r] = 0.f;
 #pragma unroll
-                for (int n = 0; n < D / 16; ++n)
+            for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
                     p[u] = mfma32x32x16(*(const bf16x8*)(kb + (32 * u + i) * D * 2 + 16 * k_slot(i, 2 * n + h)), q[n], p[u]);
-            }
             if (first + kTile > all || groups != 15) {            // a token that some row does not see
 #pragma unroll
                 for (int u = 0; u < 2; ++u)

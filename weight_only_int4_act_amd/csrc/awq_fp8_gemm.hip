@@ -448,33 +448,46 @@ constexpr size_t kCounterBytes = 65536;
 constexpr int kCus = kNumXcd * kCusPerXcd;
 constexpr int kMaxSlices = 16;
 
+// Which kernel, and how many slices of K, by the time that each would take: us on this card, fitted to launches on weights that
+// no cache holds (K = 1024 .. 28672, N = 1024 .. 28672):
+//   register kernel: one workgroup per CU once K is cut, with a group of channels or more for every wavefront (1 x 8192 x 1024,
+//     1, 2, 4, 8 slices: 12.9, 9.9, 7.5, 6.6 us; 1 x 1024 x 8192, 1 and 2: 5.1, 6.0; 1 x 28672 x 8192, 1, 2, 4: 54.8, 41.8,
+//     42.1); for 33 to 64 rows 4.5 + .25 + .0047 M for each group of channels that a CU takes;
+//   tiles of 64 wm rows: 2.5 + turns * turn_us for each round of one workgroup per CU, where a turn takes the longer the more
+//     CUs have one (2 x 128 rows: .83 us with half of the CUs, 1.0 with all), and for joining slices 3 + .35 per MB of
+//     partials; not less than the weights' bytes at 4.6 TB/s.  257 x 5120 x 13824: 37 us with 128 rows a tile, 68 with 64, 62 with 256;
+//     2048 x 8192 x 8192: 120 us with 256 rows, 132 with 128; 512 x 8192 x 8192, 128 rows, 1, 2, 4 slices: 60, 51, 61; 64 x 8192
+//     x 28672: 53 us by tiles, 69 by the register kernel, 48 x 8192 x 8192 22 and 20.
 Fp8GemmPlan plan_fp8_gemm(int64_t M, int64_t K, int64_t N) {
-    Fp8GemmPlan p{};
+    Fp8GemmPlan p{};                             // wm = 0: the register kernel
     const int64_t chunks = fp8_kc(K);
+    double best = 1e30;
     if (M <= 64) {
         p.col_tiles = fp8_nt(N);
-        const int rf = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-        p.row_tiles = (M + 16 * rf - 1) / (16 * rf);
-        const int64_t groups = p.col_tiles * p.row_tiles;
+        p.row_tiles = 1;
+        const int rf = M <= 16 ? 1 : M <= 32 ? 2 : 4, least = rf == 1 ? 8 : 4;   // wavefronts: groups of channels per slice
         p.nz = 1;
-        if (groups <= (int64_t)(kCounterBytes / 4))
-            while (p.nz < kMaxSlices && groups * p.nz * 2 <= kCus && chunks / (p.nz * 2) >= 4) p.nz *= 2;
-        p.cstride = (int)std::max<int64_t>(1, std::min<int64_t>(32, kCounterBytes / 4 / groups));
-        p.ws_bytes = p.nz > 1 ? kCounterBytes + (size_t)groups * p.nz * rf * 4096 : 0;
-        return p;
+        if (p.col_tiles <= (int64_t)(kCounterBytes / 4))
+            while (p.nz < kMaxSlices && p.col_tiles * p.nz * 2 <= kCus && chunks >= p.nz * 2 * least) p.nz *= 2;
+        p.cstride = (int)std::max<int64_t>(1, std::min<int64_t>(32, kCounterBytes / 4 / p.col_tiles));
+        p.ws_bytes = p.nz > 1 ? kCounterBytes + (size_t)p.col_tiles * p.nz * rf * 4096 : 0;
+        if (M <= 32) return p;
+        const double per_cu = std::max((double)((chunks + p.nz - 1) / p.nz), (double)(p.col_tiles * chunks) / kCus);
+        best = 4.5 + per_cu * (.25 + .0047 * (double)M);
     }
-    static const double start_us[3] = {4, 6, 8.5}, turn_us[3] = {.39, .63, 1.10};
-    const double stream = 2 + (double)fp8_codes_bytes(K, N) / 4e6;
-    double best = 1e30;
+    static const double turn_us[3] = {.45, .65, 1.3}, crowd_us[3] = {.41, .35, .5};
+    const double stream = 2 + (double)fp8_codes_bytes(K, N) / 4.6e6;
     for (int k = 0; k < 3; ++k) {
         const int wm = 1 << k;
         const int64_t rt = (M + 64 * wm - 1) / (64 * wm), ct = (N + 255) / 256, tiles = rt * ct;
         for (int nz = 1; nz <= kMaxSlices; ++nz) {
-            const int64_t turns = (chunks + nz - 1) / nz, groups = tiles * nz;
+            const int64_t turns = (chunks + nz - 1) / nz, groups = tiles * nz, full = groups / kCus, rest = groups % kCus;
             if (nz > 1 && (turns < 4 || groups > kCus)) break;
-            const double rounds = (double)((groups + kCus - 1) / kCus);
-            const double us = std::max(stream, 1.5 + rounds * (start_us[k] + turns * turn_us[k])) +
-                              (nz == 1 ? 0 : 2 + .35e-6 * (double)(groups * 64 * wm * 256 * 4));
+            const double rounds = (double)full * (turn_us[k] + crowd_us[k]) +
+                                  (rest ? turn_us[k] + crowd_us[k] * (double)rest / kCus : 0);
+            const double total = 2.5 + (double)turns * rounds +
+                                 (nz == 1 ? 0 : 3 + .35e-6 * (double)(groups * 64 * wm * 256 * 4));
+            const double us = std::max(stream, total) + .1 * total;
             if (us >= best) continue;
             best = us;
             p.wm = wm;
