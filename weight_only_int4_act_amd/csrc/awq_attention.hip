@@ -5,6 +5,7 @@
 // row r is token r / G, head r % G.  A key or value that one workgroup has loaded serves all of them.
 #include <algorithm>
 
+#include "awq_buffer.h"
 #include "awq_cache.h"
 
 namespace awq {
@@ -273,28 +274,32 @@ __global__ __launch_bounds__(64) void k_attention_join_rows(Args a, Sequences s,
     const TileRows<16, kTile> t(a, s, c, rest / a.tiles, rest % a.tiles);
     const int i = part * R + threadIdx.x / L, d = threadIdx.x % L * 4, row = 16 * t.rt + i;
     if (row >= t.rows || t.used == 1) return;
-    const float* const from = a.part + (int64_t)((t.b * a.tiles + t.rt) * c.Hk + h) * a.split * (16 * (2 + D));
+    constexpr uint32_t kPart = 16 * (2 + D) * 4;
+    const float* const from = a.part + (int64_t)((t.b * a.tiles + t.rt) * c.Hk + h) * a.split * (kPart / 4);
+    // a slice past the last lies outside: it brings zeros and costs nothing (the last one again, instead, cost 4 us)
+    const __amdgpu_buffer_rsrc_t pr = rsrc(from, (int64_t)t.used * kPart);
     float m = -INFINITY, sum = 0.f;
     floatx4 x = {0.f, 0.f, 0.f, 0.f};
     for (int z0 = 0; z0 < t.used; z0 += kFlight) {
-        float2 st[kFlight];
+        float top[kFlight], part_sum[kFlight];
         floatx4 v[kFlight];
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            const float* const p = from + (int64_t)min(z0 + u, t.used - 1) * (16 * (2 + D));
-            st[u] = *(const float2*)(p + 2 * i);
-            v[u] = *(const floatx4*)(p + 32 + i * D + d);
+            const uint32_t p = (uint32_t)(z0 + u) * kPart;
+            const auto st = __builtin_amdgcn_raw_buffer_load_b64(pr, p + 8 * i, 0, 0);
+            top[u] = __uint_as_float(st[0]), part_sum[u] = __uint_as_float(st[1]);
+            v[u] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(pr, p + 128 + (i * D + d) * 4, 0, 0));
         }
         // every load is on its way before the first is waited for (a branch around their use would take them along)
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) asm volatile("" : "+v"(st[u].x), "+v"(st[u].y), "+v"(v[u]));
+        for (int u = 0; u < kFlight; ++u) asm volatile("" : "+v"(top[u]), "+v"(part_sum[u]), "+v"(v[u]));
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            if (z0 + u >= t.used) break;
-            const float now = fmaxf(m, st[u].x), base = now == -INFINITY ? 0.f : now;
-            const float keep = __builtin_amdgcn_exp2f(m - base), f = __builtin_amdgcn_exp2f(st[u].x - base);
+            if (z0 + u >= t.used) top[u] = -INFINITY;            // past the last slice: nothing
+            const float now = fmaxf(m, top[u]), base = now == -INFINITY ? 0.f : now;
+            const float keep = __builtin_amdgcn_exp2f(m - base), f = __builtin_amdgcn_exp2f(top[u] - base);
             m = now;
-            sum = sum * keep + st[u].y * f;
+            sum = sum * keep + part_sum[u] * f;
             x = x * keep + v[u] * f;
         }
     }
@@ -337,9 +342,10 @@ struct Partial {
     static constexpr int kRows = 32 * NW, kFloats = kRows * 2 + kRows * D;
     float* base;
     __device__ __forceinline__ Partial(const Args& a, int slot) : base(a.part + (int64_t)slot * a.split * kFloats) {}
-    __device__ __forceinline__ float* stats(int z, int row) const { return base + (int64_t)z * kFloats + row * 2; }
-    __device__ __forceinline__ floatx4* numbers(int z, int wave, int n, int y, int lane) const {
-        return (floatx4*)(base + (int64_t)z * kFloats + kRows * 2 + (((wave * (D / 32) + n) * 4 + y) * 64 + lane) * 4);
+    // offsets in floats: of a slice's row's maximum and sum, of four of its numbers
+    static __device__ __forceinline__ uint32_t stats_at(int z, int row) { return (uint32_t)z * kFloats + row * 2; }
+    static __device__ __forceinline__ uint32_t numbers_at(int z, int wave, int n, int y, int lane) {
+        return (uint32_t)z * kFloats + kRows * 2 + (((wave * (D / 32) + n) * 4 + y) * 64 + lane) * 4;
     }
 };
 // 32 numbers of a row, of which lane (i, h) holds 8y + 4h .. + 3: as bf16, 16 bytes a lane.
@@ -541,13 +547,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
 #pragma unroll
     for (int n = 0; n < NB; ++n) asm volatile("" : "+v"(o[n]));  // the products stay before the branches
     if (used > 1) {                              // several slices: k_attention_join adds them
-        const Partial<D, NW> to(a, (b * a.tiles + rt) * c.Hk + head);
+        using P = Partial<D, NW>;
+        const P to(a, (b * a.tiles + rt) * c.Hk + head);
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-                *to.numbers(z, wave, n, y, lane) = floatx4{o[n][4 * y], o[n][4 * y + 1], o[n][4 * y + 2], o[n][4 * y + 3]};
-        to.stats(z, 32 * wave + i)[h] = h ? sum : m;
+                *(floatx4*)(to.base + P::numbers_at(z, wave, n, y, lane)) = floatx4{o[n][4 * y], o[n][4 * y + 1], o[n][4 * y + 2], o[n][4 * y + 3]};
+        to.base[P::stats_at(z, 32 * wave + i) + h] = h ? sum : m;
         return;
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;              // nothing seen: zeros
@@ -564,31 +571,34 @@ __global__ __launch_bounds__(2 * D) void k_attention_join(Args a, Sequences s, C
     const TileRows<32 * NW, 16 * NW> r(a, s, c, rest / a.tiles, rest % a.tiles);
     const int row = 32 * NW * r.rt + 32 * wave + i;
     if (32 * NW * r.rt + 32 * wave >= r.rows || r.used == 1) return;
-    const Partial<D, NW> from(a, (r.b * a.tiles + r.rt) * c.Hk + head);
+    using P = Partial<D, NW>;
+    const P from(a, (r.b * a.tiles + r.rt) * c.Hk + head);
+    const __amdgpu_buffer_rsrc_t pr = rsrc(from.base, (int64_t)r.used * P::kFloats * 4);   // past the last slice: zeros
     float m = -INFINITY, sum = 0.f;
     floatx16 o;
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[e] = 0.f;
     for (int z0 = 0; z0 < r.used; z0 += 4) {     // four slices' loads in flight
-        float2 st[4];
+        float top[4], part_sum[4];
         floatx4 v[4][4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int z = min(z0 + u, r.used - 1);
-            st[u] = *(const float2*)from.stats(z, 32 * wave + i);
+            const auto st = __builtin_amdgcn_raw_buffer_load_b64(pr, P::stats_at(z0 + u, 32 * wave + i) * 4, 0, 0);
+            top[u] = __uint_as_float(st[0]), part_sum[u] = __uint_as_float(st[1]);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) v[u][y] = *from.numbers(z, wave, n, y, lane);
+            for (int y = 0; y < 4; ++y)
+                v[u][y] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(pr, P::numbers_at(z0 + u, wave, n, y, lane) * 4, 0, 0));
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)              // on their way together
-            asm volatile("" : "+v"(st[u].x), "+v"(st[u].y), "+v"(v[u][0]), "+v"(v[u][1]), "+v"(v[u][2]), "+v"(v[u][3]));
+            asm volatile("" : "+v"(top[u]), "+v"(part_sum[u]), "+v"(v[u][0]), "+v"(v[u][1]), "+v"(v[u][2]), "+v"(v[u][3]));
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            if (z0 + u >= r.used) break;
-            const float now = fmaxf(m, st[u].x), base = now == -INFINITY ? 0.f : now;
-            const float keep = __builtin_amdgcn_exp2f(m - base), g = __builtin_amdgcn_exp2f(st[u].x - base);
+            if (z0 + u >= r.used) top[u] = -INFINITY;            // past the last slice: nothing
+            const float now = fmaxf(m, top[u]), base = now == -INFINITY ? 0.f : now;
+            const float keep = __builtin_amdgcn_exp2f(m - base), g = __builtin_amdgcn_exp2f(top[u] - base);
             m = now;
-            sum = sum * keep + st[u].y * g;
+            sum = sum * keep + part_sum[u] * g;
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = o[e] * keep + v[u][e / 4][e % 4] * g;
         }
