@@ -413,41 +413,52 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
     auto group_of = [&](int n) { return D == 128 ? NG / 2 * n + (wave >> 1) : wave; };
     constexpr int kPieces = D / 16;              // of a K row
     const int token = threadIdx.x / kPieces, piece = threadIdx.x % kPieces, number = threadIdx.x % D;
+    // What belongs to 16 tokens is worked out by the lane of that number, for all groups at once, and handed to the
+    // wavefront from there: addresses in scalar arithmetic cost more than the products waited.
+    const uint32_t k_off = (uint32_t)((token & 15) * D + 16 * piece), v_off = (uint32_t)(16 * number);
+    const uint32_t block_bytes = (uint32_t)(c.Hk * c.T * D);
+    const uint64_t head_bytes = (uint64_t)(head * c.T) * D;
+    auto handed = [&](uint64_t v, int grp) __attribute__((always_inline)) {
+        return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, grp) |
+                         (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), grp) << 32);
+    };
     u32x4 kn[NP], vn[NP];
     auto load = [&](int tile, int blk) __attribute__((always_inline)) {
+        const int first = tile * kTokens + 16 * (lane & (NG - 1));
+        const uint64_t base = (uint64_t)(uint32_t)max(blk, 0) * block_bytes + head_bytes + (uint32_t)((first & (c.T - 1)) * D);
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-            const int grp = group_of(n), first = tile * kTokens + 16 * grp;
-            const int64_t base = ((int64_t)max(__builtin_amdgcn_readlane(blk, grp), 0) * c.Hk + head) * c.T + (first & (c.T - 1));
-            kn[n] = *(const u32x4*)(c.k + (base + (token & 15)) * D + 16 * piece);
-            vn[n] = *(const u32x4*)(c.v + base * D + 16 * number);
+            const int64_t at = handed(base, group_of(n));
+            kn[n] = *(const u32x4*)(c.k + at + k_off);
+            vn[n] = *(const u32x4*)(c.v + at + v_off);
         }
     };
     uint8_t* const lb = (uint8_t*)lds;
     auto k_slot = [](int r, int p) { return D == 128 ? p ^ (r & 15) : p ^ (r / 2 & 7); };
     auto v_slot = [](int r, int p) { return kVRow == 256 ? p ^ (r & 15) : p ^ (r / 2 & 7); };
-    auto store = [&](int tile, int stage, int blk, uint32_t sc) __attribute__((always_inline)) {
+    auto store = [&](int tile, int stage, int blk, uint32_t e, bool whole) __attribute__((always_inline)) {
+        const bool marked = (e & 255) == 255 || e >> 8 == 255;   // K becomes NaN, V finite
+        const uint32_t ks = marked ? 0x7f800000u : (e & 255) << 23, vs = marked ? 127u << 23 : (e >> 8) << 23;
+        const int live = blk < 0 ? 0 : g.length - tile * kTokens - 16 * (lane & (NG - 1));
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
             const int grp = group_of(n), r = 16 * grp + (token & 15);
-            const uint32_t e = __builtin_amdgcn_readlane(sc, grp);
-            const bool marked = (e & 255) == 255 || e >> 8 == 255;   // K becomes NaN, V finite
-            const float ks = __uint_as_float(marked ? 0x7f800000u : (e & 255) << 23);
-            const float vs = __uint_as_float(marked ? 127u << 23 : (e >> 8) << 23);
+            const float k_scale = __uint_as_float(__builtin_amdgcn_readlane(ks, grp));
+            const float v_scale = __uint_as_float(__builtin_amdgcn_readlane(vs, grp));
             uint8_t* const kr = lb + stage * kStage + r * D * 2;
-            *(bf16x8*)(kr + 16 * k_slot(r, 2 * piece)) = widen_codes(kn[n][0], kn[n][1], ks);
-            *(bf16x8*)(kr + 16 * k_slot(r, 2 * piece + 1)) = widen_codes(kn[n][2], kn[n][3], ks);
-            // what lies behind the sequence's last token, or in no block, may be anything, NaN among it: zeros
-            const int live = __builtin_amdgcn_readlane(blk, grp) < 0 ? 0 : g.length - tile * kTokens - 16 * grp;
+            *(bf16x8*)(kr + 16 * k_slot(r, 2 * piece)) = widen_codes(kn[n][0], kn[n][1], k_scale);
+            *(bf16x8*)(kr + 16 * k_slot(r, 2 * piece + 1)) = widen_codes(kn[n][2], kn[n][3], k_scale);
             u32x4 x = vn[n];
-            if (live < 16) {
-                const uint64_t bytes = live >= 8 ? ~0ull : (1ull << 8 * max(live, 0)) - 1;
-                const uint64_t more = live <= 8 ? 0ull : (1ull << 8 * (live - 8)) - 1;
-                x &= u32x4{(uint32_t)bytes, (uint32_t)(bytes >> 32), (uint32_t)more, (uint32_t)(more >> 32)};
+            if (!whole) {
+                // what lies behind the sequence's last token, or in no block, may be anything, NaN among it: zeros
+                const int left = __builtin_amdgcn_readlane(live, grp);
+                const uint64_t lo = left >= 8 ? ~0ull : (1ull << 8 * max(left, 0)) - 1;
+                const uint64_t hi = left >= 16 ? ~0ull : left <= 8 ? 0ull : (1ull << 8 * (left - 8)) - 1;
+                x &= u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
             }
             uint8_t* const vr = lb + stage * kStage + kK + number * kVRow;
-            *(bf16x8*)(vr + 16 * v_slot(number, 2 * grp)) = widen_codes(x[0], x[2], vs);
-            *(bf16x8*)(vr + 16 * v_slot(number, 2 * grp + 1)) = widen_codes(x[1], x[3], vs);
+            *(bf16x8*)(vr + 16 * v_slot(number, 2 * grp)) = widen_codes(x[0], x[2], v_scale);
+            *(bf16x8*)(vr + 16 * v_slot(number, 2 * grp + 1)) = widen_codes(x[1], x[3], v_scale);
         }
     };
 
@@ -463,7 +474,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
     constexpr uint32_t kAll = (1u << NG) - 1;
     uint32_t holes = (uint32_t)__ballot(blk >= 0) & kAll;        // 16-token groups that are there
     load(tb, blk);
-    store(tb, 0, blk, sc);
+    store(tb, 0, blk, sc, false);
     __syncthreads();
     for (int tile = tb; tile < te; ++tile) {
         const int stage = (tile - tb) & 1, base_token = tile * kTokens;
@@ -539,7 +550,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
                 for (int n = 0; n < NB; ++n)
                     o[n] = mfma32x32x16(*(const bf16x8*)(vb + (32 * n + i) * kVRow + 16 * v_slot(i, 8 * part + 2 * y + h)), w[y], o[n]);
         }
-        if (tile + 1 < te) store(tile + 1, stage ^ 1, blk, sc);
+        if (tile + 1 < te) store(tile + 1, stage ^ 1, blk, sc, holes == kAll && (tile + 2) * kTokens <= g.length);
         __syncthreads();
     }
     const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
