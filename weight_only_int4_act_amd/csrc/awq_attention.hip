@@ -518,8 +518,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
                 top = __builtin_elementwise_maximum(top, __builtin_elementwise_maximum(p[0][r], p[1][r]));
             const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
             top = __builtin_elementwise_maximum(__uint_as_float(both[0]), __uint_as_float(both[1])) * f;
-            if (__any(top > m + 8.f)) {          // the first numbers are, beside minus infinity
-                const float now = fmaxf(m, top), base = now == -INFINITY ? 0.f : now;
+            const bool passed = top > m + 8.f;   // the first numbers are, beside minus infinity
+            if (__any(passed)) {                 // each row by itself: its result does not depend on its neighbours'
+                const float now = passed ? top : m, base = now == -INFINITY ? 0.f : now;
                 const float keep = __builtin_amdgcn_exp2f(m - base);
                 m = now;
                 sum *= keep;
@@ -529,11 +530,19 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
                     for (int r = 0; r < 16; ++r) o[n][r] *= keep;
             }
             const float base = m == -INFINITY ? 0.f : m;
+            float by = f;
+            if (__any(fabsf(base) > 0x1p24f)) {  // the products rounded before the difference, as the maximum was: half a step
+                by = 1.f;                        // of such a maximum would be a power of two of its own
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) p[u][r] *= f;
+            }
             bf16x8 w[4];                         // 16 tokens each
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) p[u][r] = __builtin_amdgcn_exp2f(fmaf(p[u][r], f, -base));
+                for (int r = 0; r < 16; ++r) p[u][r] = __builtin_amdgcn_exp2f(fmaf(p[u][r], by, -base));
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
                     w[2 * u + y] = __builtin_bit_cast(
@@ -638,7 +647,7 @@ hipError_t launch_attention(const uint16_t* q, int64_t M, int Hq, const Sequence
                  scale * kLog2e};
     const unsigned grid = (unsigned)((int64_t)s.n * p.tiles * p.split * c.Hk);
     const auto go = [&](auto kernel) {
-        kernel<<<grid, p.rows == 256 ? 512 : 256, 0, st>>>(a, s, c);
+        kernel<<<grid, attention_threads(p), 0, st>>>(a, s, c);
         return hipGetLastError();
     };
     const auto both = [&](auto kernel, auto join, int per_slot, int threads) {

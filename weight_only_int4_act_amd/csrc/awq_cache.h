@@ -61,6 +61,7 @@ struct AttentionPlan {
     int tiles;                   // row tiles per sequence and head
     size_t ws_bytes;
 };
+inline int attention_threads(const AttentionPlan& p) { return p.rows == 256 ? 512 : 256; }   // of a workgroup
 AttentionPlan plan_attention(int64_t M, int n_seq, int max_q, int Hq, int Hk, int D);
 hipError_t launch_attention(const uint16_t* q, int64_t M, int Hq, const Sequences& s, const Cache& c, float scale,
                             int causal, uint16_t* out, void* ws, const AttentionPlan& p, hipStream_t st);

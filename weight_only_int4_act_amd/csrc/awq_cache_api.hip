@@ -1,5 +1,6 @@
 // C ABI of the 8-bit cache's operators (declared in include/awq.h): argument validation on the host, then launches on
 // the caller's stream.  Nothing is allocated, freed or synchronized here.
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/awq.h"
@@ -10,6 +11,7 @@ namespace {
 constexpr int64_t kIntMax = 0x7fffffff;
 constexpr int kHeadsMax = 1024;
 constexpr int64_t kTokensMax = (int64_t)1 << 30;         // width * T: positions stay far from 2^31
+constexpr int64_t kThreadsMax = 0xffffffff;              // of a launch
 
 bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -66,8 +68,9 @@ int awq_qkv_append(const void* qkv_bf16, int64_t M, int32_t Hq, int32_t Hk, int3
     if (!aligned(qkv_bf16, 16) || !aligned(q_weight_bf16, 16) || !aligned(k_weight_bf16, 16) || !aligned(rope, 16) ||
         !aligned(q_bf16, 16))
         return AWQ_ERR_INVALID_ARG;
-    const int64_t each = (int64_t)Hk * (awq::append_parts(n_seq, max_q, Hq / Hk, Hk, T, D) + 1);
-    if (n_seq * awq::append_per_seq(max_q, T) > kIntMax / each) return AWQ_ERR_INVALID_ARG;
+    const int32_t most = (int32_t)std::min<int64_t>(max_q, M);
+    const int64_t each = (int64_t)Hk * (awq::append_parts(n_seq, most, Hq / Hk, Hk, T, D) + 1);
+    if (n_seq * awq::append_per_seq(most, T) > kThreadsMax / 256 / each) return AWQ_ERR_INVALID_ARG;
     const size_t row = (size_t)M * D * 2, kv = block_bytes(blocks, Hk, T, D);
     const Range out[] = {{q_bf16, row * Hq}, {k_codes, kv}, {v_codes, kv}, {scales, (size_t)blocks * Hk * 2}};
     const Range in[] = {{qkv_bf16, row * (Hq + 2 * Hk)}, {q_weight_bf16, (size_t)D * 2}, {k_weight_bf16, (size_t)D * 2},
@@ -76,7 +79,7 @@ int awq_qkv_append(const void* qkv_bf16, int64_t M, int32_t Hq, int32_t Hk, int3
     if (!disjoint(out, in)) return AWQ_ERR_INVALID_ARG;
     const awq::AppendArgs a{(const uint16_t*)qkv_bf16, (const uint16_t*)q_weight_bf16, (const uint16_t*)k_weight_bf16,
                             rope, (uint16_t*)q_bf16, M, Hq, (int)P, R, interleaved, (double)eps};
-    const awq::Sequences s{cu, length, table, n_seq, width, max_q};
+    const awq::Sequences s{cu, length, table, n_seq, width, most};
     const awq::Cache c{k_codes, v_codes, scales, blocks, Hk, D, T, log2_of(T)};
     return awq::record_hip(awq::launch_qkv_append(a, s, c, (hipStream_t)stream));
 }
@@ -97,7 +100,7 @@ int awq_attention(const void* q_bf16, int64_t M, int32_t Hq, int32_t Hk, int32_t
     if (!std::isfinite(scale) || (causal != 0 && causal != 1)) return AWQ_ERR_INVALID_ARG;
     if (!aligned(q_bf16, 16) || !aligned(out_bf16, 16)) return AWQ_ERR_INVALID_ARG;
     const awq::AttentionPlan p = awq::plan_attention(M, n_seq, max_q, Hq, Hk, D);
-    if ((int64_t)n_seq * p.tiles > kIntMax / ((int64_t)p.split * Hk)) return AWQ_ERR_INVALID_ARG;
+    if ((int64_t)n_seq * p.tiles > kThreadsMax / awq::attention_threads(p) / ((int64_t)p.split * Hk)) return AWQ_ERR_INVALID_ARG;
     if (ws_bytes < p.ws_bytes || (p.ws_bytes && !workspace)) return AWQ_ERR_WORKSPACE;
     if (p.ws_bytes && !aligned(workspace, 256)) return AWQ_ERR_INVALID_ARG;
     const size_t row = (size_t)M * Hq * D * 2, kv = block_bytes(blocks, Hk, T, D);
