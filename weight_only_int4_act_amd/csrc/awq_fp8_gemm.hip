@@ -426,15 +426,15 @@ __global__ __launch_bounds__(256) void k_fp8_join(const float* __restrict__ part
     const int panel = tile / (8 * col_tiles), in = tile % (8 * col_tiles), prow = min(8, row_tiles - 8 * panel);
     const int rt = 8 * panel + in % prow, ct = in / prow;
     const int a = f % 4, j = f / 4 % CF, rf = f / (4 * CF) % 2, wave = f / (8 * CF);
-    const float* p = part + (int64_t)tile * nz * (kPart / 4) + f * 256 + lane * 4;
+    const __amdgpu_buffer_rsrc_t pr = rsrc(part + (int64_t)tile * nz * (kPart / 4), (int64_t)nz * kPart);   // past the last slice: zeros
     floatx4 sum = floatx4{0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s < nz; s += 8) {
         floatx4 v[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = *(const floatx4*)(p + (int64_t)min(s + u, nz - 1) * (kPart / 4));
-#pragma unroll
         for (int u = 0; u < 8; ++u)
-            if (s + u < nz) sum += v[u];
+            v[u] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(pr, (uint32_t)(s + u) * kPart + f * 1024 + lane * 16, 0, 0));
+#pragma unroll
+        for (int u = 0; u < 8; ++u) sum += v[u];
     }
     const int64_t m = (int64_t)rt * kRows + wave / WN * 64 + rf * 32 + i;
     const int64_t n = (int64_t)ct * 256 + (wave % WN * CF + j) * 32 + 8 * a + 4 * h;
