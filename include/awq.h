@@ -445,7 +445,8 @@ int awq_fp8_gemm(const uint8_t* xcodes, const float* xscales, int64_t M, const u
  *   length  int32 [n_seq]: the sequence's tokens, the new ones included: the i-th of n new ones has position
  *           length - n + i.
  *   table   int32 [n_seq, width]: tokens T j .. T j + T - 1 of sequence b are in block table[b, j].
- *   max_q   at least the largest number of new tokens of one sequence (a host number; it sizes the launch).
+ *   max_q   at least the largest number of new tokens of one sequence (a host number; it sizes the launch, which is
+ *           refused where it would pass 2^32 threads).
  * The arrays are read on the device and may change between replays of a captured graph.  Values that fit
  * nothing are taken as follows, without a fault: a cu below the one before it or past the rows: as that bound; a
  * block outside [0, blocks) or past the table's width: its tokens are neither stored nor seen; a token at a
@@ -459,13 +460,13 @@ int awq_fp8_gemm(const uint8_t* xcodes, const float* xscales, int64_t M, const u
  *             in float64; eps in (0, 1] (read only with a weight).
  *   rope      float32 [P, R] or NULL (no rotation): cosines, then sines, of position p's R/2 angles.  Pair i of a head
  *             is numbers i and i + R/2, or 2i and 2i + 1 (interleaved = 1); (a, c) becomes (a cos - c sin,
- *             c cos + a sin); numbers past R stay.  R a multiple of 16, at most D.  A position past P counts as a
- *             negative one does.
+ *             c cos + a sin); numbers past R stay.  R a multiple of 16, at most D.  A token past position P - 1 is not
+ *             stored and its q is zero.
  *   q         bf16 [M, Hq, D] out.
  * All in float32, rounded once.  A block that a sequence begins takes its scale from its new tokens alone; one
  * that already holds tokens of the sequence keeps the larger of its scale and theirs, and where that grows its
  * older codes are rounded again to the new scale (only numbers in e4m3's subnormal range change).  Slots of a block
- * that no token has reached are left as they were.  A block that tokens are appended to must belong to one sequence only.
+ * that no token has reached are left as they were.  A block that tokens are appended to must stand in the tables once.
  * M at most 2^31 / ((Hq + 2 Hk) D).
  */
 int awq_qkv_append(const void* qkv_bf16, int64_t M, int32_t Hq, int32_t Hk, int32_t D, const void* q_weight_bf16,
@@ -477,11 +478,15 @@ int awq_qkv_append(const void* qkv_bf16, int64_t M, int32_t Hq, int32_t Hk, int3
 /* Attention over the cache: with head j of q reading head j / (Hq/Hk) of the cache, for every new token
  *   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q . k_t),
  * over the tokens of its sequence up to its own position (causal = 1) or all of them (causal = 0); zero where it sees
- * none.  Sums and exponents in float32; p_t is rounded to bf16 for the second product (its error, 2^-9 at most, is
- * of the output's own rounding's size), K and V are exact in it.
- *   q, out  bf16 [M, Hq, D];  scale  finite (often 1/sqrt(D)).
- *   workspace >= awq_attention_workspace_size(M, n_seq, max_q, Hq, Hk, D) bytes, under the rules of
- *   awq_fp8_gemm's.
+ * none, or none but with scores of minus infinity.  Sums and exponents in float32, K and V exact.  For the second
+ * product p_t is two bf16 numbers where min(max_q, M) Hq/Hk is at most 32 (16 bits of it), and one above
+ * (half a step, 2^-8 at most, of the output's own rounding's size).  A row's result does not depend on the numbers of
+ * other rows.
+ *   q, out  bf16 [M, Hq, D], M at most 2^31 / ((Hq + 2 Hk) D);  scale  finite (often 1/sqrt(D)).
+ *   workspace >= awq_attention_workspace_size(M, n_seq, max_q, Hq, Hk, D) bytes (the size may be 0), 256-byte
+ *   aligned; what it holds before a call does not matter, and its first 64 KiB are not touched: one workspace
+ *   serves any sequence of calls of this and of the products, ordered by the caller, replays of captured graphs
+ *   included.
  */
 size_t awq_attention_workspace_size(int64_t M, int32_t n_seq, int32_t max_q, int32_t Hq, int32_t Hk, int32_t D);
 int awq_attention(const void* q_bf16, int64_t M, int32_t Hq, int32_t Hk, int32_t D, const int32_t* cu,

@@ -93,3 +93,18 @@ def test_an_infinite_query_spoils_its_own_row_only(n):
         assert torch.isnan(got[1, 5]).all(), bad
         got[1, 5] = clean[1, 5]
         assert torch.equal(got, clean), bad
+
+
+@pytest.mark.parametrize("n", [3, 50, 100])
+def test_a_row_does_not_depend_on_the_numbers_of_others(n):
+    B = Batch([(150, n)], 32, 2, 128, 16, 6)
+    B.upload()
+    q0 = dev(B.queries())
+    clean = attend(B, q0)
+    for size in (2.0 ** -10, 30.0, 2.0 ** 50):            # small, beyond the running maximum, past 2^31
+        q = q0.clone()
+        q[1, 3:6] *= size
+        q[n - 1, 20] *= -size
+        got = attend(B, q)
+        got[1, 3:6], got[n - 1, 20] = clean[1, 3:6], clean[n - 1, 20]
+        assert torch.equal(got, clean), size

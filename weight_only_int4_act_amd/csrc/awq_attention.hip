@@ -531,12 +531,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
             }
             const float base = m == -INFINITY ? 0.f : m;
             float by = f;
-            if (__any(fabsf(base) > 0x1p24f)) {  // the products rounded before the difference, as the maximum was: half a step
-                by = 1.f;                        // of such a maximum would be a power of two of its own
+            const bool far = fabsf(base) > 0x1p24f;
+            if (__any(far)) {                    // the products rounded before the difference, as the maximum was: half a step
+                by = far ? 1.f : f;              // of such a maximum would be a power of two of its own
+                const float to = far ? f : 1.f;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) p[u][r] *= f;
+                    for (int r = 0; r < 16; ++r) p[u][r] *= to;
             }
             bf16x8 w[4];                         // 16 tokens each
 #pragma unroll
