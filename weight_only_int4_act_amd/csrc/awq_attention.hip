@@ -14,6 +14,7 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kTile = 64;                        // tokens that a wavefront takes at a time
+constexpr int kSliceTokens = 256;                // least tokens of a slice
 constexpr size_t kCounterBytes = 65536;          // left alone: the products' arrival counters, in a workspace that they share
 
 // Eight e4m3 codes (two words) times 2^(E - 127), the scale's exponent field, in bf16: exact.
@@ -46,8 +47,8 @@ struct Args {
     float scale;                 // times log2 e
 };
 
-// What a tile of R rows is: its sequence, its rows, the tokens that they see, and the slices of four or more tiles of
-// TOKENS tokens that these make.
+// What a tile of R rows is: its sequence, its rows, the tokens that they see, and the slices of tiles of TOKENS tokens
+// that these make.
 template <int R, int TOKENS>
 struct TileRows {
     int b, rt, rows, row0, start, length, G, cap, most, tiles, used;
@@ -58,7 +59,7 @@ struct TileRows {
         cap = s.width << c.logT;                 // what the table covers
         most = reach(R * rt + R - 1, a);
         tiles = (most + TOKENS - 1) / TOKENS;
-        used = max(min(a.split, (tiles + 3) / 4), 1);
+        used = max(min(a.split, (most + kSliceTokens - 1) / kSliceTokens), 1);
     }
     // tokens that a row sees (of one past the last: what the last sees), and where its numbers are
     __device__ __forceinline__ int reach(int row, const Args& a) const {
@@ -631,15 +632,43 @@ __global__ __launch_bounds__(2 * D) void k_attention_join(Args a, Sequences s, C
 
 }  // namespace
 
-AttentionPlan plan_attention(int64_t M, int n_seq, int max_q, int Hq, int Hk, int D) {
+// Which kernel, and how many slices of the tokens, by the time that each would take: us on this card, fitted to 3000
+// launches (1 .. 64 sequences of 1 .. 2048 new tokens and up to 16384, 1 .. 40 heads; a kernel in the mean within 15 %):
+//   start + turns * turn * (1 + crowd * workgroups / workgroups that the card holds at a time), where a turn is the kernel's
+//   tokens at a time (256 of the rows kernel's four wavefronts), and for joining slices 1.6 + per MB of partials.
+// What this takes is in the mean 2 % slower than the best of all, where 32 rows and 1024 rows as bounds between the kernels and
+// slices for 512 workgroups took 10 %: 2 sequences of 85 tokens, 32 heads: 16 rows 9.2 us, 128 rows 15.8; 42 of 109 tokens, 16
+// heads of q on one: 16, 128, 256 rows 36, 17, 20; 38 of 103 tokens behind 8400, 32 heads on 8: 633, 448, 393.
+// `tokens`: what the table covers, the only bound of the lengths that the host has.
+AttentionPlan plan_attention(int64_t M, int n_seq, int max_q, int Hq, int Hk, int D, int64_t tokens) {
+    struct Kernel {
+        int rows, turn_tokens, held;
+        double start[2], turn[2], crowd[2], join;                // for D = 64 and 128
+    };
+    static const Kernel kernels[3] = {{16, 256, 512, {5.4, 6.1}, {.95, 1.35}, {.9, 1.15}, .9},
+                                      {128, 64, 512, {6.5, 8.2}, {.95, 1.2}, {.55, .75}, .21},
+                                      {256, 128, 256, {6.7, 11.3}, {2., 2.5}, {.58, .62}, .21}};
     AttentionPlan p{};
-    const int64_t rows = std::min<int64_t>(max_q, M) * (Hq / Hk);
-    p.rows = rows <= 32 ? 16 : rows <= 1024 ? 128 : 256;
-    p.tiles = (int)((rows + p.rows - 1) / p.rows);
-    const int64_t slots = (int64_t)n_seq * p.tiles * Hk, enough = 512;
-    p.split = 1;
-    while (p.split < 32 && slots * p.split < enough) p.split *= 2;
-    p.ws_bytes = p.split > 1 ? kCounterBytes + (size_t)slots * p.split * p.rows * (8 + 4 * (size_t)D) : 0;
+    const int64_t rows = std::min<int64_t>(max_q, M) * (Hq / Hk), slices = (tokens + kSliceTokens - 1) / kSliceTokens;
+    const int d = D == 128;
+    double best = 1e300;
+    for (const Kernel& k : kernels) {
+        if (k.rows > 16 && rows <= k.rows / 2) break;
+        const int64_t tiles = (rows + k.rows - 1) / k.rows, slots = n_seq * tiles * Hk, turns = (tokens + k.turn_tokens - 1) / k.turn_tokens;
+        const int most = (int)std::max<int64_t>(std::min<int64_t>(32, 1024 / slots), 1);
+        const size_t part = k.rows * (8 + 4 * (size_t)D);
+        // whatever the table covers: the size that a caller asks for does not know it
+        if (most > 1) p.ws_bytes = std::max(p.ws_bytes, kCounterBytes + (size_t)slots * most * part);
+        for (int z = 1; z <= most && (z == 1 || z <= slices); z += z < 4 ? 1 : (z & (z - 1)) == 0 ? z / 2 : z / 3) {
+            const double us = k.start[d] + (double)((turns + z - 1) / z) * k.turn[d] * (1 + k.crowd[d] * (double)(slots * z) / k.held) +
+                              (z == 1 ? 0 : 1.6 + k.join * 1e-6 * (double)(slots * z) * (double)part);
+            if (us >= best) continue;
+            best = us;
+            p.rows = k.rows;
+            p.tiles = (int)tiles;
+            p.split = z;
+        }
+    }
     return p;
 }
 

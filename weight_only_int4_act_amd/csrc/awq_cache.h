@@ -59,10 +59,10 @@ struct AttentionPlan {
     int split;                   // most slices of a sequence's tokens
     int rows;                    // rows per workgroup, which says which kernel: 16, 128 or 256
     int tiles;                   // row tiles per sequence and head
-    size_t ws_bytes;
+    size_t ws_bytes;             // of any `tokens`
 };
 inline int attention_threads(const AttentionPlan& p) { return p.rows == 256 ? 512 : 256; }   // of a workgroup
-AttentionPlan plan_attention(int64_t M, int n_seq, int max_q, int Hq, int Hk, int D);
+AttentionPlan plan_attention(int64_t M, int n_seq, int max_q, int Hq, int Hk, int D, int64_t tokens);
 hipError_t launch_attention(const uint16_t* q, int64_t M, int Hq, const Sequences& s, const Cache& c, float scale,
                             int causal, uint16_t* out, void* ws, const AttentionPlan& p, hipStream_t st);
 

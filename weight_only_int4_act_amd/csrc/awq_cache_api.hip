@@ -86,7 +86,7 @@ int awq_qkv_append(const void* qkv_bf16, int64_t M, int32_t Hq, int32_t Hk, int3
 
 size_t awq_attention_workspace_size(int64_t M, int32_t n_seq, int32_t max_q, int32_t Hq, int32_t Hk, int32_t D) {
     if (!heads_ok(M, Hq, Hk, D) || n_seq <= 0 || max_q <= 0 || (D != 64 && D != 128)) return 0;
-    return awq::plan_attention(M, n_seq, max_q, Hq, Hk, D).ws_bytes;
+    return awq::plan_attention(M, n_seq, max_q, Hq, Hk, D, 1).ws_bytes;
 }
 
 int awq_attention(const void* q_bf16, int64_t M, int32_t Hq, int32_t Hk, int32_t D, const int32_t* cu,
@@ -99,7 +99,7 @@ int awq_attention(const void* q_bf16, int64_t M, int32_t Hq, int32_t Hk, int32_t
         return AWQ_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || (causal != 0 && causal != 1)) return AWQ_ERR_INVALID_ARG;
     if (!aligned(q_bf16, 16) || !aligned(out_bf16, 16)) return AWQ_ERR_INVALID_ARG;
-    const awq::AttentionPlan p = awq::plan_attention(M, n_seq, max_q, Hq, Hk, D);
+    const awq::AttentionPlan p = awq::plan_attention(M, n_seq, max_q, Hq, Hk, D, (int64_t)width * T);
     if ((int64_t)n_seq * p.tiles > kThreadsMax / awq::attention_threads(p) / ((int64_t)p.split * Hk)) return AWQ_ERR_INVALID_ARG;
     if (ws_bytes < p.ws_bytes || (p.ws_bytes && !workspace)) return AWQ_ERR_WORKSPACE;
     if (p.ws_bytes && !aligned(workspace, 256)) return AWQ_ERR_INVALID_ARG;
