@@ -479,9 +479,9 @@ int awq_qkv_append(const void* qkv_bf16, int64_t M, int32_t Hq, int32_t Hk, int3
  *   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q . k_t),
  * over the tokens of its sequence up to its own position (causal = 1) or all of them (causal = 0); zero where it sees
  * none, or none but with scores of minus infinity.  Sums and exponents in float32, K and V exact.  For the second
- * product p_t is two bf16 numbers where min(max_q, M) Hq/Hk is at most 32 (16 bits of it), and one above
- * (half a step, 2^-8 at most, of the output's own rounding's size).  A row's result does not depend on the numbers of
- * other rows.
+ * product p_t is one bf16 number (half a step, 2^-8 at most, of the output's own rounding's size), or two where
+ * few rows make the kernel that streams the cache the faster one.  A row's result does not depend on the numbers
+ * of other rows.
  *   q, out  bf16 [M, Hq, D], M at most 2^31 / ((Hq + 2 Hk) D);  scale  finite (often 1/sqrt(D)).
  *   workspace >= awq_attention_workspace_size(M, n_seq, max_q, Hq, Hk, D) bytes (the size may be 0), 256-byte
  *   aligned; what it holds before a call does not matter, and its first 64 KiB are not touched: one workspace

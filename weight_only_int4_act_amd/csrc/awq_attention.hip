@@ -632,36 +632,44 @@ __global__ __launch_bounds__(2 * D) void k_attention_join(Args a, Sequences s, C
 
 }  // namespace
 
-// Which kernel, and how many slices of the tokens, by the time that each would take: us on this card, fitted to 3000
-// launches (1 .. 64 sequences of 1 .. 2048 new tokens and up to 16384, 1 .. 40 heads; a kernel in the mean within 15 %):
-//   start + turns * turn * (1 + crowd * workgroups / workgroups that the card holds at a time), where a turn is the kernel's
-//   tokens at a time (256 of the rows kernel's four wavefronts), and for joining slices 1.6 + per MB of partials.
-// What this takes is in the mean 2 % slower than the best of all, where 32 rows and 1024 rows as bounds between the kernels and
-// slices for 512 workgroups took 10 %: 2 sequences of 85 tokens, 32 heads: 16 rows 9.2 us, 128 rows 15.8; 42 of 109 tokens, 16
-// heads of q on one: 16, 128, 256 rows 36, 17, 20; 38 of 103 tokens behind 8400, 32 heads on 8: 633, 448, 393.
+// Which kernel, and how many slices of the tokens, by the time that each would take: us on this card, fitted to 7000
+// launches (1 .. 256 sequences of 1 .. 8192 new tokens and up to 16384, 1 .. 40 heads; a kernel in the mean within 17 %):
+//   start + each * x + turns * turn * (1 + crowd * seen * x), where x is the workgroups over those that the card holds at a
+//   time, a turn the kernel's tokens at a time (256 of the rows kernel's four wavefronts), seen the part of the tokens that
+//   causal rows see, and for joining slices join + per MB of partials.
+// What this takes is in the mean 1.6 % slower than the best of all, where 32 rows and 1024 rows as bounds between the kernels
+// and slices for 512 workgroups took 10 %: 2 sequences of 85 tokens, 32 heads: 16 rows 9.2 us, 128 rows 15.8; 42 of 109 tokens,
+// 16 heads of q on one: 16, 128, 256 rows 36, 17, 20; 38 of 103 tokens behind 8400, 32 heads on 8: 633, 448, 393.
+// Where there are 512 workgroups or more without slices there are none (64 sequences of up to 8192, 64 heads on 8: 1 slice
+// 118 us, 2 130), and never more than 1024 with them (up to 2048: the same in the mean).
 // `tokens`: what the table covers, the only bound of the lengths that the host has.
 AttentionPlan plan_attention(int64_t M, int n_seq, int max_q, int Hq, int Hk, int D, int64_t tokens) {
     struct Kernel {
         int rows, turn_tokens, held;
-        double start[2], turn[2], crowd[2], join;                // for D = 64 and 128
+        double start[2], each[2], turn[2], crowd[2], join[2], join_mb;   // for D = 64 and 128
     };
-    static const Kernel kernels[3] = {{16, 256, 512, {5.4, 6.1}, {.95, 1.35}, {.9, 1.15}, .9},
-                                      {128, 64, 512, {6.5, 8.2}, {.95, 1.2}, {.55, .75}, .21},
-                                      {256, 128, 256, {6.7, 11.3}, {2., 2.5}, {.58, .62}, .21}};
+    static const Kernel kernels[3] = {
+        {16, 256, 512, {4.9, 4.8}, {1.17, 2.08}, {1.04, 1.47}, {.83, 1.05}, {1.9, 2.}, .6},
+        {128, 64, 512, {5.9, 7.1}, {1.4, 1.5}, {.95, 1.28}, {.6, .77}, {2.3, 1.6}, .25},
+        {256, 128, 256, {6.3, 9.2}, {1.9, 1.9}, {2.05, 2.7}, {.585, .657}, {2.5, 1.}, .25}};
     AttentionPlan p{};
     const int64_t rows = std::min<int64_t>(max_q, M) * (Hq / Hk), slices = (tokens + kSliceTokens - 1) / kSliceTokens;
+    const double seen = 1 - .5 * std::min((double)max_q / (double)tokens, 1.);
     const int d = D == 128;
     double best = 1e300;
+    int before = 0;
     for (const Kernel& k : kernels) {
-        if (k.rows > 16 && rows <= k.rows / 2) break;
+        if (rows <= before) break;               // the kernel before holds them in one tile
+        before = k.rows;
         const int64_t tiles = (rows + k.rows - 1) / k.rows, slots = n_seq * tiles * Hk, turns = (tokens + k.turn_tokens - 1) / k.turn_tokens;
-        const int most = (int)std::max<int64_t>(std::min<int64_t>(32, 1024 / slots), 1);
+        const int most = slots >= 512 ? 1 : (int)std::min<int64_t>(32, 1024 / slots);
         const size_t part = k.rows * (8 + 4 * (size_t)D);
         // whatever the table covers: the size that a caller asks for does not know it
         if (most > 1) p.ws_bytes = std::max(p.ws_bytes, kCounterBytes + (size_t)slots * most * part);
         for (int z = 1; z <= most && (z == 1 || z <= slices); z += z < 4 ? 1 : (z & (z - 1)) == 0 ? z / 2 : z / 3) {
-            const double us = k.start[d] + (double)((turns + z - 1) / z) * k.turn[d] * (1 + k.crowd[d] * (double)(slots * z) / k.held) +
-                              (z == 1 ? 0 : 1.6 + k.join * 1e-6 * (double)(slots * z) * (double)part);
+            const double x = (double)(slots * z) / k.held, mb = 1e-6 * (double)(slots * z) * (double)part;
+            const double us = k.start[d] + k.each[d] * x + (double)((turns + z - 1) / z) * k.turn[d] * (1 + k.crowd[d] * seen * x) +
+                              (z == 1 ? 0 : k.join[d] + k.join_mb * mb);
             if (us >= best) continue;
             best = us;
             p.rows = k.rows;
