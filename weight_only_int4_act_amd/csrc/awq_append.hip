@@ -1,5 +1,7 @@
 // q|k|v of new tokens: norms of queries and keys per head, rotation, and the append of keys and values to the 8-bit
 // cache.
+#include <type_traits>
+
 #include "awq_cache.h"
 
 namespace awq {
@@ -122,12 +124,15 @@ __device__ __forceinline__ uint2 four_tokens(const uint2& w) {
 }
 
 // The new tokens of one block of the cache for one head of K and V are one workgroup's work, those of the heads of q that
-// read it another `parts` workgroups', or its own (parts = 0) where they are no more heads than a block has of K.  Bound by HBM for many tokens (per number of q 4 bytes, of K and V 3), by the
-// chain of dependent reads for few (lengths, blocks, rows).  The numbers of K (float32, normed and rotated) and V (bf16)
-// stay in registers until the block's largest are known.  V's codes go through LDS into their order: sixteen tokens of
-// a number in one store where all of them are new, else bytes.
-template <int D, int T>
-__global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, Cache c, int per_seq, int parts) {
+// read it another `parts` workgroups', or its own (OWN) where they are no more heads than a block has of K.  Bound by HBM for
+// many tokens (per number of q 4 bytes, of K and V 3), by the chain of dependent reads for few (lengths, blocks, rows).
+// Two kernels rather than one with both ways: its registers left half the wavefronts (12000 tokens of 64 heads on 8
+// 160 us, now 109).  The numbers of K (float32, normed and rotated) and V (bf16) stay in registers until the block's
+// largest are known.  V's codes go through LDS into their order: sixteen tokens of a number in one store where all of
+// them are new, else bytes.
+template <int D, int T, bool OWN>
+__global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, Cache c, int per_seq, int most_parts) {
+    const int parts = OWN ? 0 : most_parts;
     using H = Head<D>;
     constexpr int L = H::L, W = 256 / L, U = (T + W - 1) / W;   // lanes of a head, heads at a time, rounds of a block
     __shared__ uint32_t tops[4][2];
@@ -184,13 +189,15 @@ __global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, C
             *(u32x4*)(a.q + (int64_t)(row0 + q.tok) * a.Hq * D + q.col) =
                 u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
     };
-    if (part < parts) {                          // the tokens' G heads, two at a time
-        for (int i0 = part * 2 * W; i0 < items; i0 += 2 * W * parts) {
-            Item x, y;
-            q_load(i0 + w, x);
-            q_load(i0 + W + w, y);
-            q_do(x);
-            q_do(y);
+    if (part < parts) {                          // the tokens' G heads, four at a time
+        for (int i0 = part * 4 * W; i0 < items; i0 += 4 * W * parts) {
+            Item x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i0 + e * W < items) q_load(i0 + e * W + w, x[e]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i0 + e * W < items) q_do(x[e]);
         }
         return;
     }
@@ -203,7 +210,7 @@ __global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, C
     Item qr[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-        if (parts == 0 && u * W < items) q_load(u * W + w, qr[u]);
+        if (OWN && u * W < items) q_load(u * W + w, qr[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int i = min(max(u * W + w - slot0, 0), n - 1);
@@ -214,7 +221,7 @@ __global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, C
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-        if (parts == 0 && u * W < items) q_do(qr[u]);
+        if (OWN && u * W < items) q_do(qr[u]);
     if (!stored) return;                         // the whole workgroup
     const uint32_t before = *(const uint16_t*)(c.scales + at * 2);
 
@@ -295,20 +302,17 @@ hipError_t launch_qkv_append(const AppendArgs& a, const Sequences& s, const Cach
         kernel<<<grid, 256, 0, st>>>(a, s, c, (int)per_seq, parts);
         return hipGetLastError();
     };
-    if (c.D == 128) {
+    const auto blocks = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        const auto own = [&](auto with, auto without) { return parts ? go(without) : go(with); };
         switch (c.T) {
-            case 16: return go(k_qkv_append<128, 16>);
-            case 32: return go(k_qkv_append<128, 32>);
-            case 64: return go(k_qkv_append<128, 64>);
-            default: return go(k_qkv_append<128, 128>);
+            case 16: return own(k_qkv_append<D, 16, true>, k_qkv_append<D, 16, false>);
+            case 32: return own(k_qkv_append<D, 32, true>, k_qkv_append<D, 32, false>);
+            case 64: return own(k_qkv_append<D, 64, true>, k_qkv_append<D, 64, false>);
+            default: return own(k_qkv_append<D, 128, true>, k_qkv_append<D, 128, false>);
         }
-    }
-    switch (c.T) {
-        case 16: return go(k_qkv_append<64, 16>);
-        case 32: return go(k_qkv_append<64, 32>);
-        case 64: return go(k_qkv_append<64, 64>);
-        default: return go(k_qkv_append<64, 128>);
-    }
+    };
+    return c.D == 128 ? blocks(std::integral_constant<int, 128>{}) : blocks(std::integral_constant<int, 64>{});
 }
 
 }  // namespace awq

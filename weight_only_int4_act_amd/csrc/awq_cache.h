@@ -43,15 +43,17 @@ struct AppendArgs {
     double eps;
 };
 // The blocks that max_q tokens touch at most, wherever the first lies, and the workgroups that share the heads of q of one of
-// them and one head of K and V: up to four rounds of heads each.  None, where these are no more heads than a block
-// has of K and there are workgroups enough for several per CU: K's and V's take them along (6100 tokens of 40 heads,
-// each with its own K, T = 16: 97 us, with a workgroup of their own 120; one token of 64 such sequences 14.5 and 17.8; but
-// one token of one sequence of 64 and 8 heads 6.2 and 5.0, and 4096 of its tokens, T = 64: 76 and, by eight, 49).
+// them and one head of K and V: up to four rounds of heads each, or eight where there are thousands of workgroups and K's
+// and V's have as much to do (4096 tokens of 64 heads on 8, T = 64: 49.0 and 46.4 us, 12000, T = 128: 116 and 109; but 3
+// sequences of 40 7.2 and 9.7, and 18000 of 32 heads on 8, T = 32: 66 and 74).  None, where these are no more heads than a block has of K and there are workgroups enough for several per
+// CU: K's and V's take them along (6100 tokens of 40 heads, each with its own K, T = 16: 97 us, with a workgroup of their own
+// 120; one token of 64 such sequences 14.5 and 17.8; but one token of one sequence of 64 and 8 heads 6.2 and 5.0).
 inline int64_t append_per_seq(int max_q, int T) { return ((int64_t)max_q + T - 2) / T + 1; }
 inline int append_parts(int n_seq, int max_q, int G, int Hk, int T, int D) {
-    const int64_t heads = (int64_t)(max_q < T ? max_q : T) * G, round = 256 / (D / 8);
-    if (heads <= T && n_seq * append_per_seq(max_q, T) >= 1024 / Hk) return 0;
-    return (int)((heads + 4 * round - 1) / (4 * round));
+    const int64_t heads = (int64_t)(max_q < T ? max_q : T) * G, round = 256 / (D / 8), blocks = n_seq * append_per_seq(max_q, T);
+    if (heads <= T && blocks >= 1024 / Hk) return 0;
+    const int64_t parts = (heads + 4 * round - 1) / (4 * round);
+    return (int)(T >= 64 && blocks * Hk * parts > 4096 ? (parts + 1) / 2 : parts);
 }
 hipError_t launch_qkv_append(const AppendArgs& a, const Sequences& s, const Cache& c, hipStream_t st);
 
