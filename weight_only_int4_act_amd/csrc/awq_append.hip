@@ -129,7 +129,8 @@ __device__ __forceinline__ uint2 four_tokens(const uint2& w) {
 // Two kernels rather than one with both ways: its registers left half the wavefronts (12000 tokens of 64 heads on 8
 // 160 us, now 109).  The numbers of K (float32, normed and rotated) and V (bf16) stay in registers until the block's
 // largest are known.  V's codes go through LDS into their order: sixteen tokens of a number in one store where all of
-// them are new, else bytes.
+// them are new, else bytes.  6100 tokens of 40 heads, T = 16: 89 us (3.9 TB/s); one token of 64 sequences, 64 heads on 8, with
+// norms: 6.8 us, of which the launch takes 2.2 and three trips to memory one after the other the rest.
 template <int D, int T, bool OWN>
 __global__ __launch_bounds__(256) void k_qkv_append(AppendArgs a, Sequences s, Cache c, int per_seq, int most_parts) {
     const int parts = OWN ? 0 : most_parts;

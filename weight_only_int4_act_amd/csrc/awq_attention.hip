@@ -81,6 +81,9 @@ struct TileRows {
 // K and V become bf16 in registers (exact); p goes into the second product as two bf16 numbers, whose cost the loads
 // hide.  The running maximum and sum are per row; every wavefront has its own,
 // joined in LDS at the end, and those of several slices by k_attention_join_rows.
+// 64 sequences of up to 8192 tokens, 64 heads on 8, D = 128 (554 MB): 114-134 us by the boxes' memory (4.1-4.8 TB/s, a copy 4.75); one
+// of 4097 tokens 7.8 us and 2.9 for the join: lengths, blocks, codes, the join in LDS and the partials are trips to memory
+// one after the other, on 128 workgroups.
 template <int D>
 __global__ __launch_bounds__(256) void k_attention_rows(Args a, Sequences s, Cache c) {
     constexpr int ND = D / 16, NH = D / 64;
@@ -320,6 +323,15 @@ __global__ __launch_bounds__(64) void k_attention_join_rows(Args a, Sequences s,
 // than 2^8 (any reference gives the same quotient, and p up to 2^8 loses nothing), so that the sums are seldom rescaled.
 // LDS rows (K: a token, V: a number of the head) keep 16-byte piece q at slot q ^ (row % 16) where a row is 256 bytes, at
 // q ^ (row / 2 % 8) where it is 128: lanes that a read serves together hit different banks.
+// 256 rows by eight wavefronts and 128 tokens at a time halve what is widened and stored for each product: the faster
+// one where there are rows enough (the plan below).
+//
+// 4096 tokens behind 4096, 64 heads on 8, D = 128: 740-790 us (1.05-1.11 PFLOP/s; a large bf16 product reaches 1.38); 32 heads, D = 64:
+// 250 and 262 with 256 and 128 rows (.8).  Matrix cores busy in 48 % of the cycles, vector units in about as many: a product on
+// one wavefront of a SIMD slows another's additions to two thirds (measured alone), so that exponentials, maxima,
+// roundings and widening are not hidden behind it but added.  On one card, 751 us without the products, 713 without
+// loads and widening, 530 without the softmax, in a form with the wavefronts' phases set against each other (itself
+// 970; the one kept lets the hardware choose).
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ floatx16 mfma32x32x16(const bf16x8& a, const bf16x8& b, const floatx16& c) {
