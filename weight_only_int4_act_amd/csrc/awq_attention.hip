@@ -524,11 +524,17 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
                         if (!(first + at < seen && groups >> (2 * u + r / 8) & 1)) p[u][r] = -INFINITY;
                     }
             }
-            // (a maximum that hands on NaN, which makes the row NaN anyway: one instruction for two numbers)
-            float top = __builtin_elementwise_maximum(p[0][0], p[1][0]);
+            // (a maximum that hands on NaN, which makes the row NaN anyway: one instruction for two numbers, in two chains:
+            // pairs first would be half as many instructions again)
+            float tops[2] = {p[0][0], p[1][0]};
 #pragma unroll
-            for (int r = 1; r < 16; ++r)
-                top = __builtin_elementwise_maximum(top, __builtin_elementwise_maximum(p[0][r], p[1][r]));
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int r = 1; r < 15; r += 2) {
+                    tops[u] = __builtin_elementwise_maximum(__builtin_elementwise_maximum(tops[u], p[u][r]), p[u][r + 1]);
+                }
+            }
+            float top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(tops[0], p[0][15]), __builtin_elementwise_maximum(tops[1], p[1][15]));
             const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
             top = __builtin_elementwise_maximum(__uint_as_float(both[0]), __uint_as_float(both[1])) * f;
             const bool passed = top > m + 8.f;   // the first numbers are, beside minus infinity
