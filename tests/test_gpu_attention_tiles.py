@@ -108,3 +108,25 @@ def test_a_row_does_not_depend_on_the_numbers_of_others(n):
         got = attend(B, q)
         got[1, 3:6], got[n - 1, 20] = clean[1, 3:6], clean[n - 1, 20]
         assert torch.equal(got, clean), size
+
+
+@pytest.mark.parametrize("lengths", [[(130, 1), (1, 1)], [(100, 20), (40, 3)], [(292, 85), (60, 60)], [(500, 300), (3, 2)]])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_table_much_wider_than_the_sequences(lengths, D):
+    """The width chooses the kernel and the slices; columns behind the last token are not looked at."""
+    B = Batch(lengths, 8, 2, D, 32, 7)
+    n, width = B.table.shape
+    rest = B.rng.integers(-5, B.blocks + 5, (n, 1000)).astype(np.int32)
+    rest[:, ::7] = np.iinfo(np.int32).max
+    B.table = np.concatenate((B.table, rest), 1)
+    for b, (L, _) in enumerate(lengths):
+        B.table[b, -(-L // 32):width] = rest[b, 0]
+    B.upload()
+    q = dev(B.queries())
+    for causal in (True, False):
+        check_attention(B, q, attend(B, q, causal), causal, label=(lengths, D, causal))
+
+
+@pytest.mark.parametrize("n", [1, 60])
+def test_many_short_sequences_and_one_long(n):
+    run([(9000, n)] + [(L, min(L, n)) for L in range(1, 60)], 8, 2, 128, 16, 8)
