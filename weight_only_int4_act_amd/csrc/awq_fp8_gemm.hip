@@ -456,53 +456,64 @@ constexpr size_t kCounterBytes = 65536;
 constexpr int kCus = kNumXcd * kCusPerXcd;
 constexpr int kMaxSlices = 16;
 
-// Which kernel, and how many slices of K, by the time that each would take: us on this card, fitted to launches on weights that
-// no cache holds (K = 1024 .. 28672, N = 1024 .. 28672):
-//   register kernel: one workgroup per CU once K is cut, with a group of channels or more for every wavefront (1 x 8192 x 1024,
-//     1, 2, 4, 8 slices: 12.9, 9.9, 7.5, 6.6 us; 1 x 1024 x 8192, 1 and 2: 5.1, 6.0; 1 x 28672 x 8192, 1, 2, 4: 54.8, 41.8,
-//     42.1); for 33 to 64 rows 4.5 + .25 + .0047 M for each group of channels that a CU takes;
-//   tiles of 64 wm rows: 2.5 + turns * turn_us for each round of one workgroup per CU, where a turn takes the longer the more
-//     CUs have one (2 x 128 rows: .83 us with half of the CUs, 1.0 with all), and for joining slices 3 + .35 per MB of
-//     partials; not less than the weights' bytes at 4.6 TB/s.  257 x 5120 x 13824: 37 us with 128 rows a tile, 68 with 64, 62 with 256;
-//     2048 x 8192 x 8192: 120 us with 256 rows, 132 with 128; 512 x 8192 x 8192, 128 rows, 1, 2, 4 slices: 60, 51, 61; 64 x 8192
-//     x 28672: 53 us by tiles, 69 by the register kernel, 48 x 8192 x 8192 22 and 20.
+// Which kernel, and how many slices of K, by the time that each would take: us on this card, fitted to 5200 launches of 33 .. 3000
+// rows (K = 128 .. 28672, N = 64 .. 28672):
+//   register kernel, 64 rows of 64 columns a workgroup: 4.3 + 1.25 x + steps * 1.44 (1 + 1.8 x rows / 64), where x is the
+//     workgroups over 512 and a step a group of channels for each of four wavefronts; for slices 1.7 + .11 for each of them +
+//     .17 per MB of partials; not less than the weights' bytes at 3.4 TB/s;
+//   tiles of 64 wm rows: start + each * x + turns * turn for each round of one workgroup per CU (crowd more, where every CU
+//     has one; x: workgroups over 256), for joining slices join + per MB of partials; not less than the weights' bytes at 4.6.
+// What this takes is in the mean 1.3 % slower than the best of all.  92 x 2176 x 4952: 11.5 us by the register kernel, 17.9 by tiles;
+// 435 x 800 x 136 6.6 and 10.0; 643 x 7312 x 1104 35.5 and 25.0; 64 x 8192 x 28672 69 and 53; 257 x 5120 x 13824: 37 us with 128 rows a tile,
+// 68 with 64, 62 with 256; 2048 x 8192 x 8192: 120 us with 256 rows, 132 with 128; 512 x 8192 x 8192, 128 rows, 1, 2, 4
+// slices: 60, 51, 61.
+// Up to 32 rows the register kernel alone, cut where that leaves one workgroup per CU, with a group of channels or more
+// for every wavefront (1 x 8192 x 1024, 1, 2, 4, 8 slices: 12.9, 9.9, 7.5, 6.6 us; 1 x 1024 x 8192, 1 and 2: 5.1, 6.0; 1 x
+// 28672 x 8192, 1, 2, 4: 54.8, 41.8, 42.1).
 Fp8GemmPlan plan_fp8_gemm(int64_t M, int64_t K, int64_t N) {
     Fp8GemmPlan p{};                             // wm = 0: the register kernel
-    const int64_t chunks = fp8_kc(K);
-    double best = 1e30;
-    if (M <= 64) {
-        p.col_tiles = fp8_nt(N);
-        p.row_tiles = 1;
-        const int rf = M <= 16 ? 1 : M <= 32 ? 2 : 4, least = rf == 1 ? 8 : 4;   // wavefronts: groups of channels per slice
-        p.nz = 1;
-        if (p.col_tiles <= (int64_t)(kCounterBytes / 4))
-            while (p.nz < kMaxSlices && p.col_tiles * p.nz * 2 <= kCus && chunks >= p.nz * 2 * least) p.nz *= 2;
-        p.cstride = (int)std::max<int64_t>(1, std::min<int64_t>(32, kCounterBytes / 4 / p.col_tiles));
-        p.ws_bytes = p.nz > 1 ? kCounterBytes + (size_t)p.col_tiles * p.nz * rf * 4096 : 0;
-        if (M <= 32) return p;
-        const double per_cu = std::max((double)((chunks + p.nz - 1) / p.nz), (double)(p.col_tiles * chunks) / kCus);
-        best = 4.5 + per_cu * (.25 + .0047 * (double)M);
+    const int64_t chunks = fp8_kc(K), slots = fp8_nt(N) * ((M + 63) / 64);
+    const int rf = M <= 16 ? 1 : M <= 32 ? 2 : 4, least = rf == 1 ? 8 : rf == 2 ? 4 : 2;   // groups of channels per slice
+    const double bytes = (double)fp8_codes_bytes(K, N), row_part = M < 64 ? (double)M / 64 : 1.;
+    double best = 1e300;
+    for (int nz = 1; nz <= kMaxSlices; nz *= 2) {
+        if (nz > 1 && (slots * nz > kCus || chunks < nz * least)) break;
+        const double x = (double)(slots * nz) / 512, steps = (double)((chunks + 4 * nz - 1) / (4 * nz));
+        const double total = 4.3 + 1.25 * x + steps * 1.44 * (1 + 1.8 * x * row_part) +
+                             (nz == 1 ? 0 : 1.7 + .11 * nz + .17e-6 * (double)(slots * nz * 16384));
+        const double us = rf < 4 ? -nz : std::max(2 + bytes / 3.4e6, total) + .02 * total;
+        if (us >= best) continue;
+        best = us;
+        p.nz = nz;
     }
-    static const double turn_us[3] = {.45, .65, 1.3}, crowd_us[3] = {.41, .35, .5};
-    const double stream = 2 + (double)fp8_codes_bytes(K, N) / 4.6e6;
+    p.col_tiles = fp8_nt(N);
+    p.row_tiles = (M + 63) / 64;
+    p.cstride = (int)std::max<int64_t>(1, std::min<int64_t>(32, kCounterBytes / 4 / slots));
+    p.ws_bytes = p.nz > 1 ? kCounterBytes + (size_t)slots * p.nz * rf * 4096 : 0;
+    if (rf < 4) return p;
+    struct Tile {
+        double start, each, turn, crowd, join, join_mb;
+    };
+    static const Tile tiles[3] = {{5.3, 3.4, .75, .04, 2., .31}, {5.9, 5.2, .66, .13, 2.1, .31}, {6.7, 8.9, 1.15, .24, 2.8, .23}};
     for (int k = 0; k < 3; ++k) {
+        const Tile& t = tiles[k];
         const int wm = 1 << k;
-        const int64_t rt = (M + 64 * wm - 1) / (64 * wm), ct = (N + 255) / 256, tiles = rt * ct;
+        const int64_t rt = (M + 64 * wm - 1) / (64 * wm), ct = (N + 255) / 256;
         for (int nz = 1; nz <= kMaxSlices; ++nz) {
-            const int64_t turns = (chunks + nz - 1) / nz, groups = tiles * nz, full = groups / kCus, rest = groups % kCus;
-            if (nz > 1 && (turns < 4 || groups > kCus)) break;
-            const double rounds = (double)full * (turn_us[k] + crowd_us[k]) +
-                                  (rest ? turn_us[k] + crowd_us[k] * (double)rest / kCus : 0);
-            const double total = 2.5 + (double)turns * rounds +
-                                 (nz == 1 ? 0 : 3 + .35e-6 * (double)(groups * 64 * wm * 256 * 4));
-            const double us = std::max(stream, total) + .1 * total;
+            const int64_t turns = (chunks + nz - 1) / nz, groups = rt * ct * nz, full = groups / kCus, rest = groups % kCus;
+            if (nz > 1 && (turns < 2 || groups > kCus)) break;
+            const double rounds = (double)full * (t.turn + t.crowd) + (rest ? t.turn + t.crowd * (double)rest / kCus : 0);
+            const size_t part = (size_t)groups * 64 * wm * 256 * 4;
+            const double total = t.start + t.each * (double)groups / kCus + (double)turns * rounds +
+                                 (nz == 1 ? 0 : t.join + t.join_mb * 1e-6 * (double)part);
+            const double us = std::max(2 + bytes / 4.6e6, total) + .02 * total;
             if (us >= best) continue;
             best = us;
             p.wm = wm;
             p.row_tiles = rt;
             p.col_tiles = ct;
             p.nz = nz;
-            p.ws_bytes = nz > 1 ? kCounterBytes + (size_t)groups * 64 * wm * 256 * 4 : 0;
+            p.ws_bytes = nz > 1 ? kCounterBytes + part : 0;
         }
     }
     return p;
