@@ -22,14 +22,15 @@ __device__ __forceinline__ i32x8 join8(const u32x4& a, const u32x4& b) {
     return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
-// ---------------------------------------------------------------- few rows: weights streamed once
-// Bound by the weights' bytes.  A workgroup owns 64 columns (one tile of packed weights, contiguous in memory), up to
-// 16 RF rows and a slice of K; its NW wavefronts take every NW-th group of channels, one in flight each, in registers: 8 KB
-// of codes by non-temporal loads, and the rows' elements and scales (repeated reads that the caches serve).  A load past
-// the slice, past K or past the last row lies outside its buffer resource: it brings zeros and costs no
-// traffic.  The wavefronts' sums meet in LDS in a fixed order; with several slices the last workgroup to arrive
-// adds the float32 partials in slice order.  1 x 8192 x 10240, from HBM: 19.0 us (4.4 TB/s), 1 x 28672 x 8192 41.8 (5.6, a
-// part from the Infinity Cache); two groups in flight per wavefront are no faster.
+// ---------------------------------------------------------------- few rows or little work: operands in registers
+// Bound by the weights' bytes up to 32 rows, by latency beyond.  A workgroup owns 64 columns (one tile of packed weights,
+// contiguous in memory), up to 16 RF rows and a slice of K; its NW wavefronts take every NW-th group of channels, one in
+// flight each, in registers: 8 KB of codes (by non-temporal loads where they are read once), and the rows' elements and
+// scales (repeated reads that the caches serve).  A load past the slice, past K or past the last row lies outside its
+// buffer resource: it brings zeros and costs no traffic.  The wavefronts' sums meet in LDS in a fixed order; with several
+// slices the last workgroup to arrive adds the float32 partials in slice order.  1 x 8192 x 10240, from HBM: 19.0 us (4.4
+// TB/s), 1 x 28672 x 8192 41.8 (5.6, a part from the Infinity Cache); two groups in flight per wavefront are no faster.
+// 435 x 800 x 136: 5.9 us, where a launch takes 2.2; 420 x 2256 x 568: 10.5, 11.4 with non-temporal loads.
 template <int RF, int NW>
 __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_rows(
     const uint8_t* __restrict__ xcodes, const float* __restrict__ xscales, int64_t M,
@@ -50,6 +51,7 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_rows(
     const __amdgpu_buffer_rsrc_t xr = rsrc(xcodes + m0 * K, (int64_t)rows * xrow);
     const __amdgpu_buffer_rsrc_t sr = rsrc(xscales + m0 * chunks, (int64_t)rows * chunks * 4);
 
+    constexpr int kPolicy = RF == 4 ? 0 : kCpolStream;           // weights that other row tiles read, too, stay in the caches
     struct Buf {
         u32x4 w[8], x[RF][2];
         float sw, sx[RF];
@@ -73,7 +75,7 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_rows(
         b.sw = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(fr, in ? (uint32_t)c * 4 : kOutside, 0, 0));
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            b.w[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo, j * 1024, kCpolStream));
+            b.w[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo, j * 1024, kPolicy));
     };
     floatx4 acc[RF][4];
 #pragma unroll
@@ -164,7 +166,7 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_rows(
     if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// ---------------------------------------------------------------- rows by the hundred: tiles in LDS
+// ---------------------------------------------------------------- many rows: tiles in LDS
 // 64 WM rows x 256 columns per workgroup, WM x WN wavefronts of 64 rows x 32 CF columns, by 32x32x64 products (half the
 // operand reads of 16x16x128 ones for the same work).  Lane (i, h) = (lane % 32, lane / 32).  First operand: column i
 // of 32 weights; second: row i of 32; both take pieces (16 bytes) 4y + 2h and 4y + 2h + 1 of the group's eight for half y of
