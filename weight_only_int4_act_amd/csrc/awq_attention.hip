@@ -326,7 +326,7 @@ __global__ __launch_bounds__(64) void k_attention_join_rows(Args a, Sequences s,
 // 256 rows by eight wavefronts and 128 tokens at a time halve what is widened and stored for each product: the faster
 // one where there are rows enough (the plan below).
 //
-// 4096 tokens behind 4096, 64 heads on 8, D = 128: 740-790 us (1.05-1.11 PFLOP/s; a large bf16 product reaches 1.38); 32 heads, D = 64:
+// 4096 tokens behind 4096, 64 heads on 8, D = 128: 730-790 us (1.05-1.13 PFLOP/s; a large bf16 product reaches 1.38); 32 heads, D = 64:
 // 250 and 262 with 256 and 128 rows (.8).  Matrix cores busy in 48 % of the cycles, vector units in about as many: a product on
 // one wavefront of a SIMD slows another's additions to two thirds (measured alone), so that exponentials, maxima,
 // roundings and widening are not hidden behind it but added.  On one card, 751 us without the products, 713 without

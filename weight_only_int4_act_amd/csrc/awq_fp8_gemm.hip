@@ -184,7 +184,7 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_gemm_rows(
 // fragment a barrier says that the group is in every wavefront's registers and the next one has landed; its place
 // is then filled with group c + ST.
 //
-// 4096 x 8192 x 28672: 820-890 us by the clock that the card holds (2.2-2.35 PFLOP/s; the matrix cores busy in 64 % of the cycles).
+// 4096 x 8192 x 28672: 809-890 us by the clock that the card holds (2.2-2.4 PFLOP/s; the matrix cores busy in 64 % of the cycles).
 // On one card, 891 us as it is, 843-865 without the float32 additions, 720 without transfers, 647 without both, 813 with
 // transfers that always hit the L2: so what the additions cost (a vector instruction per result and group of 128
 // channels, where a scale per row alone needs none) and what the transfers cost is power as much as issue.
