@@ -183,3 +183,15 @@ def test_binding_checks():
     no("out must", A.awq_attention, q, cu, ln, tab, 2, k, v, e, 0.1, True, q[:2], None)
     no("q must", A.awq_attention, q[..., :32], cu, ln, tab, 2, k, v, e, 0.1, True, q, None)
     no("no head", A.qkv_append, qkv[:, :4 * D], A.Sequences(cu, ln, tab, 2), type("C", (), dict(k=k, v=v, scales=e)))
+
+
+def test_max_q_past_32_bits():
+    """The foreign call would take 2^32 + 1 as 1 and leave rows out."""
+    bf, i32 = torch.bfloat16, torch.int32
+    k, v, e = (torch.zeros(5, 2, *s, dtype=torch.uint8) for s in ((16, 64), (1, 64, 16), (2,)))
+    q, qkv = torch.zeros(4, 4, 64, dtype=bf), torch.zeros(4, 8 * 64, dtype=bf)
+    seqs = torch.zeros(3, dtype=i32), torch.zeros(2, dtype=i32), torch.zeros(2, 3, dtype=i32), (1 << 32) + 1
+    with pytest.raises(ValueError, match="max_q"):
+        A.awq_qkv_append(qkv, None, None, 1e-5, None, False, *seqs, q, k, v, e)
+    with pytest.raises(ValueError, match="max_q"):
+        A.awq_attention(q, *seqs, k, v, e, 0.1, True, q.clone(), None)

@@ -821,8 +821,10 @@ def fp8_gemm(a: Fp8Acts, q: Fp8Weights, stream=None) -> torch.Tensor:
 
 
 # ------------------------------------------------------------------ 8-bit cache and its attention
-def _sequences(fn: str, cu: torch.Tensor, length: torch.Tensor, table: torch.Tensor):
+def _sequences(fn: str, cu: torch.Tensor, length: torch.Tensor, table: torch.Tensor, max_q: int):
     n, width = _matrix(fn, "table", table, torch.int32)
+    if max_q > 0x7fffffff:                          # the foreign call would take its low 32 bits
+        raise ValueError(f"{fn}: max_q = {max_q} is no 32-bit number")
     return (_mx_arg(fn, "cu", cu, torch.int32, (n + 1,)), _mx_arg(fn, "length", length, torch.int32, (n,)),
             table.data_ptr(), n, width)
 
@@ -850,7 +852,7 @@ def awq_qkv_append(qkv: torch.Tensor, q_weight: Optional[torch.Tensor], k_weight
     fn = "awq_qkv_append"
     pk, pv, pe, blocks, Hk, T, D = _cache(fn, k_codes, v_codes, scales)
     M, Hq = _query(fn, "q", q, D)
-    pc, pl, pt, n, width = _sequences(fn, cu, length, table)
+    pc, pl, pt, n, width = _sequences(fn, cu, length, table, max_q)
     px = _mx_arg(fn, "qkv", qkv, torch.bfloat16, (M, (Hq + 2 * Hk) * D))
     pqw = None if q_weight is None else _mx_arg(fn, "q_weight", q_weight, torch.bfloat16, (D,))
     pkw = None if k_weight is None else _mx_arg(fn, "k_weight", k_weight, torch.bfloat16, (D,))
@@ -874,7 +876,7 @@ def awq_attention(q: torch.Tensor, cu: torch.Tensor, length: torch.Tensor, table
     pk, pv, pe, blocks, Hk, T, D = _cache(fn, k_codes, v_codes, scales)
     M, Hq = _query(fn, "q", q, D)
     po = _mx_arg(fn, "out", out, torch.bfloat16, q.shape)
-    pc, pl, pt, n, width = _sequences(fn, cu, length, table)
+    pc, pl, pt, n, width = _sequences(fn, cu, length, table, max_q)
     st = _lib.awq_attention(q.data_ptr(), M, Hq, Hk, D, pc, pl, pt, n, width, max_q, pk, pv, pe, blocks, T, scale,
                             1 if causal else 0, po, None if ws is None else ws.data_ptr(), _nbytes(ws),
                             _mx_stream(fn, stream, q, cu, length, table, k_codes, v_codes, scales, out, ws))
