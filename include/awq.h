@@ -385,8 +385,7 @@ int awq_mx_gemm(const uint8_t* xcodes, const uint8_t* xscales, int32_t bits, int
  * Elements are e4m3 (largest 448).  A group holds one float32 scale s: 128 consecutive channels of one
  * row of activations, or 128 channels x 128 output columns of weights.  Quantizing a group of float32
  * numbers p:
- *   s = max(max|p|, 448 * 2^-120) / 448;  element = p / s rounded to nearest even, where the float32
- *   quotient is off by at most 2 units in its last place.
+ *   s = max(max|p|, 448 * 2^-120) / 448;  element = p / s, the float32 quotient, rounded to nearest even.
  * A group that holds an infinity or a NaN has s = NaN and zero elements: every value it stands for is
  * NaN, and so is every product with it.  The value of an element is element * s.
  *
