@@ -440,17 +440,19 @@ int awq_fp8_gemm(const uint8_t* xcodes, const float* xscales, int64_t M, const u
  *
  * Sequences (device arrays; n_seq of them):
  *   cu      int32 [n_seq + 1]: the new tokens of sequence b are rows cu[b] .. cu[b+1] - 1 of q|k|v, of q and of the
- *           attention's output; not decreasing.  Rows that no sequence has are left as they were.
+ *           attention's output; not decreasing, so that a row has one sequence at most.  Rows that no sequence has are
+ *           left as they were.
  *   length  int32 [n_seq]: the sequence's tokens, the new ones included: the i-th of n new ones has position
  *           length - n + i.
  *   table   int32 [n_seq, width]: tokens T j .. T j + T - 1 of sequence b are in block table[b, j].
  *   max_q   at least the largest number of new tokens of one sequence (a host number; it sizes the launch, which is
  *           refused where it would pass 2^32 threads).
  * The arrays are read on the device and may change between replays of a captured graph.  Values that fit
- * nothing are taken as follows, without a fault: a cu below the one before it or past the rows: as that bound; a
- * block outside [0, blocks) or past the table's width: its tokens are neither stored nor seen; a token at a
- * negative position (length below the new tokens): not stored, its q and its output are zero; rows past
- * max_q: left out.
+ * nothing are taken as follows, without a fault: a cu below zero or past the rows: as that bound; a cu[b+1] below
+ * cu[b]: sequence b has no rows (but where counts decrease, a later sequence may then have rows of an earlier one:
+ * each stores its own tokens, and which of the two leaves q and the output of such a row is not determined); a block
+ * outside [0, blocks) or past the table's width: its tokens are neither stored nor seen; a token at a negative
+ * position (length below the new tokens): not stored, its q and its output are zero; rows past max_q: left out.
  */
 
 /* q|k|v of new tokens: q and k normed per head and rotated, q out in bf16, k and v into the cache.

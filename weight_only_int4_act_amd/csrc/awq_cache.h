@@ -18,7 +18,9 @@ struct Sequences {
     int n, width, max_q;
 };
 
-// The new tokens of a sequence: rows row0 .. row0 + count - 1, at positions start, start + 1, ...
+// The new tokens of a sequence: rows row0 .. row0 + count - 1, at positions start, start + 1, ...  In bounds whatever the
+// arrays hold.  Counts that decrease may give a row to two sequences: looking through the counts before one's own would tell,
+// but cost every call (one token behind 4096: 10.3 -> 10.7 us; 4096 sequences of 200: 167 -> 209).
 struct NewTokens {
     int row0, count, start, length;
 };
