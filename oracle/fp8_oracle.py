@@ -109,7 +109,8 @@ def rotate(x: np.ndarray, turn, R: int, interleaved: bool):
 
 def attention(q, k, v, causal: bool, scale: float):
     """One head of one sequence, float64: q [n, D] at the last n positions of k, v [L, D] (None where a token is
-    missing: seen by nobody).  Returns (out, sum p |v| / sum p, the largest |q| . |k| * scale)."""
+    missing: seen by nobody; a query at a position below zero sees none).  Returns (out, sum p |v| / sum p, the largest
+    |q| . |k| * scale)."""
     n, D = q.shape
     L = k.shape[0]
     pos = np.arange(L - n, L)
@@ -119,7 +120,7 @@ def attention(q, k, v, causal: bool, scale: float):
     kk = np.nan_to_num(k, nan=0.0)
     vv = np.nan_to_num(v, nan=0.0)
     s = np.where(seen, q @ kk.T * scale, -np.inf)
-    any_ = seen.any(1) & (pos >= 0 if causal else True)
+    any_ = seen.any(1) & (pos >= 0)
     m = np.where(any_, s.max(1, initial=-np.inf), 0.0)
     p = np.where(any_[:, None], np.exp(s - m[:, None]), 0.0)
     total = np.where(any_, p.sum(1), 1.0)

@@ -61,9 +61,11 @@ struct TileRows {
         tiles = (most + TOKENS - 1) / TOKENS;
         used = max(min(a.split, (most + kSliceTokens - 1) / kSliceTokens), 1);
     }
-    // tokens that a row sees (of one past the last: what the last sees), and where its numbers are
+    // tokens that a row sees (of one past the last: what the last sees; never fewer than a row before it; none from a
+    // position below zero), and where its numbers are
     __device__ __forceinline__ int reach(int row, const Args& a) const {
-        return min(a.causal ? max(start + max(min(row, rows - 1), 0) / G + 1, 0) : length, cap);
+        const int upto = start + max(min(row, rows - 1), 0) / G + 1;
+        return upto <= 0 ? 0 : min(a.causal ? upto : length, cap);
     }
     __device__ __forceinline__ int64_t at(int row, int head, const Args& a, int D) const {
         const int r = max(min(row, rows - 1), 0);
