@@ -431,7 +431,8 @@ int awq_fp8_gemm(const uint8_t* xcodes, const float* xscales, int64_t M, const u
  * The cache holds K and V of `blocks` blocks of T tokens for Hk heads of D numbers, in e4m3, with one
  * power-of-two scale each for K and V per block and head: a byte E stands for 2^(E - 127), the least E >= 0 under which
  * the block's largest number is at most 448.  E = 255 marks a block (of one head) that an infinity or a NaN has
- * been appended to, as K or as V: attention gives NaN to every query that sees one of its tokens.
+ * been appended to, as K or as V: attention gives NaN to every query that sees one of its tokens.  A number of 1.9375 * 2^127
+ * or more, which would round to 2^128, counts as an infinity.
  *   k_codes  uint8 [blocks, Hk, T, D]
  *   v_codes  uint8 [blocks, Hk, T/16, D, 16]: the 16 tokens of a group side by side (the order of the
  *            second product's operand)
@@ -479,7 +480,8 @@ int awq_qkv_append(const void* qkv_bf16, int64_t M, int32_t Hq, int32_t Hk, int3
 /* Attention over the cache: with head j of q reading head j / (Hq/Hk) of the cache, for every new token
  *   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q . k_t),
  * over the tokens of its sequence up to its own position (causal = 1) or all of them (causal = 0); zero where it sees
- * none, or none but with scores of minus infinity.  Sums and exponents in float32, K and V exact.  For the second
+ * none, or none but with scores of minus infinity.  Sums and exponents in float32; K and V exact, but for multiples of less than
+ * 2^-133 (E < 3), which count as the nearest multiple of that.  For the second
  * product p_t is one bf16 number (half a step, 2^-8 at most, of the output's own rounding's size), or two where
  * few rows make the kernel that streams the cache the faster one.  A row's result does not depend on the numbers
  * of other rows.

@@ -62,8 +62,8 @@ def weights_codes(packed: np.ndarray, K: int, N: int) -> np.ndarray:
 
 # ---------------------------------------------------------------- cache
 def cache_byte(top: float) -> int:
-    """The least E >= 0 with top <= 448 * 2^(E - 127); 255 for what is not finite."""
-    if not np.isfinite(top):
+    """The least E >= 0 with top <= 448 * 2^(E - 127); 255 for what is not finite or would round to 2^128 under it."""
+    if not top < 1.9375 * 2.0 ** 127:
         return 255
     E = 0
     if top > 0:

@@ -17,7 +17,8 @@ constexpr int kTile = 64;                        // tokens that a wavefront take
 constexpr int kSliceTokens = 256;                // least tokens of a slice
 constexpr size_t kCounterBytes = 65536;          // left alone: the products' arrival counters, in a workspace that they share
 
-// Eight e4m3 codes (two words) times 2^(E - 127), the scale's exponent field, in bf16: exact.
+// Eight e4m3 codes (two words) times 2^(E - 127), the scale's exponent field, in bf16: exact, but for E < 3, whose smallest
+// numbers lie below bf16's least step, 2^-133.
 __device__ __forceinline__ bf16x8 widen_codes(uint32_t a, uint32_t b, float scale) {
     const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false);
     const bf16x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, true);
