@@ -821,9 +821,13 @@ def fp8_gemm(a: Fp8Acts, q: Fp8Weights, stream=None) -> torch.Tensor:
 
 
 # ------------------------------------------------------------------ 8-bit cache and its attention
+def _int32(v: int) -> bool:
+    return -0x80000000 <= v <= 0x7fffffff
+
+
 def _sequences(fn: str, cu: torch.Tensor, length: torch.Tensor, table: torch.Tensor, max_q: int):
     n, width = _matrix(fn, "table", table, torch.int32)
-    if max_q > 0x7fffffff:                          # the foreign call would take its low 32 bits
+    if not _int32(max_q):                           # the foreign call would take its low 32 bits
         raise ValueError(f"{fn}: max_q = {max_q} is no 32-bit number")
     return (_mx_arg(fn, "cu", cu, torch.int32, (n + 1,)), _mx_arg(fn, "length", length, torch.int32, (n,)),
             table.data_ptr(), n, width)
@@ -866,6 +870,8 @@ def awq_qkv_append(qkv: torch.Tensor, q_weight: Optional[torch.Tensor], k_weight
 
 
 def awq_attention_workspace_size(M: int, n_seq: int, max_q: int, Hq: int, Hk: int, D: int) -> int:
+    if not all(_int32(v) for v in (n_seq, max_q, Hq, Hk, D)):
+        return 0
     return int(_lib.awq_attention_workspace_size(M, n_seq, max_q, Hq, Hk, D))
 
 
