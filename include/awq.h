@@ -485,7 +485,9 @@ int awq_qkv_append(const void* qkv_bf16, int64_t M, int32_t Hq, int32_t Hk, int3
  * product p_t is one bf16 number (half a step, 2^-8 at most, of the output's own rounding's size), or two where
  * few rows make the kernel that streams the cache the faster one.  A row's result does not depend on the numbers
  * of other rows.
- *   q, out  bf16 [M, Hq, D], M at most 2^31 / ((Hq + 2 Hk) D);  scale  finite (often 1/sqrt(D)).
+ * A score (scale log2 e q . k) within float32's range is right if the numbers of q are below 2^100 in magnitude; sums of p_t v_t, p_t
+ * up to 2^8 times the largest, past that range are infinite.
+ *   q, out  bf16 [M, Hq, D], M at most 2^31 / ((Hq + 2 Hk) D);  scale  finite, as is scale * log2 e (often 1/sqrt(D)).
  *   workspace >= awq_attention_workspace_size(M, n_seq, max_q, Hq, Hk, D) bytes (the size may be 0), 256-byte
  *   aligned; what it holds before a call does not matter, and its first 64 KiB are not touched: one workspace
  *   serves any sequence of calls of this and of the products, ordered by the caller, replays of captured graphs

@@ -12,7 +12,6 @@ namespace awq {
 namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kTile = 64;                        // tokens that a wavefront takes at a time
 constexpr int kSliceTokens = 256;                // least tokens of a slice
 constexpr size_t kCounterBytes = 65536;          // left alone: the products' arrival counters, in a workspace that they share
@@ -155,8 +154,9 @@ __global__ __launch_bounds__(256) void k_attention_rows(Args a, Sequences s, Cac
         const bool more = first + 4 * kTile < end;
         const int bk2 = block_of(first + 8 * kTile + 16 * kg), bv2 = block_of(first + 8 * kTile + 16 * g);
         const bool poisoned = (e & 255) == 255 || e >> 8 == 255;
-        // a marked block makes what is seen of it NaN; V's own scale then is any finite one
-        const float f = poisoned ? NAN : __uint_as_float((e & 255) == 0 ? 0x00400000u : (e & 255) << 23) * a.scale;
+        // a marked block makes what is seen of it NaN; V's own scale then is any finite one.  (K's times a.scale may pass
+        // float32's range where no score does: the two are applied one after the other.)
+        const float f = poisoned ? NAN : __uint_as_float((e & 255) == 0 ? 0x00400000u : (e & 255) << 23);
         const float fv = __uint_as_float(poisoned ? 127u << 23 : (e >> 8) << 23);
 
         floatx4 p[4];
@@ -181,7 +181,7 @@ __global__ __launch_bounds__(256) void k_attention_rows(Args a, Sequences s, Cac
         for (int u = 0; u < 4; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                p[u][r] = 4 * u + r < limit ? p[u][r] * f : -INFINITY;
+                p[u][r] = 4 * u + r < limit ? p[u][r] * f * a.scale : -INFINITY;
                 top = fmaxf(top, p[u][r]);
             }
         const float next = fmaxf(m, max_g(top));

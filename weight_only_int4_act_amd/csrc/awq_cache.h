@@ -59,6 +59,7 @@ inline int append_parts(int n_seq, int max_q, int G, int Hk, int T, int D) {
 }
 hipError_t launch_qkv_append(const AppendArgs& a, const Sequences& s, const Cache& c, hipStream_t st);
 
+constexpr float kLog2e = 1.44269504088896340736f;
 struct AttentionPlan {
     int split;                   // most slices of a sequence's tokens
     int rows;                    // rows per workgroup, which says which kernel: 16, 128 or 256

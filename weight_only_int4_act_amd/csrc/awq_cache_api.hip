@@ -97,7 +97,7 @@ int awq_attention(const void* q_bf16, int64_t M, int32_t Hq, int32_t Hk, int32_t
     if ((D != 64 && D != 128) || log2_of(T) < 0) return AWQ_ERR_UNSUPPORTED;
     if (!sequences_ok(cu, length, table, n_seq, width, max_q, T) || !cache_ok(k_codes, v_codes, scales, blocks, Hk, T, D))
         return AWQ_ERR_INVALID_ARG;
-    if (!std::isfinite(scale) || (causal != 0 && causal != 1)) return AWQ_ERR_INVALID_ARG;
+    if (!std::isfinite(scale * awq::kLog2e) || (causal != 0 && causal != 1)) return AWQ_ERR_INVALID_ARG;
     if (!aligned(q_bf16, 16) || !aligned(out_bf16, 16)) return AWQ_ERR_INVALID_ARG;
     const awq::AttentionPlan p = awq::plan_attention(M, n_seq, max_q, Hq, Hk, D, (int64_t)width * T);
     if ((int64_t)n_seq * p.tiles > kThreadsMax / awq::attention_threads(p) / ((int64_t)p.split * Hk)) return AWQ_ERR_INVALID_ARG;
