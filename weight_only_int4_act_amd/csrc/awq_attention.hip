@@ -495,6 +495,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
     for (int tile = tb; tile < te; ++tile) {
         const int stage = (tile - tb) & 1, base_token = tile * kTokens;
         const uint32_t there = holes;
+        if constexpr (kLdsPoison) {              // the other stage, between its last reader and its next writer
+            for (int e = threadIdx.x; e < kStage / 16; e += 64 * NW) lds[(stage ^ 1) * (kStage / 16) + e] = lds_nan16();
+            __syncthreads();
+        }
         blk = next;
         next = blocks_of(tile + 2);
         if (tile + 1 < te) {
