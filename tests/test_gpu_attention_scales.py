@@ -3,33 +3,35 @@ no score does."""
 import pytest
 import torch
 
-from tests.fp8_util import Batch, attend, check_attention, dev
+from tests.attention_kernels import check, take
+from tests.fp8_util import Batch, attend, dev
 
 pytestmark = pytest.mark.gpu
-SHAPES = [(1, 200, 2, 1), (8, 40, 1, 1), (60, 70, 4, 2), (257, 300, 16, 1)]    # 16, 128 and 256 rows a workgroup
+Hq, Hk = 16, 1
+SHAPES = [(16, 1, 200), (128, 60, 70), (256, 60, 70), (128, 90, 600)]    # rows a workgroup, new tokens, tokens
 
 
-@pytest.mark.parametrize("n,L,Hq,Hk", SHAPES)
+@pytest.mark.parametrize("rows,n,L", SHAPES)
 @pytest.mark.parametrize("scale", [1e3, -1e30, 2.3e38])
-def test_queries_of_zeros_under_large_scales(n, L, Hq, Hk, scale):
+def test_queries_of_zeros_under_large_scales(rows, n, L, scale):
     """All scores are zero."""
-    B = Batch([(L, n)], Hq, Hk, 64, 16, 1)
+    B = take(Batch([(L, n)], Hq, Hk, 64, 16, 1), rows)
     B.E[:, :, 0] = 247
     B.k[(B.k & 127) > 0x77] = 0x77                       # 240 at most, as the append stores
     B.upload()
     q = dev(torch.zeros((B.M, Hq, 64), dtype=torch.bfloat16))
-    check_attention(B, q, attend(B, q, scale=scale), scale=0.0, label=(n, scale))
+    check(B, rows, q, attend(B, q, scale=scale), scale=0.0, label=(n, scale))
 
 
-@pytest.mark.parametrize("n,L,Hq,Hk", SHAPES)
+@pytest.mark.parametrize("rows,n,L", SHAPES)
 @pytest.mark.parametrize("E,size,scale", [(247, 2.0 ** -60, 2.0 ** -70), (240, 2.0 ** -120, 2.0 ** 8), (0, 2.0 ** 60, 2.0 ** 60),
                                           (20, 2.0 ** 97, 0.125)])
-def test_scores_of_ordinary_size_from_numbers_that_are_not(n, L, Hq, Hk, E, size, scale):
-    B = Batch([(L, n)], Hq, Hk, 64, 16, 2)
+def test_scores_of_ordinary_size_from_numbers_that_are_not(rows, n, L, E, size, scale):
+    B = take(Batch([(L, n)], Hq, Hk, 64, 16, 2), rows)
     B.E[:, :, 0] = E
     B.k[(B.k & 127) > 0x77] = 0x77
     if E == 0:
         B.k[(B.k & 127) < 0x20] = 0x20                   # 2^-3: its step and those above are 2^-6 or more, times 2^-127
     B.upload()
     q = dev(B.queries(size))
-    check_attention(B, q, attend(B, q, scale=scale), scale=scale, label=(n, E))
+    check(B, rows, q, attend(B, q, scale=scale), scale=scale, label=(n, E))
