@@ -35,3 +35,19 @@ def test_scores_of_ordinary_size_from_numbers_that_are_not(rows, n, L, E, size, 
     B.upload()
     q = dev(B.queries(size))
     check(B, rows, q, attend(B, q, scale=scale), scale=scale, label=(n, E))
+
+
+@pytest.mark.parametrize("rows,n,L", SHAPES)
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_scale_of_zero_and_a_query_that_is_no_number(rows, n, L, bad):
+    """0 times it is NaN: its row, and no other."""
+    B = take(Batch([(L, n)], Hq, Hk, 64, 16, 3), rows)
+    B.upload()
+    q = dev(B.queries())
+    clean = attend(B, q, scale=0.0)
+    check(B, rows, q, clean, scale=0.0, label=n)
+    q[n - 1, Hq - 1, 5] = bad
+    got = attend(B, q, scale=0.0)
+    assert torch.isnan(got[n - 1, Hq - 1]).all()
+    got[n - 1, Hq - 1] = clean[n - 1, Hq - 1]
+    assert torch.equal(got, clean)

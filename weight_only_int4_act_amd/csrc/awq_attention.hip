@@ -402,15 +402,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attention_tile(Args a, Sequences
     const int seen = g.reach(row, a), all = g.reach(base_row, a), wave_most = base_row < rows ? g.reach(base_row + 31, a) : 0;
     const int per = (g.tiles + used - 1) / used, tb = min(z * per, g.tiles), te = min(tb + per, g.tiles);
 
-    // scores are f times the products with f > 0: a negative scale's sign goes into q, a zero scale makes q zero
+    // scores are f times the products with f > 0: a negative scale's sign goes into q, and so does a zero scale (0 times an
+    // infinity or a NaN stays NaN)
     const float f = a.scale == 0.f ? 1.f : fabsf(a.scale);
-    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u, keep_q = a.scale == 0.f ? 0u : ~0u;
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
     bf16x8 q[D / 16];
 #pragma unroll
     for (int n = 0; n < D / 16; ++n) {
         u32x4 v = *(const u32x4*)(a.q + qat + 16 * n + 8 * h);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = (v[e] ^ flip) & keep_q;
+        for (int e = 0; e < 4; ++e) v[e] = a.scale == 0.f ? pack_bf16x2(bf16_lo(v[e]) * 0.f, bf16_hi(v[e]) * 0.f) : v[e] ^ flip;
         q[n] = __builtin_bit_cast(bf16x8, v);
     }
 
