@@ -405,7 +405,8 @@ int awq_mx_gemm(const uint8_t* xcodes, const uint8_t* xscales, int32_t bits, int
 size_t awq_fp8_codes_bytes(int64_t K, int64_t N);
 size_t awq_fp8_scales_count(int64_t K, int64_t N);
 
-/* Weights into groups of 128 x 128.  W bf16 [K, N], any N. */
+/* Weights into groups of 128 x 128.  W bf16 [K, N], any N.  (awq_fp8_gemm takes multiples of 8: what is packed of N columns is at
+ * the same time what would be packed of the next multiple with columns of zeros, and is handed to it as that.) */
 int awq_fp8_pack(const void* W_bf16, int64_t K, int64_t N, uint8_t* codes, float* scales, void* stream);
 
 /* Activations into groups of 128 channels: p = x, or with a gate p = x * g / (1 + e^-g), in float32 (1 / (1 + e^-g) below
@@ -454,6 +455,8 @@ int awq_fp8_gemm(const uint8_t* xcodes, const float* xscales, int64_t M, const u
  * each stores its own tokens, and which of the two leaves q and the output of such a row is not determined); a block
  * outside [0, blocks) or past the table's width: its tokens are neither stored nor seen; a token at a negative
  * position (length below the new tokens): not stored, its q and its output are zero; rows past max_q: left out.
+ * A slot below a sequence's length in which no token was stored (one left out, here or by the rotation's table) is seen with
+ * what it holds, which must be numbers under a scale byte up to 247, as in a cache that began with zeros.
  */
 
 /* q|k|v of new tokens: q and k normed per head and rotated, q out in bf16, k and v into the cache.

@@ -85,7 +85,7 @@ struct TileRows {
 // joined in LDS at the end, and those of several slices by k_attention_join_rows.
 // 64 sequences of up to 8192 tokens, 64 heads on 8, D = 128 (554 MB): 114-134 us by the boxes' memory (4.1-4.8 TB/s, a copy 4.75); one
 // of 4097 tokens 7.8 us and 2.9 for the join: lengths, blocks, codes, the join in LDS and the partials are trips to memory
-// one after the other, on 128 workgroups.
+// one after the other, on 96 workgroups.
 template <int D>
 __global__ __launch_bounds__(256) void k_attention_rows(Args a, Sequences s, Cache c) {
     constexpr int ND = D / 16, NH = D / 64;
@@ -329,8 +329,9 @@ __global__ __launch_bounds__(64) void k_attention_join_rows(Args a, Sequences s,
 // 256 rows by eight wavefronts and 128 tokens at a time halve what is widened and stored for each product: the faster
 // one where there are rows enough (the plan below).
 //
-// 4096 tokens behind 4096, 64 heads on 8, D = 128: 730-790 us (1.05-1.13 PFLOP/s; a large bf16 product reaches 1.38); 32 heads, D = 64:
-// 250 and 262 with 256 and 128 rows (.8).  Matrix cores busy in 48 % of the cycles, vector units in about as many: a product on
+// 4096 tokens behind 4096, 64 heads on 8, D = 128: 730-800 us (1.03-1.13 PFLOP/s; a large bf16 product reaches 1.38), 830 with
+// 128 rows.  D = 64 by 128 rows, and by 256: 32 heads on 8 298 and 294 us, 32 heads 277 and 265, 4 sequences of 2048 behind 2048 182
+// and 170, but one prompt of 2048 43 and 49 (the plan takes 128).  Matrix cores busy in 48 % of the cycles, vector units in about as many: a product on
 // one wavefront of a SIMD slows another's additions to two thirds (measured alone), so that exponentials, maxima,
 // roundings and widening are not hidden behind it but added.  On one card, 751 us without the products, 713 without
 // loads and widening, 530 without the softmax, in a form with the wavefronts' phases set against each other (itself
@@ -666,9 +667,12 @@ __global__ __launch_bounds__(2 * D) void k_attention_join(Args a, Sequences s, C
 // What this takes is in the mean 1.6 % slower than the best of all, where 32 rows and 1024 rows as bounds between the kernels
 // and slices for 512 workgroups took 10 %: 2 sequences of 85 tokens, 32 heads: 16 rows 9.2 us, 128 rows 15.8; 42 of 109 tokens,
 // 16 heads of q on one: 16, 128, 256 rows 36, 17, 20; 38 of 103 tokens behind 8400, 32 heads on 8: 633, 448, 393.
+// (The fit puts D = 64's 256 rows a few percent too high: long prompts lose up to 6 % by it, short ones would lose 14.)
 // Where there are 512 workgroups or more without slices there are none (64 sequences of up to 8192, 64 heads on 8: 1 slice
 // 118 us, 2 130), and never more than 1024 with them (up to 2048: the same in the mean).
-// `tokens`: what the table covers, the only bound of the lengths that the host has.
+// `tokens`: what the table covers, the only bound of the lengths that the host has.  One kernel and one number of slices
+// serve all sequences of a call: one of 65536 tokens among 63 of 1000 takes 422 us (alone 30), a prompt of 2048 beside 63
+// single tokens behind 8000 1354 (apart 97 and 189).
 AttentionPlan plan_attention(int64_t M, int n_seq, int max_q, int Hq, int Hk, int D, int64_t tokens) {
     struct Kernel {
         int rows, turn_tokens, held;
