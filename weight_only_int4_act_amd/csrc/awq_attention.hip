@@ -329,7 +329,7 @@ __global__ __launch_bounds__(64) void k_attention_join_rows(Args a, Sequences s,
 // 256 rows by eight wavefronts and 128 tokens at a time halve what is widened and stored for each product: the faster
 // one where there are rows enough (the plan below).
 //
-// 4096 tokens behind 4096, 64 heads on 8, D = 128: 730-800 us (1.03-1.13 PFLOP/s; a large bf16 product reaches 1.38), 830 with
+// 4096 tokens behind 4096, 64 heads on 8, D = 128: 730-810 us (1.02-1.13 PFLOP/s; a large bf16 product reaches 1.38), 830 with
 // 128 rows.  D = 64 by 128 rows, and by 256: 32 heads on 8 298 and 294 us, 32 heads 277 and 265, 4 sequences of 2048 behind 2048 182
 // and 170, but one prompt of 2048 43 and 49 (the plan takes 128).  Matrix cores busy in 48 % of the cycles, vector units in about as many: a product on
 // one wavefront of a SIMD slows another's additions to two thirds (measured alone), so that exponentials, maxima,
