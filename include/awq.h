@@ -487,8 +487,8 @@ int awq_qkv_append(const void* qkv_bf16, int64_t M, int32_t Hq, int32_t Hk, int3
  * less than 2^-133 (E < 3), which count as the nearest multiple of that.  p_t is one bf16 number in both sums, which puts
  * the result off by 2^-8 sum_t p_t |v_t - out| / sum_t p_t at most, or, where few rows make the kernel that streams the cache the
  * faster one, two in the first and float32 in the second.  A row's result does not depend on the numbers of other rows.
- * A score (scale log2 e q . k) within float32's range is right if the numbers of q are below 2^100 in magnitude; sums of
- * p_t v_t, p_t up to 2^8 times the largest, past that range are infinite.
+ * A score is right where q . k and scale log2 e q . k lie within float32's range and the numbers of q are below 2^100 in
+ * magnitude; sums of p_t v_t, p_t up to 2^8 times the largest, past that range are infinite.
  *   q, out  bf16 [M, Hq, D], M at most 2^31 / ((Hq + 2 Hk) D);  scale  finite, as is scale * log2 e (often 1/sqrt(D)).
  *   workspace >= awq_attention_workspace_size(M, n_seq, max_q, Hq, Hk, D) bytes (the size may be 0), 256-byte
  *   aligned; what it holds before a call does not matter, and its first 64 KiB are not touched: one workspace

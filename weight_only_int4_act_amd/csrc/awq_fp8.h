@@ -33,13 +33,14 @@ __device__ __forceinline__ Fp8Scale fp8_scale(uint32_t top) {
     f.s = f.bad ? __uint_as_float(0x7fc00000u) : f.d;
     return f;
 }
-// Eight elements: the float32 quotient p / s, then its rounding to e4m3.  q = p r is at most 1.5 of its steps away from the
-// quotient, and its remainder exact: R / S steps, S the 24-bit scale and R a whole number.  The correction R / S (1 + e), |e| <=
-// 2^-24, misses R / S by less than its distance from every border of float32, at least 1 / (2 S), so the result is the
-// rounded quotient.  A remainder below 2^-149 would be lost: small groups are taken 2^64 times as large (beside them, numbers
-// below 2^-10 scales, whose elements are zero either way).  No quotient rounds above 448.  p r alone gave other codes where
-// p / s lies midway between two of them, as quotients of bf16 numbers often do (4096 x 8192: 19.8 us, that way 19.4; packing
-// 4096 x 4096: 11.5 and 11.7).
+// Eight elements: e4m3 of the float32 quotient p / s.  With S / 2^23 = t the scale's 24-bit mantissa, r is off by 2^-25 t of
+// itself at most, so q = p r, of mantissa m, is less than m t / 4 + 1/2 of its steps away from the quotient: R / S steps, R a whole
+// number.  Only quotients next to a border of two codes matter, where m <= 31/16: |R / S| < 1.47, so that q - R / S rounds right
+// unless it lies by the border half a step from q.  There R is below 2^24, its remainder in float32 exact, and the correction
+// misses R / S by 2^-26 t, less than its distance from the border, which is 0 or at least 1 / (2 S) = 2^-24 / t.  A remainder below
+// 2^-149 would be lost: small groups are taken 2^64 times as large (beside them, numbers below 2^-10 scales, whose elements
+// are zero either way).  No quotient rounds above 448.  p r alone gave other codes where p / s lies midway between two of them, as
+// quotients of bf16 numbers often do (4096 x 8192: 19.8 us, that way 19.4; packing 4096 x 4096: 11.5 and 11.7).
 __device__ __forceinline__ uint2 fp8_codes8(const float (&p)[8], const Fp8Scale& f) {
     float x[8], d = f.d, r = f.r;
 #pragma unroll
